@@ -13,10 +13,15 @@ Steps (same names as the C ABI):
   idx_select_translate_planned: the same over a work list built once per step
   from the row lengths; idx_expand_translate_shared: the expansion of a
   selection reused across speculative draft steps)
+What consumes the chosen slots:
+  kv4_store / kv4_load (a 4-bit KV cache, written and read back) and
+  attn_slots / attn_window (attention over a selection's slots, and over a
+  sliding window plus the first tokens; 16-bit pools or the 4-bit cache)
 """
 from __future__ import annotations
 
 import ctypes as C
+import math
 import os
 from typing import Optional
 
@@ -30,6 +35,7 @@ DIM = 128
 PAGE_TOKENS = 64
 KMAX = 2048
 NOALLOC_SCRATCH_BYTES = 8 << 20  # BS_NOALLOC_SCRATCH_BYTES
+ATTN_WORKSPACE_BYTES = (32 << 20) + (64 << 10)  # BS_ATTN_WORKSPACE_BYTES
 
 _lib = None
 
@@ -79,6 +85,15 @@ def lib():
         L.idx_compress_store.argtypes = [P, i32, P, P, P, i32, i32, i32, i32, i32, i32, C.c_double, P, P, P, i32,
                                          P, i64, P]
         L.idx_compress_store.restype = C.c_int
+        L.kv4_store.argtypes = [P, P, i32, i64, i64, P, i32, i32, i32, P, P, i64, P]
+        L.kv4_store.restype = C.c_int
+        L.kv4_load.argtypes = [P, P, i64, P, i32, i32, i32, P, P, i32, i64, i64, P]
+        L.kv4_load.restype = C.c_int
+        attn_args = [P, i32, i64, i32, i32, i32, i32, P, P, i32, i64, i64]
+        L.attn_slots.argtypes = [*attn_args, P, i32, P, C.c_float, P, i64, P, P, C.c_size_t, P]
+        L.attn_slots.restype = C.c_int
+        L.attn_window.argtypes = [*attn_args, P, i32, P, i32, P, i32, i32, i32, C.c_float, P, i64, P, P, C.c_size_t, P]
+        L.attn_window.restype = C.c_int
         L.bs_status_string.argtypes = [C.c_int]
         L.bs_status_string.restype = C.c_char_p
         L.bs_abi_version.argtypes = []
@@ -372,6 +387,183 @@ def idx_compress_store(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary
     _check(lib().idx_compress_store(*args, _stream(stream, k_raw.device)), "idx_compress_store")
 
 
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # bs_dtype
+_U8 = (torch.uint8,)
+
+
+class KV4Cache:
+    """A 4-bit KV cache (layout: ``kv4_store`` in blockscore.h): ``codes``
+    uint8 [slots, kv_heads, 2, head_dim / 2] and ``scales`` uint8 [slots,
+    kv_heads, 2, head_dim / 32], contiguous, ``slots`` a multiple of 64."""
+
+    form = 1  # BS_KV_4
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
+        if codes.dim() != 4 or codes.shape[2] != 2 or codes.shape[0] % PAGE_TOKENS:
+            raise ValueError("codes must be [num_pages * 64, kv_heads, 2, head_dim / 2]")
+        self.codes, self.scales = codes, scales
+        self.kv_heads, self.head_dim = int(codes.shape[1]), 2 * int(codes.shape[3])
+        self.num_pages = int(codes.shape[0]) // PAGE_TOKENS
+        if scales.shape != (codes.shape[0], self.kv_heads, 2, self.head_dim // 32):
+            raise ValueError("scales must be [num_pages * 64, kv_heads, 2, head_dim / 32]")
+        self.device = codes.device
+
+    @classmethod
+    def empty(cls, num_pages: int, kv_heads: int, head_dim: int, device) -> "KV4Cache":
+        """Storage for ``num_pages`` pages (every slot reads back as zeros)."""
+        n = int(num_pages) * PAGE_TOKENS
+        return cls(torch.zeros((n, kv_heads, 2, head_dim // 2), dtype=torch.uint8, device=device),
+                   torch.full((n, kv_heads, 2, head_dim // 32), 127, dtype=torch.uint8, device=device))
+
+    def _args(self, dtype, dev):
+        return _ptr(self.codes, _U8, "codes", dev), _ptr(self.scales, _U8, "scales", dev), self.form, 0, self.num_pages
+
+
+class KV16Cache:
+    """K and V pools of the queries' 16-bit type: [slots, kv_heads, head_dim]
+    each, ``slots`` a multiple of 64, both with the same stride from a slot to
+    the next (views of one interleaved pool are fine)."""
+
+    form = 0  # BS_KV_16
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        if k.dim() != 3 or k.shape != v.shape or k.shape[0] % PAGE_TOKENS:
+            raise ValueError("k and v must both be [num_pages * 64, kv_heads, head_dim]")
+        if k.stride() != v.stride() or k.dtype != v.dtype:
+            raise ValueError("k and v must have the same strides and dtype")
+        self.k, self.v = k, v
+        self.kv_heads, self.head_dim = int(k.shape[1]), int(k.shape[2])
+        self.num_pages = int(k.shape[0]) // PAGE_TOKENS
+        self.device = k.device
+
+    def _args(self, dtype, dev):
+        return (_rows_ptr(self.k, (dtype,), "k pool", dev), _rows_ptr(self.v, (dtype,), "v pool", dev), self.form,
+                int(self.k.stride(0)), self.num_pages)
+
+
+def _rows_ptr(t: torch.Tensor, dtypes, name: str, device):
+    """Pointer of a [rows, heads, dim] tensor whose rows may lie apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name} must be [rows, heads, dim] with contiguous rows")
+    return C.c_void_p(t.data_ptr())
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Elements from a row to the next (a lone row's stride means nothing)."""
+    return int(t.stride(0)) if t.shape[0] > 1 else int(t.shape[1] * t.shape[2])
+
+
+def _kv4_store_args(k, v, slots, cache):
+    """Checked argument tuple of a ``kv4_store`` call (all but the stream)."""
+    dev = cache.device
+    if not isinstance(cache, KV4Cache):
+        raise TypeError("cache must be a KV4Cache")
+    if k.dim() != 3 or k.shape != v.shape or k.shape[1:] != (cache.kv_heads, cache.head_dim) or k.dtype != v.dtype:
+        raise ValueError("k and v must both be [num_tok, kv_heads, head_dim] of one dtype")
+    if slots.numel() != k.shape[0]:
+        raise ValueError("slots must hold num_tok entries")
+    return (_rows_ptr(k, tuple(_DTYPES), "k", dev), _rows_ptr(v, tuple(_DTYPES), "v", dev), _DTYPES[k.dtype], _ld(k),
+            _ld(v), _ptr(slots, _I32, "slots", dev), int(k.shape[0]), cache.kv_heads, cache.head_dim,
+            _ptr(cache.codes, _U8, "codes", dev), _ptr(cache.scales, _U8, "scales", dev), cache.num_pages)
+
+
+def kv4_store(k, v, slots, cache: KV4Cache, stream=None):
+    """Quantise new K/V rows into the 4-bit cache.  See ``kv4_store`` in blockscore.h."""
+    PreparedCall("kv4_store", _kv4_store_args(k, v, slots, cache), cache.device)(stream)
+
+
+def _kv4_load_args(cache, slots, k, v):
+    """Checked argument tuple of a ``kv4_load`` call (all but the stream)."""
+    dev = cache.device
+    if not isinstance(cache, KV4Cache):
+        raise TypeError("cache must be a KV4Cache")
+    if k.dim() != 3 or k.shape != v.shape or k.shape[1:] != (cache.kv_heads, cache.head_dim) or k.dtype != v.dtype:
+        raise ValueError("k and v must both be [num_slots, kv_heads, head_dim] of one dtype")
+    if slots.numel() != k.shape[0]:
+        raise ValueError("slots must hold one entry per row of k")
+    return (_ptr(cache.codes, _U8, "codes", dev), _ptr(cache.scales, _U8, "scales", dev), cache.num_pages,
+            _ptr(slots, _I32, "slots", dev), int(k.shape[0]), cache.kv_heads, cache.head_dim,
+            _rows_ptr(k, tuple(_DTYPES), "k", dev), _rows_ptr(v, tuple(_DTYPES), "v", dev), _DTYPES[k.dtype], _ld(k),
+            _ld(v))
+
+
+def kv4_load(cache: KV4Cache, slots, k, v, stream=None):
+    """Read rows of the 4-bit cache back.  See ``kv4_load`` in blockscore.h."""
+    PreparedCall("kv4_load", _kv4_load_args(cache, slots, k, v), cache.device)(stream)
+
+
+def attn_workspace(device) -> torch.Tensor:
+    """A zero-filled workspace that serves every ``attn_slots`` and
+    ``attn_window`` call on one stream."""
+    return torch.zeros(ATTN_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+
+
+def _attn_common(q, cache, out, scale, lse, workspace):
+    dev = q.device
+    if q.dim() != 3 or out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("q and out must both be [num_rows, q_heads, head_dim] of one dtype")
+    if q.shape[2] != cache.head_dim or q.shape[1] % cache.kv_heads:
+        raise ValueError("q does not fit the cache's heads")
+    if lse is not None and lse.shape != q.shape[:2]:
+        raise ValueError("lse must be [num_rows, q_heads]")
+    half = (torch.bfloat16, torch.float16)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    head = (_rows_ptr(q, half, "q", dev), _DTYPES[q.dtype], _ld(q), int(q.shape[0]), int(q.shape[1]), cache.kv_heads,
+            cache.head_dim, *cache._args(q.dtype, dev))
+    tail = (float(scale) if scale is not None else 1.0 / math.sqrt(cache.head_dim), _rows_ptr(out, half, "out", dev),
+            _ld(out), _ptr(lse, _F32, "lse", dev), _ptr(workspace, _U8, "workspace", dev), ws_bytes)
+    return head, tail
+
+
+def _attn_slots_args(q, cache, slots, out, count=None, scale=None, lse=None, workspace=None):
+    """Checked argument tuple of an ``attn_slots`` call (all but the stream)."""
+    dev = q.device
+    head, tail = _attn_common(q, cache, out, scale, lse, workspace)
+    if slots.dim() != 2 or slots.shape[0] != q.shape[0]:
+        raise ValueError("slots must be [num_rows, ld_slots]")
+    if count is not None and count.numel() != q.shape[0]:
+        raise ValueError("count must hold num_rows entries")
+    return (*head, _ptr(slots, _I32, "slots", dev), int(slots.shape[1]), _ptr(count, _I32, "count", dev), *tail)
+
+
+def attn_slots(q, cache, slots, out, count=None, scale=None, lse=None, workspace=None, stream=None):
+    """Attention of each row over its slots (``scale`` defaults to
+    1/sqrt(head_dim)).  See ``attn_slots`` in blockscore.h."""
+    PreparedCall("attn_slots", _attn_slots_args(q, cache, slots, out, count, scale, lse, workspace), q.device)(stream)
+
+
+def _attn_window_args(q, cache, page_table, req_row_ptr, row_pos, max_rows, window, sinks, out, scale=None, lse=None,
+                      workspace=None):
+    """Checked argument tuple of an ``attn_window`` call (all but the stream)."""
+    dev = q.device
+    head, tail = _attn_common(q, cache, out, scale, lse, workspace)
+    B = int(req_row_ptr.shape[0]) - 1
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be [num_req, pt_stride]")
+    if row_pos.numel() != q.shape[0]:
+        raise ValueError("row_pos must hold num_rows entries")
+    return (*head, _ptr(page_table, _I32, "page_table", dev), int(page_table.shape[1]),
+            _ptr(req_row_ptr, _I32, "req_row_ptr", dev), B, _ptr(row_pos, _I32, "row_pos", dev), int(max_rows),
+            int(window), int(sinks), *tail)
+
+
+def attn_window(q, cache, page_table, req_row_ptr, row_pos, max_rows, window, sinks, out, scale=None, lse=None,
+                workspace=None, stream=None):
+    """Attention over a sliding window and the first ``sinks`` tokens
+    (``scale`` defaults to 1/sqrt(head_dim)).  See ``attn_window`` in
+    blockscore.h."""
+    PreparedCall("attn_window", _attn_window_args(q, cache, page_table, req_row_ptr, row_pos, max_rows, window, sinks,
+                                                  out, scale, lse, workspace), q.device)(stream)
+
+
 class PreparedCall:
     """One C call with its arguments checked and marshalled once (the tensors
     behind the pointers must outlive it); ``__call__`` adds the stream and
@@ -384,13 +576,19 @@ class PreparedCall:
         self._f = getattr(lib(), fn)
 
     def __call__(self, stream=None):
-        st = self._f(*self.args, _stream(stream, self.device))
+        # A launch goes to the current device; tensors may live on another.
+        if self.device.index is not None and self.device.index != torch.cuda.current_device():
+            with torch.cuda.device(self.device):
+                st = self._f(*self.args, _stream(stream, self.device))
+        else:
+            st = self._f(*self.args, _stream(stream, self.device))
         if st != 0:
             _check(st, self.fn)
 
     def bind(self, stream=None) -> "BoundCall":
         """The same call with the stream resolved now (default: the current
-        stream): each call is then one C call with nothing looked up."""
+        stream): each call is then one C call with nothing looked up (the
+        tensors' device must be the current one)."""
         return BoundCall(self, _stream(stream, self.device))
 
 
@@ -466,7 +664,9 @@ __all__ = [
     "lib", "PreparedCall", "BoundCall", "prepare_score", "prepare_topk", "prepare_select_translate", "prepare_expand_shared",
     "prepare_compress_store", "topk_plan_bytes", "topk_planned_workspace_bytes", "topk_plan",
     "topk_planned_workspace", "topk_plan_rows", "idx_select_translate_planned", "prepare_plan",
-    "prepare_select_translate_planned",
+    "prepare_select_translate_planned", "KV4Cache", "KV16Cache", "kv4_store", "kv4_load", "attn_workspace",
+    "ATTN_WORKSPACE_BYTES", "attn_slots", "attn_window", "prepare_kv4_store", "prepare_kv4_load",
+    "prepare_attn_slots", "prepare_attn_window",
 ]
 
 
@@ -476,3 +676,25 @@ def prepare_compress_store(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, ro
     return PreparedCall("idx_compress_store",
                         _compress_args(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary_dim, sections,
                                        theta, ring, ring_pos, page_table, kcache, num_pages), k_raw.device)
+
+
+def prepare_kv4_store(k, v, slots, cache: KV4Cache) -> PreparedCall:
+    """``kv4_store`` with fixed arguments."""
+    return PreparedCall("kv4_store", _kv4_store_args(k, v, slots, cache), cache.device)
+
+
+def prepare_kv4_load(cache: KV4Cache, slots, k, v) -> PreparedCall:
+    """``kv4_load`` with fixed arguments."""
+    return PreparedCall("kv4_load", _kv4_load_args(cache, slots, k, v), cache.device)
+
+
+def prepare_attn_slots(q, cache, slots, out, count=None, scale=None, lse=None, workspace=None) -> PreparedCall:
+    """``attn_slots`` with fixed arguments."""
+    return PreparedCall("attn_slots", _attn_slots_args(q, cache, slots, out, count, scale, lse, workspace), q.device)
+
+
+def prepare_attn_window(q, cache, page_table, req_row_ptr, row_pos, max_rows, window, sinks, out, scale=None, lse=None,
+                        workspace=None) -> PreparedCall:
+    """``attn_window`` with fixed arguments."""
+    return PreparedCall("attn_window", _attn_window_args(q, cache, page_table, req_row_ptr, row_pos, max_rows, window,
+                                                         sinks, out, scale, lse, workspace), q.device)

@@ -237,6 +237,106 @@ BS_EXPORT int idx_compress_store(const uint16_t* k_raw, int32_t num_tok, const i
                              static_cast<hipStream_t>(stream));
 }
 
+namespace {
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+inline bool head_dim_ok(int32_t d) { return d == 64 || d == 128 || d == 256; }
+inline bool row_stride_ok(int64_t ld, int64_t width) { return ld >= width && (ld & 7) == 0; }
+// Slots are int32: a pool past 2^31 slots admits every non-negative one.
+inline int32_t slots_of_pages(int64_t num_pages) {
+  return num_pages > (0x7FFFFFFF / BS_PAGE_TOKENS) ? 0x7FFFFFFF : (int32_t)(num_pages * BS_PAGE_TOKENS);
+}
+
+inline int check_kv4_args(const void* k, const void* v, int32_t dtype, int64_t ld_k, int64_t ld_v,
+                          const int32_t* slots, int32_t rows, int32_t kv_heads, int32_t head_dim,
+                          const uint8_t* codes, const uint8_t* scales, int64_t num_pages) {
+  if (rows < 0 || num_pages < 0 || kv_heads < 1 || !head_dim_ok(head_dim)) return BS_ERR_ARG;
+  if (dtype != BS_BF16 && dtype != BS_F16 && dtype != BS_F32) return BS_ERR_ARG;
+  const int64_t width = (int64_t)kv_heads * head_dim;
+  if (width > (1 << 20) || !row_stride_ok(ld_k, width) || !row_stride_ok(ld_v, width)) return BS_ERR_ARG;
+  if (rows == 0) return BS_OK;
+  if (!k || !v || !slots || !codes || !scales) return BS_ERR_NULL;
+  if (num_pages < 1 || !aligned16(k) || !aligned16(v) || !aligned16(codes) || !aligned16(scales)) return BS_ERR_ARG;
+  return BS_OK;
+}
+
+inline int check_attn_args(const void* q, int32_t dtype, int64_t ld_q, int32_t num_rows, int32_t q_heads,
+                           int32_t kv_heads, int32_t head_dim, const void* cache0, const void* cache1,
+                           int32_t cache_form, int64_t ld_cache, int64_t num_pages, float scale, const void* out,
+                           int64_t ld_out, const void* workspace, size_t workspace_bytes) {
+  if (num_rows < 0 || num_pages < 0 || kv_heads < 1 || q_heads < 1 || !head_dim_ok(head_dim)) return BS_ERR_ARG;
+  if (dtype != BS_BF16 && dtype != BS_F16) return BS_ERR_ARG;
+  if (cache_form != BS_KV_16 && cache_form != BS_KV_4) return BS_ERR_ARG;
+  if (q_heads % kv_heads != 0 || !std::isfinite(scale)) return BS_ERR_ARG;
+  const int64_t qw = (int64_t)q_heads * head_dim, kvw = (int64_t)kv_heads * head_dim;
+  if (qw > (1 << 20) || !row_stride_ok(ld_q, qw) || !row_stride_ok(ld_out, qw)) return BS_ERR_ARG;
+  if (cache_form == BS_KV_16 && !row_stride_ok(ld_cache, kvw)) return BS_ERR_ARG;
+  if (num_rows == 0) return BS_OK;
+  if (!q || !cache0 || !cache1 || !out) return BS_ERR_NULL;
+  if (num_pages < 1) return BS_ERR_ARG;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(cache0) || !aligned16(cache1) || !aligned16(workspace))
+    return BS_ERR_ARG;
+  if (workspace != nullptr && workspace_bytes < BS_ATTN_WORKSPACE_BYTES) return BS_ERR_WORKSPACE;
+  return BS_OK;
+}
+
+}  // namespace
+
+BS_EXPORT int kv4_store(const void* k, const void* v, int32_t dtype, int64_t ld_k, int64_t ld_v, const int32_t* slots,
+                        int32_t num_tok, int32_t kv_heads, int32_t head_dim, uint8_t* codes, uint8_t* scales,
+                        int64_t num_pages, void* stream) {
+  const int st =
+      check_kv4_args(k, v, dtype, ld_k, ld_v, slots, num_tok, kv_heads, head_dim, codes, scales, num_pages);
+  if (st != BS_OK || num_tok == 0) return st;
+  return bs::launch_kv4_store(k, v, dtype, ld_k, ld_v, slots, num_tok, kv_heads, head_dim, codes, scales,
+                              slots_of_pages(num_pages), static_cast<hipStream_t>(stream));
+}
+
+BS_EXPORT int kv4_load(const uint8_t* codes, const uint8_t* scales, int64_t num_pages, const int32_t* slots,
+                       int32_t num_slots, int32_t kv_heads, int32_t head_dim, void* k, void* v, int32_t dtype,
+                       int64_t ld_k, int64_t ld_v, void* stream) {
+  const int st =
+      check_kv4_args(k, v, dtype, ld_k, ld_v, slots, num_slots, kv_heads, head_dim, codes, scales, num_pages);
+  if (st != BS_OK || num_slots == 0) return st;
+  return bs::launch_kv4_load(codes, scales, slots_of_pages(num_pages), slots, num_slots, kv_heads, head_dim, k, v,
+                             dtype, ld_k, ld_v, static_cast<hipStream_t>(stream));
+}
+
+BS_EXPORT int attn_slots(const void* q, int32_t dtype, int64_t ld_q, int32_t num_rows, int32_t q_heads,
+                         int32_t kv_heads, int32_t head_dim, const void* cache0, const void* cache1,
+                         int32_t cache_form, int64_t ld_cache, int64_t num_pages, const int32_t* slots,
+                         int32_t ld_slots, const int32_t* count, float scale, void* out, int64_t ld_out, float* lse,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  const int st = check_attn_args(q, dtype, ld_q, num_rows, q_heads, kv_heads, head_dim, cache0, cache1, cache_form,
+                                 ld_cache, num_pages, scale, out, ld_out, workspace, workspace_bytes);
+  if (st != BS_OK) return st;
+  if (ld_slots < 0) return BS_ERR_ARG;
+  if (num_rows == 0) return BS_OK;
+  if (!slots) return BS_ERR_NULL;
+  const bs::AttnCall c = {q,      dtype,      ld_q,     num_rows,   q_heads, kv_heads, head_dim, cache0, cache1,
+                          cache_form, ld_cache, slots_of_pages(num_pages), scale, out, ld_out, lse, workspace};
+  return bs::launch_attn_slots(c, slots, ld_slots, count, static_cast<hipStream_t>(stream));
+}
+
+BS_EXPORT int attn_window(const void* q, int32_t dtype, int64_t ld_q, int32_t num_rows, int32_t q_heads,
+                          int32_t kv_heads, int32_t head_dim, const void* cache0, const void* cache1,
+                          int32_t cache_form, int64_t ld_cache, int64_t num_pages, const int32_t* page_table,
+                          int32_t pt_stride, const int32_t* req_row_ptr, int32_t num_req, const int32_t* row_pos,
+                          int32_t max_rows, int32_t window, int32_t sinks, float scale, void* out, int64_t ld_out,
+                          float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  const int st = check_attn_args(q, dtype, ld_q, num_rows, q_heads, kv_heads, head_dim, cache0, cache1, cache_form,
+                                 ld_cache, num_pages, scale, out, ld_out, workspace, workspace_bytes);
+  if (st != BS_OK) return st;
+  if (num_req < 0 || max_rows < 0 || window < 0 || sinks < 0) return BS_ERR_ARG;
+  if (num_rows == 0 || num_req == 0 || max_rows == 0) return BS_OK;
+  if (!page_table || !req_row_ptr || !row_pos) return BS_ERR_NULL;
+  if (pt_stride < 1) return BS_ERR_ARG;
+  const bs::AttnCall c = {q,      dtype,      ld_q,     num_rows,   q_heads, kv_heads, head_dim, cache0, cache1,
+                          cache_form, ld_cache, slots_of_pages(num_pages), scale, out, ld_out, lse, workspace};
+  return bs::launch_attn_window(c, page_table, pt_stride, req_row_ptr, num_req, row_pos, max_rows, window, sinks,
+                                static_cast<hipStream_t>(stream));
+}
+
 BS_EXPORT const char* bs_status_string(int status) {
   switch (status) {
     case BS_OK: return "BS_OK";

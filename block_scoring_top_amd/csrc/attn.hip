@@ -1,0 +1,84 @@
+// attn.hip - host side of the attention calls: which kernel, its tiles, and
+// over how many workgroups a row's keys are split.
+#include <algorithm>
+
+#include "attn_gather.h"
+
+namespace bs {
+
+extern template int launch_attn_gather<Bf16, true>(const GatherArgs&, int, int, bool, uint32_t, hipStream_t);
+extern template int launch_attn_gather<Bf16, false>(const GatherArgs&, int, int, bool, uint32_t, hipStream_t);
+extern template int launch_attn_gather<F16, true>(const GatherArgs&, int, int, bool, uint32_t, hipStream_t);
+extern template int launch_attn_gather<F16, false>(const GatherArgs&, int, int, bool, uint32_t, hipStream_t);
+
+namespace {
+
+constexpr int64_t kCounterBytes = 64 << 10;  // first part of the workspace: arrival counters
+constexpr int64_t kPartialBytes = (int64_t)BS_ATTN_WORKSPACE_BYTES - kCounterBytes;
+constexpr int64_t kFillBlocks = 1024;        // workgroups worth splitting for: 4 on each of 256 compute units
+
+GatherArgs common_args(const AttnCall& c) {
+  GatherArgs a = {};
+  a.q = c.q, a.ld_q = c.ld_q;
+  a.a = static_cast<const uint8_t*>(c.cache0), a.b = static_cast<const uint8_t*>(c.cache1);
+  a.ld_kv = c.ld_cache;
+  a.num_slots = c.num_slots, a.num_rows = c.num_rows, a.hq = c.hq, a.hkv = c.hkv;
+  a.scale_log2 = c.scale * kLog2e;
+  a.out = c.out, a.ld_out = c.ld_out, a.lse = c.lse;
+  a.nsplit = 1;
+  return a;
+}
+
+// Heads of one kv head's group in blocks of at most 16*nt, as even as possible.
+void split_heads(GatherArgs& a, int nt) {
+  const int g = a.hq / a.hkv;
+  a.hblocks = (g + 16 * nt - 1) / (16 * nt);
+  a.gb = (g + a.hblocks - 1) / a.hblocks;
+}
+
+int run_gather(GatherArgs& a, const AttnCall& c, int nt, bool window, int64_t tiles, int64_t max_keys,
+               hipStream_t stream) {
+  const int64_t groups = tiles * a.hkv * a.hblocks;
+  if (c.workspace != nullptr && groups < kFillBlocks) {
+    const int64_t per = (int64_t)16 * nt * (c.d + 2) * 4;
+    int64_t n = std::min((kFillBlocks + groups - 1) / groups, (max_keys + kGaWaves * kGaKeys - 1) / (kGaWaves * kGaKeys));
+    n = std::min(n, kPartialBytes / per / groups);
+    a.nsplit = (int)std::max<int64_t>(n, 1);
+    a.counters = static_cast<uint32_t*>(c.workspace);
+    a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(c.workspace) + kCounterBytes);
+  }
+  if (groups * a.nsplit > (int64_t)1 << 23) return BS_ERR_ARG;  // 2^31 lanes
+  const uint32_t blocks = (uint32_t)(groups * a.nsplit);
+  if (c.dtype == BS_BF16)
+    return c.form == BS_KV_4 ? launch_attn_gather<Bf16, true>(a, c.d, nt, window, blocks, stream)
+                             : launch_attn_gather<Bf16, false>(a, c.d, nt, window, blocks, stream);
+  return c.form == BS_KV_4 ? launch_attn_gather<F16, true>(a, c.d, nt, window, blocks, stream)
+                           : launch_attn_gather<F16, false>(a, c.d, nt, window, blocks, stream);
+}
+
+}  // namespace
+
+int launch_attn_slots(const AttnCall& c, const int32_t* slots, int32_t ld_slots, const int32_t* count,
+                      hipStream_t stream) {
+  GatherArgs a = common_args(c);
+  const int nt = c.hq / c.hkv <= 16 ? 1 : 2;
+  split_heads(a, nt);
+  a.slots = slots, a.ld_slots = ld_slots, a.count = count;
+  return run_gather(a, c, nt, false, c.num_rows, ld_slots, stream);
+}
+
+int launch_attn_window(const AttnCall& c, const int32_t* page_table, int32_t pt_stride, const int32_t* req_row_ptr,
+                       int32_t num_req, const int32_t* row_pos, int32_t max_rows, int32_t window, int32_t sinks,
+                       hipStream_t stream) {
+  GatherArgs a = common_args(c);
+  const int g = c.hq / c.hkv, nt = (int64_t)g * max_rows <= 16 ? 1 : 2;
+  split_heads(a, nt);
+  a.page_table = page_table, a.pt_stride = pt_stride, a.req_row_ptr = req_row_ptr, a.row_pos = row_pos;
+  a.max_rows = max_rows, a.window = window, a.sinks = sinks;
+  a.rows_per_tile = std::max(1, 16 * nt / a.gb);
+  a.tiles_per_req = (int)(((int64_t)max_rows + a.rows_per_tile - 1) / a.rows_per_tile);
+  const int64_t keys = std::min<int64_t>((int64_t)pt_stride * kPage, (int64_t)window + sinks + a.rows_per_tile - 1);
+  return run_gather(a, c, nt, true, (int64_t)num_req * a.tiles_per_req, keys, stream);
+}
+
+}  // namespace bs

@@ -1,0 +1,571 @@
+// attn_gather.h - attention over gathered KV slots, for few query rows a key:
+// the rows of a selection (attn_slots), and decode or verify rows of a
+// sliding window (attn_window).
+//
+// Per query row r and head h (kv head h / G): x_i = scale * <q, K_i> over the
+// row's keys, o = sum_i softmax(x)_i V_i, lse = log sum_i exp(x_i).  One pass
+// over the keys with a running maximum and sum in FP32.
+//
+// What bounds it is the gather: a key is read once for the G (times rows)
+// query vectors that share it, 4*G*D flops for 17/16*D bytes (4-bit) or 4*D
+// bytes (16-bit).  So the kernel keeps loads in flight and the rest small:
+//   * a wave works alone on 32-key chunks, the next chunk's K and V in flight
+//     while it computes; no LDS tile, no workgroup barrier in the loop;
+//   * S^T = K q^T with v_mfma_f32_16x16x32: the A operand's lane is a key, so
+//     a lane loads a quarter of one key's row contiguously (16 bytes of codes
+//     hold one group of 32 channels at D = 128: one scale a lane).  The order
+//     of channels inside the product is free as long as q has the same;
+//   * O^T += V^T P^T: in S^T's accumulator a lane already holds the P of one
+//     query vector and of keys 4*(lane/16)+0..3 of each 16-key tile, which is
+//     the B operand of a 32-key product whose key order is chosen to match.
+//     The A operand needs 8 keys of one channel: a lane loads D/16 channels
+//     of 8 keys, converts, and transposes pairs of keys with byte permutes;
+//   * one maximum and rescaling per chunk; the rescaling is skipped when no
+//     maximum of the wave grew;
+//   * P is rounded to the 16-bit operand type for the product (relative
+//     2^-9 in bf16, as the output's own rounding); its sum is of the FP32
+//     values.
+// The 4 waves of a workgroup interleave chunks and join through LDS.  With
+// few rows the keys are split over workgroups too: partial results go to the
+// workspace and the last workgroup of a group to arrive joins them in split
+// order (so the result does not depend on the arrival order).
+#pragma once
+
+#include "attn.h"
+
+namespace bs {
+
+constexpr int kGaWaves = 4;
+constexpr int kGaKeys = 32;  // keys per wave and step
+
+struct GatherArgs {
+  const void* q;
+  int64_t ld_q;
+  const uint8_t *a, *b;  // 4-bit: codes, scales; 16-bit: K and V pools
+  int64_t ld_kv;         // 16-bit pools: elements from one slot to the next
+  int32_t num_slots, num_rows, hq, hkv;
+  int32_t gb, hblocks;   // heads per block and blocks of one kv head's query heads
+  // a selection's slot lists
+  const int32_t* slots;
+  int32_t ld_slots;
+  const int32_t* count;
+  // a window
+  const int32_t *page_table, *req_row_ptr, *row_pos;
+  int32_t pt_stride, max_rows, rows_per_tile, tiles_per_req, window, sinks;
+  float scale_log2;
+  void* out;
+  int64_t ld_out;
+  float* lse;
+  uint32_t* counters;  // one per group of splits, zero between calls
+  float* partial;
+  int32_t nsplit;
+};
+
+template <bool FP4, int D>
+struct GatherRaw {
+  static constexpr int kKDwords = FP4 ? D / 32 : D / 8;                 // a quarter of a key's row
+  static constexpr int kVDwords = FP4 ? (D < 128 ? 1 : D / 128) : D / 32;  // D/16 channels of a key
+  uint32_t k[2][kKDwords];
+  uint32_t v[8][kVDwords];
+  uint32_t s[FP4 ? D / 64 : 1];  // lanes 0..31: the scale bytes of one key
+};
+
+template <int N>
+__device__ __forceinline__ void load_dwords(uint32_t (&dst)[N], const uint8_t* p) {
+  if constexpr (N == 1) {
+    dst[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (N == 2) {
+    const u32x2_t x = *reinterpret_cast<const u32x2_t*>(p);
+    dst[0] = x.x, dst[1] = x.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const u32x4_t x = *reinterpret_cast<const u32x4_t*>(p + 4 * i);
+      dst[i] = x.x, dst[i + 1] = x.y, dst[i + 2] = x.z, dst[i + 3] = x.w;
+    }
+  }
+}
+
+// A workspace region that splits exchange results through: relaxed
+// device-scope accesses only (performed at the device's coherence point, not
+// in an XCD's L2), so no cache write-back is needed.
+struct SplitBuffer {
+  __amdgpu_buffer_rsrc_t rs;
+  __device__ __forceinline__ SplitBuffer(float* p, uint32_t bytes)
+      : rs(__builtin_amdgcn_make_buffer_rsrc(p, (short)0, bytes, 0x00020000)) {}
+  static constexpr int kSc1 = 16;
+  __device__ __forceinline__ void store4(uint32_t off, const f32x4_t& v) const {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), rs, off, 0, kSc1);
+  }
+  __device__ __forceinline__ void store2(uint32_t off, float x, float y) const {
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{__float_as_uint(x), __float_as_uint(y)}, rs, off, 0, kSc1);
+  }
+  __device__ __forceinline__ f32x4_t load4(uint32_t off) const {
+    return __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, kSc1));
+  }
+  __device__ __forceinline__ float2 load2(uint32_t off) const {
+    const u32x2_t v = __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, kSc1);
+    return make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+  }
+};
+
+template <class T, bool FP4, int D, int NT, bool WINDOW>
+__global__ __launch_bounds__(64 * kGaWaves, NT * D > 256 ? 1 : 2) void attn_gather_kernel(const GatherArgs a) {
+  typedef GatherRaw<FP4, D> Raw;
+  constexpr int KS = D / 32;       // 32-channel steps of the score product
+  constexpr int VD = D / 16;       // channels of the output per lane and accumulator row
+  constexpr int COLS = 16 * NT;    // (row, head) pairs of a tile
+  constexpr int OLD = D + 4;       // LDS row of the join, in floats
+  __shared__ union {
+    struct {
+      __attribute__((aligned(16))) int32_t slot[kGaWaves][kGaKeys];
+      __attribute__((aligned(16))) uint8_t scale[kGaWaves][kGaKeys][D / 16];
+    } st;
+    struct {
+      __attribute__((aligned(16))) float o[kGaWaves][16][OLD];
+      float m[kGaWaves][16], l[kGaWaves][16];
+    } jn;
+  } sh;
+  __shared__ uint32_t arrived;
+
+  const int tid = threadIdx.x, lane = tid & 63, n16 = lane & 15, qd = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int split = blockIdx.x % a.nsplit, group = blockIdx.x / a.nsplit;
+  const int hb = group % (a.hkv * a.hblocks), tile = group / (a.hkv * a.hblocks);
+  const int kvh = hb / a.hblocks, G = a.hq / a.hkv, hin = (hb % a.hblocks) * a.gb;
+  const int heads = min(a.gb, G - hin), h0 = kvh * G + hin;
+
+  // The tile's rows, and its key list: n keys.
+  int row0, nrows, n;
+  // Window: positions of the rows that have one, first keys, where the window
+  // starts, and the last position that every row of the tile sees.
+  int tmin = 0, tmax = 0, ns = 0, start = 0, seen_by_all = 0;
+  const int32_t* ptab = nullptr;
+  if constexpr (WINDOW) {
+    const int b = tile / a.tiles_per_req, i = tile % a.tiles_per_req;
+    const int ra = max(a.req_row_ptr[b], 0);
+    const int rb = (int)min((int64_t)min(a.req_row_ptr[b + 1], a.num_rows), (int64_t)ra + a.max_rows);
+    const int64_t first = (int64_t)ra + (int64_t)i * a.rows_per_tile;
+    if (first >= rb) return;
+    row0 = (int)first;
+    nrows = min(a.rows_per_tile, rb - row0);
+    ptab = a.page_table + (int64_t)b * a.pt_stride;
+    const int t = a.row_pos[row0 + min(lane, nrows - 1)];
+    int lo = t < 0 ? 0x7FFFFFFF : t, hi = t;
+    for (int o = 32; o > 0; o >>= 1) lo = min(lo, __shfl_xor(lo, o)), hi = max(hi, __shfl_xor(hi, o));
+    tmin = __builtin_amdgcn_readfirstlane(lo), tmax = __builtin_amdgcn_readfirstlane(hi);
+    seen_by_all = ballot(t < 0) ? -1 : tmin;  // a row without a position sees nothing
+    // last addressable position (and its chunk's keys stay below 2^31)
+    const int last = (int)min((int64_t)min(tmax, 0x7FFFFF00), (int64_t)a.pt_stride * kPage - 1);
+    ns = max(0, min(a.sinks, last + 1));
+    start = max(max(0, tmin - a.window + 1), ns);
+    n = last < 0 ? 0 : ns + max(0, last + 1 - start);
+  } else {
+    row0 = tile, nrows = 1;
+    n = a.ld_slots;
+    if (a.count != nullptr) n = min(n, a.count[row0]);
+    n = max(n, 0);
+  }
+  const int chunks = (int)(((int64_t)n + kGaKeys - 1) / kGaKeys);
+  const int c0 = (int)((int64_t)chunks * split / a.nsplit), c1 = (int)((int64_t)chunks * (split + 1) / a.nsplit);
+
+  // This lane's query vectors (column 16*nt + n16 of the tile).
+  u32x4_t qf[NT][KS];
+  int tcol[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int col = nt * 16 + n16, rr = col / a.gb, hh = col % a.gb;
+    const bool ok = rr < nrows && hh < heads;
+    const typename T::elem* src =
+        static_cast<const typename T::elem*>(a.q) + (int64_t)(row0 + (ok ? rr : 0)) * a.ld_q + (h0 + (ok ? hh : 0)) * D + qd * (D / 4);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const u32x4_t x = *reinterpret_cast<const u32x4_t*>(src + 8 * ks);
+      qf[nt][ks] = ok ? x : u32x4_t{0, 0, 0, 0};
+    }
+    tcol[nt] = WINDOW && ok ? a.row_pos[row0 + rr] : -1;
+  }
+
+  f32x4_t acc[NT][VD];
+  float m[NT], l[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    m[nt] = -INFINITY, l[nt] = 0.f;
+#pragma unroll
+    for (int d = 0; d < VD; ++d) acc[nt][d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  }
+
+  auto key_pos = [&](int i) { return i < ns ? i : start + (i - ns); };
+  // The slot of this lane's key (lane mod 32) of chunk c; -1: none.
+  auto load_slot = [&](int c) -> int {
+    const int i = c * kGaKeys + (lane & 31);
+    if (c >= c1 || i >= n) return -1;
+    if constexpr (WINDOW) {
+      const int p = key_pos(i);
+      const int page = ptab[p >> 6];
+      return page < 0 || page > (0x7FFFFFFF >> 6) ? -1 : page * kPage + (p & (kPage - 1));
+    } else {
+      return a.slots[(int64_t)row0 * a.ld_slots + i];
+    }
+  };
+  // Issues the loads of a chunk; mask: its keys whose slot is one.
+  auto fetch = [&](int sl, Raw& r, uint32_t& mask) {
+    const bool ok = sl >= 0 && sl < a.num_slots;
+    mask = (uint32_t)ballot(ok);
+    sl = ok ? sl : 0;
+    wave_fence();
+    if (lane < kGaKeys) sh.st.slot[wave][lane] = sl;
+    wave_fence();
+    const int32_t* ls = sh.st.slot[wave];
+    const int32_t ka = ls[n16], kb = ls[16 + n16];
+    const int4 va = reinterpret_cast<const int4*>(ls)[qd], vb = reinterpret_cast<const int4*>(ls)[4 + qd];
+    const int32_t vs[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
+    if constexpr (FP4) {
+      const uint32_t rec = (uint32_t)a.hkv * D;
+      const uint8_t* base = a.a + kvh * D;
+      load_dwords(r.k[0], base + (uint64_t)(uint32_t)ka * rec + qd * (D / 8));
+      load_dwords(r.k[1], base + (uint64_t)(uint32_t)kb * rec + qd * (D / 8));
+      if (lane < kGaKeys)
+        load_dwords(r.s, a.b + (uint64_t)(uint32_t)sl * ((uint32_t)a.hkv * (D / 16)) + kvh * (D / 16));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint8_t* p = base + (uint64_t)(uint32_t)vs[j] * rec + D / 2 + n16 * (D / 32);
+        if constexpr (D == 64)
+          r.v[j][0] = *reinterpret_cast<const uint16_t*>(p);
+        else
+          load_dwords(r.v[j], p);
+      }
+    } else {
+      const int64_t rec = a.ld_kv * 2;
+      const uint8_t* kb0 = a.a + kvh * D * 2;
+      const uint8_t* vb0 = a.b + kvh * D * 2 + n16 * (D / 8);
+      load_dwords(r.k[0], kb0 + ka * rec + qd * (D / 2));
+      load_dwords(r.k[1], kb0 + kb * rec + qd * (D / 2));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) load_dwords(r.v[j], vb0 + vs[j] * rec);
+    }
+  };
+
+  auto compute = [&](Raw& r, uint32_t mask, int c) {
+    float vscale[8];
+    float kscale[2][FP4 && D == 256 ? 2 : 1];
+    bool full = mask == 0xFFFFFFFFu;
+    if constexpr (FP4) {
+      wave_fence();
+      if (lane < kGaKeys) {
+        uint32_t* dst = reinterpret_cast<uint32_t*>(sh.st.scale[wave][lane]);
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) dst[i] = r.s[i];
+      }
+      wave_fence();
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint8_t* p = sh.st.scale[wave][16 * j + n16];
+        if constexpr (D == 256) {
+          kscale[j][0] = kv4_scale(p[2 * qd]), kscale[j][1] = kv4_scale(p[2 * qd + 1]);
+        } else {
+          kscale[j][0] = kv4_scale(p[qd * D / 128]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        vscale[j] = kv4_scale(sh.st.scale[wave][(j >> 2) * 16 + 4 * qd + (j & 3)][D / 32 + n16 * D / 512]);
+    }
+    // Keys without a slot: their K is read from slot 0 and masked below,
+    // their V must be zeros (0 * NaN is not 0).
+    const uint32_t own = (mask >> (4 * qd)) & 0xFu, own2 = (mask >> (16 + 4 * qd)) & 0xFu;
+    const uint32_t have = own | (own2 << 4);  // bit j: key of v[j]
+    if (!full) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool ok = (have >> j) & 1u;
+#pragma unroll
+        for (int i = 0; i < Raw::kVDwords; ++i) r.v[j][i] = ok ? r.v[j][i] : 0u;
+        if constexpr (FP4) vscale[j] = ok ? vscale[j] : 1.f;
+      }
+    }
+
+    f32x4_t s[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    static_for<KS>([&](auto ksc) {
+      constexpr int ks = decltype(ksc)::value;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        u32x4_t kf;
+        if constexpr (FP4) {
+          const float sc = kscale[j][D == 256 ? ks / 4 : 0];
+          const uint32_t w = r.k[j][ks];
+          kf = u32x4_t{T::template from_fp4<0>(w, sc), T::template from_fp4<1>(w, sc), T::template from_fp4<2>(w, sc),
+                       T::template from_fp4<3>(w, sc)};
+        } else {
+          kf = u32x4_t{r.k[j][4 * ks], r.k[j][4 * ks + 1], r.k[j][4 * ks + 2], r.k[j][4 * ks + 3]};
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[nt][j] = T::mfma16(kf, qf[nt][ks], s[nt][j]);
+      }
+    });
+
+    // Which of the lane's 8 keys each query vector sees.
+    uint32_t vis[NT];
+    int pk[8];
+    bool masked = !full;
+    if constexpr (WINDOW) {
+      const int pf = key_pos(c * kGaKeys), pl = key_pos(min(c * kGaKeys + kGaKeys - 1, n - 1));
+      masked = masked || pl > seen_by_all || !(pf > tmax - a.window || pl < a.sinks);
+      if (masked) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) pk[j] = key_pos(c * kGaKeys + (j >> 2) * 16 + 4 * qd + (j & 3));
+      }
+    }
+    u32x4_t pfr[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = s[nt][j >> 2][j & 3] * a.scale_log2;
+      if (masked) {
+        vis[nt] = have;
+        if constexpr (WINDOW) {
+          const int t = tcol[nt];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (!(pk[j] <= t && (pk[j] > t - a.window || pk[j] < a.sinks))) vis[nt] &= ~(1u << j);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = (vis[nt] >> j) & 1u ? x[j] : -INFINITY;
+      }
+      float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+      mx = fmaxf(m[nt], rows_max(mx));
+      if (ballot(mx > m[nt])) {
+        const float f = exp2_fast(m[nt] - finite_max(mx));
+        l[nt] *= f;
+#pragma unroll
+        for (int d = 0; d < VD; ++d) acc[nt][d] *= f;
+        m[nt] = mx;
+      }
+      const float mf = finite_max(mx);
+      float p[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) p[j] = exp2_fast(x[j] - mf);
+      l[nt] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+      pfr[nt] = u32x4_t{T::pack(p[0], p[1]), T::pack(p[2], p[3]), T::pack(p[4], p[5]), T::pack(p[6], p[7])};
+    }
+
+    // A key that some rows of the tile see and others do not may hold
+    // infinities or NaN: 0 * inf is NaN, so those go a way of their own.
+    bool fix = false;
+    if constexpr (WINDOW) {
+      if (masked) {
+        uint32_t bad = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if constexpr (FP4) {
+            bad |= vscale[j] > T::kTopScale;
+          } else {
+#pragma unroll
+            for (int i = 0; i < Raw::kVDwords; ++i) bad |= nonfinite_pair<T>(r.v[j][i]);
+          }
+        }
+        fix = ballot(bad != 0) != 0;
+      }
+    }
+    auto v_pair = [&](auto pic, u32x4_t& f0, u32x4_t& f1) {
+      constexpr int pi = decltype(pic)::value;
+      uint32_t two[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (FP4)
+          two[j] = T::template from_fp4<pi % 4>(r.v[j][pi / 4], vscale[j]);
+        else
+          two[j] = r.v[j][pi];
+      }
+      f0 = u32x4_t{pair_lo(two[0], two[1]), pair_lo(two[2], two[3]), pair_lo(two[4], two[5]), pair_lo(two[6], two[7])};
+      f1 = u32x4_t{pair_hi(two[0], two[1]), pair_hi(two[2], two[3]), pair_hi(two[4], two[5]), pair_hi(two[6], two[7])};
+    };
+    if (!fix) {
+      static_for<VD / 2>([&](auto pic) {
+        constexpr int pi = decltype(pic)::value;
+        u32x4_t f0, f1;
+        v_pair(pic, f0, f1);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          acc[nt][2 * pi] = T::mfma16(f0, pfr[nt], acc[nt][2 * pi]);
+          acc[nt][2 * pi + 1] = T::mfma16(f1, pfr[nt], acc[nt][2 * pi + 1]);
+        }
+      });
+    } else {
+      static_for<VD / 2>([&](auto pic) {
+        constexpr int pi = decltype(pic)::value;
+        u32x4_t f[2];
+        v_pair(pic, f[0], f[1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          u32x4_t clean, plus, minus;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t x, y, z;
+            split_nonfinite<T>(f[e][i], x, y, z);
+            clean[i] = x, plus[i] = y, minus[i] = z;
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            u32x4_t see;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              see[i] = ((vis[nt] >> (2 * i)) & 1u ? T::kOne : 0u) | ((vis[nt] >> (2 * i + 1)) & 1u ? T::kOne << 16 : 0u);
+            const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+            const f32x4_t np = T::mfma16(plus, see, zero), nm = T::mfma16(minus, see, zero);
+            f32x4_t o = T::mfma16(clean, pfr[nt], acc[nt][2 * pi + e]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] += nonfinite_term(np[i], nm[i]);
+            acc[nt][2 * pi + e] = o;
+          }
+        }
+      });
+    }
+  };
+
+  // Chunks c0 + wave, + 4, ...: the loads of the next chunk are issued before
+  // this one's products, its slots one chunk earlier still.
+  {
+    int c = c0 + wave;
+    if (c < c1) {
+      Raw r0, r1;
+      uint32_t k0, k1;
+      fetch(load_slot(c), r0, k0);
+      int sl = load_slot(c + kGaWaves);
+      auto step = [&](Raw& cur, uint32_t& kc, Raw& nxt, uint32_t& kn) {
+        if (c + kGaWaves < c1) {
+          fetch(sl, nxt, kn);
+          sl = load_slot(c + 2 * kGaWaves);
+        }
+        compute(cur, kc, c);
+        c += kGaWaves;
+        return c < c1;
+      };
+      while (step(r0, k0, r1, k1) && step(r1, k1, r0, k0)) {
+      }
+    }
+  }
+
+  // Join the waves, 16 columns at a time.  Thread (col, part) owns channels
+  // part*VD .. +VD of its column.
+  const int col = tid >> 4, part = tid & 15;
+  const uint32_t slot_floats = COLS * (D + 2);
+  const SplitBuffer sb(a.partial, a.nsplit > 1 ? (uint32_t)(gridDim.x * slot_floats * 4u) : 0u);
+  auto finish = [&](int nt, const float (&o)[VD], float mm, float ll) {
+    const int cc = nt * 16 + col, rr = cc / a.gb, hh = cc % a.gb;
+    if (rr >= nrows || hh >= heads) return;
+    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+    typename T::elem* dst = static_cast<typename T::elem*>(a.out) + (int64_t)(row0 + rr) * a.ld_out + (h0 + hh) * D + part * VD;
+    uint32_t w[VD / 2];
+#pragma unroll
+    for (int i = 0; i < VD / 2; ++i) w[i] = T::pack(o[2 * i] * inv, o[2 * i + 1] * inv);
+    if constexpr (VD == 4) {
+      *reinterpret_cast<u32x2_t*>(dst) = u32x2_t{w[0], w[1]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < VD / 2; i += 4) *reinterpret_cast<u32x4_t*>(dst + 2 * i) = u32x4_t{w[i], w[i + 1], w[i + 2], w[i + 3]};
+    }
+    if (a.lse != nullptr && part == 0)
+      a.lse[(int64_t)(row0 + rr) * a.hq + h0 + hh] = ll == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(ll)) * kLn2;
+  };
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const float ls = rows_sum(l[nt]);
+    __syncthreads();
+    if (qd == 0) sh.jn.m[wave][n16] = m[nt], sh.jn.l[wave][n16] = ls;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int d = 0; d < VD; d += 4)
+        *reinterpret_cast<f32x4_t*>(&sh.jn.o[wave][n16][VD * (4 * qd + i) + d]) =
+            f32x4_t{acc[nt][d][i], acc[nt][d + 1][i], acc[nt][d + 2][i], acc[nt][d + 3][i]};
+    __syncthreads();
+    float mm = -INFINITY, ll = 0.f, o[VD];
+#pragma unroll
+    for (int w = 0; w < kGaWaves; ++w) mm = fmaxf(mm, sh.jn.m[w][col]);
+#pragma unroll
+    for (int d = 0; d < VD; ++d) o[d] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kGaWaves; ++w) {
+      const float f = exp2_fast(sh.jn.m[w][col] - finite_max(mm));
+      ll += sh.jn.l[w][col] * f;
+#pragma unroll
+      for (int d = 0; d < VD; ++d) o[d] += sh.jn.o[w][col][part * VD + d] * f;
+    }
+    if (a.nsplit == 1) {
+      finish(nt, o, mm, ll);
+    } else {
+      const uint32_t base = blockIdx.x * slot_floats * 4;
+#pragma unroll
+      for (int d = 0; d < VD; d += 4)
+        sb.store4(base + ((nt * 16 + col) * D + part * VD + d) * 4, f32x4_t{o[d], o[d + 1], o[d + 2], o[d + 3]});
+      if (part == 0) sb.store2(base + (COLS * D + 2 * (nt * 16 + col)) * 4, mm, ll);
+    }
+  }
+  if (a.nsplit == 1) return;
+
+  // Every store of this lane is performed before the workgroup arrives.
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  if (tid == 0)
+    arrived = __hip_atomic_fetch_add(&a.counters[group], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  if (arrived != (uint32_t)a.nsplit - 1) return;
+  if (tid == 0) __hip_atomic_store(&a.counters[group], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const uint32_t first = (uint32_t)group * a.nsplit * slot_floats * 4;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    if (nt * 16 >= nrows * a.gb) break;
+    const uint32_t ml = first + (COLS * D + 2 * (nt * 16 + col)) * 4, oo = first + ((nt * 16 + col) * D + part * VD) * 4;
+    float mm = -INFINITY, ll = 0.f, o[VD];
+#pragma unroll
+    for (int d = 0; d < VD; ++d) o[d] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < a.nsplit; ++i) {
+      const float2 x = sb.load2(ml + i * slot_floats * 4);
+      const float nm = fmaxf(mm, x.x);
+      const float f = exp2_fast(mm - finite_max(nm)), g = exp2_fast(x.x - finite_max(nm));
+      ll = ll * f + x.y * g;
+#pragma unroll
+      for (int d = 0; d < VD; d += 4) {
+        const f32x4_t y = sb.load4(oo + i * slot_floats * 4 + d * 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[d + e] = o[d + e] * f + y[e] * g;
+      }
+      mm = nm;
+    }
+    finish(nt, o, mm, ll);
+  }
+}
+
+template <class T, bool FP4>
+int launch_attn_gather(const GatherArgs& a, int d, int nt, bool window, uint32_t blocks, hipStream_t stream) {
+  auto go = [&](auto dim, auto tiles, auto win) {
+    hipLaunchKernelGGL((attn_gather_kernel<T, FP4, decltype(dim)::value, decltype(tiles)::value, decltype(win)::value>),
+                       dim3(blocks), dim3(64 * kGaWaves), 0, stream, a);
+  };
+  auto by_window = [&](auto dim, auto tiles) {
+    if (window)
+      go(dim, tiles, std::true_type());
+    else
+      go(dim, tiles, std::false_type());
+  };
+  auto by_tiles = [&](auto dim) {
+    if (nt == 1)
+      by_window(dim, std::integral_constant<int, 1>());
+    else
+      by_window(dim, std::integral_constant<int, 2>());
+  };
+  if (d == 64)
+    by_tiles(std::integral_constant<int, 64>());
+  else if (d == 128)
+    by_tiles(std::integral_constant<int, 128>());
+  else
+    by_tiles(std::integral_constant<int, 256>());
+  return hipGetLastError() == hipSuccess ? BS_OK : BS_ERR_LAUNCH;
+}
+
+}  // namespace bs

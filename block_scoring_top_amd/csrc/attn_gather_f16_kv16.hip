@@ -1,0 +1,8 @@
+// attn_gather_f16_kv16.hip - the gathering attention kernels for f16 queries over the 16-bit cache.
+#include "attn_gather.h"
+
+namespace bs {
+
+template int launch_attn_gather<F16, false>(const GatherArgs&, int, int, bool, uint32_t, hipStream_t);
+
+}  // namespace bs

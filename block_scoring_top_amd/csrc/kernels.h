@@ -71,4 +71,35 @@ int launch_compress(const uint16_t* k_raw, int32_t num_tok, const int32_t* req_t
                     const int32_t* page_table, int32_t pt_stride, uint16_t* kcache, int64_t num_pages,
                     hipStream_t stream);
 
+// The 4-bit KV cache; arguments validated by the caller.
+int launch_kv4_store(const void* k, const void* v, int32_t dtype, int64_t ld_k, int64_t ld_v, const int32_t* slots,
+                     int32_t num_tok, int32_t hkv, int32_t d, uint8_t* codes, uint8_t* scales, int32_t num_slots,
+                     hipStream_t stream);
+int launch_kv4_load(const uint8_t* codes, const uint8_t* scales, int32_t num_slots, const int32_t* slots,
+                    int32_t num_slot_ids, int32_t hkv, int32_t d, void* k, void* v, int32_t dtype, int64_t ld_k,
+                    int64_t ld_v, hipStream_t stream);
+
+// Attention; arguments validated by the caller.  workspace may be null (keys
+// are then not split over workgroups).
+struct AttnCall {
+  const void* q;
+  int32_t dtype;
+  int64_t ld_q;
+  int32_t num_rows, hq, hkv, d;
+  const void *cache0, *cache1;
+  int32_t form;
+  int64_t ld_cache;
+  int32_t num_slots;
+  float scale;
+  void* out;
+  int64_t ld_out;
+  float* lse;
+  void* workspace;
+};
+int launch_attn_slots(const AttnCall& c, const int32_t* slots, int32_t ld_slots, const int32_t* count,
+                      hipStream_t stream);
+int launch_attn_window(const AttnCall& c, const int32_t* page_table, int32_t pt_stride, const int32_t* req_row_ptr,
+                       int32_t num_req, const int32_t* row_pos, int32_t max_rows, int32_t window, int32_t sinks,
+                       hipStream_t stream);
+
 }  // namespace bs

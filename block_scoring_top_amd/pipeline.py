@@ -1,4 +1,5 @@
-"""The whole hot path on one GPU: score -> top-k -> expand/translate.
+"""The whole hot path on one GPU: score -> top-k -> expand/translate, and the
+attention that reads the chosen slots.
 
 Allocates the output and workspace tensors once (torch, device memory) and
 then enqueues the three C-ABI calls on the current stream.  No host
@@ -8,7 +9,7 @@ from __future__ import annotations
 
 import torch
 
-from . import (idx_expand_translate, idx_score_decode, idx_score_prefill, idx_select_translate,
+from . import (attn_slots, attn_workspace, idx_expand_translate, idx_score_decode, idx_score_prefill, idx_select_translate,
                idx_select_translate_planned, prepare_score, prepare_select_translate, topk_plan, topk_plan_rows,
                topk_planned_workspace, topk_select_rows, topk_workspace)
 
@@ -41,6 +42,7 @@ class IndexerPath:
         self.workspace = topk_workspace(R, int(inp.max_vis), inp.k, dev)
         self.plan_buf = None          # planned selection: allocated on first use
         self.planned_workspace = None
+        self.attn_ws = None           # attention over the chosen slots: allocated on first use
         self._prepared = None
 
     def _prepare(self):
@@ -126,3 +128,12 @@ class IndexerPath:
             self.score(stream)
             self.select(stream)
             self.expand(stream)
+
+    def attend(self, q, cache, out, scale=None, lse=None, stream=None):
+        """Attention of the main query heads ``q`` [num_rows, q_heads,
+        head_dim] over the slots of the last ``run``, read from ``cache``
+        (``KV4Cache`` or ``KV16Cache``) into ``out``."""
+        if self.attn_ws is None:
+            self.attn_ws = attn_workspace(q.device)
+        attn_slots(q, cache, self.slots, out, count=self.out_count, scale=scale, lse=lse, workspace=self.attn_ws,
+                   stream=stream)

@@ -12,6 +12,11 @@
  * speculative draft steps) and idx_compress_store (the step before 1: raw
  * index keys compressed into the c = 4 key cache).
  *
+ * What consumes the chosen slots: attn_slots (attention over each row's
+ * slots) and attn_window (a sliding window and a few first tokens, for the
+ * layers without an indexer), over 16-bit K/V pools or a 4-bit cache that
+ * kv4_store writes and kv4_load reads back.
+ *
  * Sources (pages on the subject):
  *   [QSA]   "Qwen3.8-Flash-Next Day-0 in SGLang" (theainews.cc), section on Qwen
  *           sparse attention (QSA): 4 indexer query heads of 128 dims and one
@@ -404,6 +409,118 @@ int idx_compress_store(const uint16_t* k_raw, int32_t num_tok, const int32_t* re
                        uint16_t* ring, int32_t* ring_pos,
                        const int32_t* page_table, int32_t pt_stride, uint16_t* kcache, int64_t num_pages,
                        void* stream);
+
+/*
+ * Element types and cache forms of the calls below.
+ */
+enum bs_dtype { BS_BF16 = 0, BS_F16 = 1, BS_F32 = 2 };
+enum bs_kv_form {
+  BS_KV_16 = 0, /* cache0, cache1: K and V pools of the queries' 16-bit type, [num_pages * 64] slots of
+                   [kv_heads][head_dim], ld_cache elements from a slot to the next (>= kv_heads * head_dim) */
+  BS_KV_4 = 1   /* cache0, cache1: codes and scales as kv4_store writes them; ld_cache is not used */
+};
+
+/*
+ * The 4-bit KV cache.  Per (slot, kv head):
+ *   codes  [num_pages * 64][kv_heads][2][head_dim / 2] uint8: K, then V; the
+ *          E2M1 code of channel 2i in the low nibble of byte i, of channel
+ *          2i + 1 in the high one (bit 3: sign; codes 0..7: 0, 0.5, 1, 1.5, 2,
+ *          3, 4, 6);
+ *   scales [num_pages * 64][kv_heads][2][head_dim / 32] uint8: K, then V; byte
+ *          b of a group of 32 channels stands for 2^(b - 127), 255 for NaN.
+ * A channel's value is code * scale: 4.25 bits a channel.
+ *
+ * kv4_store - quantises K and V rows as they are written.  Row t of k and v
+ * goes to slot slots[t]; rows whose slot is negative or >= 64 * num_pages are
+ * skipped (padding).  Per group of 32 channels of a head: e = floor(log2(max
+ * |x|)) - 2, clamped to -120 .. 125 (-120 for a group of zeros); scale 2^e;
+ * each channel the E2M1 value nearest to x / 2^e, ties to the even code, 6 for
+ * anything larger.  A group that holds an infinity or a NaN gets scale byte
+ * 255 and codes 0: all of it reads back as NaN.  Bits of other slots are not
+ * touched.
+ *   k, v      [num_tok] rows of [kv_heads][head_dim] of `dtype` (bf16, fp16 or
+ *             fp32), ld_k / ld_v elements from a row to the next (multiples of
+ *             8, >= kv_heads * head_dim), 16-byte aligned: rows may lie inside
+ *             a fused projection's output.
+ *   head_dim  64, 128 or 256.
+ * Device precondition: the slots of one call are distinct (a slot named twice
+ * holds groups of either row).
+ *
+ * kv4_load - reads rows back: row i of k and v receives the values of slot
+ * slots[i] in `dtype` (exact in bf16 and fp32; rounded to fp16 where that
+ * type's range ends), zeros where the slot is negative or >= 64 * num_pages.
+ * Slots may repeat.
+ *
+ * Both return BS_OK (also when there are no rows), BS_ERR_NULL, BS_ERR_ARG
+ * (dtype, head_dim, kv_heads < 1, kv_heads * head_dim > 2^20, negative counts,
+ * num_pages < 1, a stride too small or no multiple of 8, a pointer that is not
+ * 16-byte aligned) or BS_ERR_LAUNCH.
+ */
+int kv4_store(const void* k, const void* v, int32_t dtype, int64_t ld_k, int64_t ld_v, const int32_t* slots,
+              int32_t num_tok, int32_t kv_heads, int32_t head_dim, uint8_t* codes, uint8_t* scales,
+              int64_t num_pages, void* stream);
+int kv4_load(const uint8_t* codes, const uint8_t* scales, int64_t num_pages, const int32_t* slots, int32_t num_slots,
+             int32_t kv_heads, int32_t head_dim, void* k, void* v, int32_t dtype, int64_t ld_k, int64_t ld_v,
+             void* stream);
+
+/*
+ * attn_slots - grouped-query attention of each query row over its own list of
+ * KV slots [QSA: sparse GQA reads the selected entries of the K/V cache; MASK:
+ * the only mask is slot >= 0], the slots as idx_select_translate emits them.
+ *
+ * For row r and query head h, kv head g = h / (q_heads / kv_heads), over the
+ * entries i < min(count[r], ld_slots) of slots[r * ld_slots + i] that are in
+ * [0, 64 * num_pages):
+ *   x_i = scale * <q[r][h], K[slot_i][g]>,
+ *   out[r][h] = sum_i exp(x_i - lse) V[slot_i][g],  lse[r][h] = log sum_i exp(x_i).
+ * A slot listed twice counts twice.  A row without a slot gives zeros and lse
+ * -inf.  Scores, running maximum, sums and outputs are held in FP32; the
+ * weights are rounded to the queries' type for their product with V, and the
+ * output once.
+ *   q          [num_rows] rows of [q_heads][head_dim], bf16 or fp16 (dtype),
+ *              ld_q elements apart (a multiple of 8, >= q_heads * head_dim).
+ *   slots      [num_rows][ld_slots] int32; count [num_rows] int32 or NULL (all
+ *              ld_slots entries, -1 where there is none).
+ *   out        as q, ld_out elements apart.  lse: [num_rows][q_heads] FP32 or
+ *              NULL.
+ *   workspace  BS_ATTN_WORKSPACE_BYTES of device memory, zero-filled before its
+ *              first use (every call leaves its first 64 KiB zero again), or
+ *              NULL with workspace_bytes 0: one size serves every call.  With
+ *              it, few rows have their keys split over workgroups; without it
+ *              they are not, which gives the same results slower.  Calls that
+ *              share a workspace must not overlap in time.
+ * q_heads is a multiple of kv_heads; head_dim is 64, 128 or 256.
+ *
+ * attn_window - causal attention over a sliding window and the first tokens:
+ * a row of request b at position t = row_pos[r] sees the positions p <= t with
+ * p > t - window or p < sinks, read through page_table (entries that are
+ * negative or >= num_pages, and positions past 64 * pt_stride, hold no token
+ * and are not seen).  Same formulas, types and conventions as attn_slots; a row
+ * that sees nothing (t < 0, say: padding) gives zeros and lse -inf.  Rows at
+ * and behind req_row_ptr[num_req], and a request's rows past its first
+ * max_rows, are left as they were.  Infinities and NaN at positions that a row
+ * does not see do not reach it.
+ *   max_rows   host-side bound on the rows of any request (sizes the grid): 1
+ *              for decode, the draft length for verify, the chunk for prefill.
+ *   window     >= 0, sinks >= 0 (window >= the context: plain causal attention).
+ *
+ * Both return BS_OK (also when there are no rows), BS_ERR_NULL, BS_ERR_ARG
+ * (dtype not bf16 or fp16, an unknown form, head_dim, head counts, negative
+ * counts, num_pages or pt_stride < 1, a stride too small or no multiple of 8,
+ * a pointer that is not 16-byte aligned, a scale that is not finite, more than
+ * 2^23 workgroups), BS_ERR_WORKSPACE (a workspace smaller than
+ * BS_ATTN_WORKSPACE_BYTES) or BS_ERR_LAUNCH.
+ */
+#define BS_ATTN_WORKSPACE_BYTES (((size_t)32 << 20) + ((size_t)64 << 10))
+int attn_slots(const void* q, int32_t dtype, int64_t ld_q, int32_t num_rows, int32_t q_heads, int32_t kv_heads,
+               int32_t head_dim, const void* cache0, const void* cache1, int32_t cache_form, int64_t ld_cache,
+               int64_t num_pages, const int32_t* slots, int32_t ld_slots, const int32_t* count, float scale,
+               void* out, int64_t ld_out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+int attn_window(const void* q, int32_t dtype, int64_t ld_q, int32_t num_rows, int32_t q_heads, int32_t kv_heads,
+                int32_t head_dim, const void* cache0, const void* cache1, int32_t cache_form, int64_t ld_cache,
+                int64_t num_pages, const int32_t* page_table, int32_t pt_stride, const int32_t* req_row_ptr,
+                int32_t num_req, const int32_t* row_pos, int32_t max_rows, int32_t window, int32_t sinks, float scale,
+                void* out, int64_t ld_out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 /* bs_status_string - a static, human-readable name for a status code. */
 const char* bs_status_string(int status);
