@@ -237,7 +237,7 @@ def _own_calls(s):
         calls = [bst.prepare_kv4_store(s["k"], s["v"], s["slots"], cache)] if case["op"] == "store" else []
         return calls + [bst.prepare_kv4_load(cache, s["slots"], s["k_out"], s["v_out"])]
     cache = (bst.KV4Cache if case["form"] == "kv4" else bst.KV16Cache)(*s["pool"])
-    ws = bst.attn_workspace(DEV)
+    ws = s["workspace"] = bst.attn_workspace(DEV)  # a prepared call holds addresses: the state keeps the tensor
     if case["op"] == "slots":
         return [bst.prepare_attn_slots(s["q"], cache, s["slots"], s["out"], count=s["count"], lse=s["lse"],
                                        workspace=ws)]
