@@ -574,14 +574,20 @@ class PreparedCall:
         self.args = args
         self.device = device
         self._f = getattr(lib(), fn)
+        # Arguments as instances of their declared C types, so that a call
+        # converts nothing but the stream.
+        self._args = tuple(a if isinstance(a, t) else t(a) for a, t in zip(args, self._f.argtypes))
 
     def __call__(self, stream=None):
-        # A launch goes to the current device; tensors may live on another.
-        if self.device.index is not None and self.device.index != torch.cuda.current_device():
+        # The current stream and device are asked for by their index: about
+        # 1 us less per call than through torch's Stream objects.
+        index = self.device.index
+        if index == torch._C._cuda_getDevice():
+            s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+            st = self._f(*self._args, s)
+        else:  # a launch goes to the current device, and the tensors live on another
             with torch.cuda.device(self.device):
-                st = self._f(*self.args, _stream(stream, self.device))
-        else:
-            st = self._f(*self.args, _stream(stream, self.device))
+                st = self._f(*self._args, _stream(stream, self.device))
         if st != 0:
             _check(st, self.fn)
 
@@ -600,10 +606,7 @@ class BoundCall:
     def __init__(self, prepared: PreparedCall, stream_ptr):
         self.fn = prepared.fn
         self._f = prepared._f
-        # Arguments as instances of their declared C types, so that a call
-        # converts nothing.
-        args = (*prepared.args, stream_ptr)
-        self._args = tuple(a if isinstance(a, t) else t(a) for a, t in zip(args, self._f.argtypes))
+        self._args = (*prepared._args, stream_ptr)
 
     def __call__(self):
         st = self._f(*self._args)

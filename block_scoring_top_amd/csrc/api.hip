@@ -312,7 +312,7 @@ BS_EXPORT int attn_slots(const void* q, int32_t dtype, int64_t ld_q, int32_t num
   if (st != BS_OK) return st;
   if (ld_slots < 0) return BS_ERR_ARG;
   if (num_rows == 0) return BS_OK;
-  if (!slots) return BS_ERR_NULL;
+  if (!slots && ld_slots > 0) return BS_ERR_NULL;  // empty lists need no storage
   const bs::AttnCall c = {q,      dtype,      ld_q,     num_rows,   q_heads, kv_heads, head_dim, cache0, cache1,
                           cache_form, ld_cache, slots_of_pages(num_pages), scale, out, ld_out, lse, workspace};
   return bs::launch_attn_slots(c, slots, ld_slots, count, static_cast<hipStream_t>(stream));

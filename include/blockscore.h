@@ -479,7 +479,7 @@ int kv4_load(const uint8_t* codes, const uint8_t* scales, int64_t num_pages, con
  * output once.
  *   q          [num_rows] rows of [q_heads][head_dim], bf16 or fp16 (dtype),
  *              ld_q elements apart (a multiple of 8, >= q_heads * head_dim).
- *   slots      [num_rows][ld_slots] int32; count [num_rows] int32 or NULL (all
+ *   slots      [num_rows][ld_slots] int32 (NULL if ld_slots is 0); count [num_rows] int32 or NULL (all
  *              ld_slots entries, -1 where there is none).
  *   out        as q, ld_out elements apart.  lse: [num_rows][q_heads] FP32 or
  *              NULL.

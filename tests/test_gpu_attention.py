@@ -226,6 +226,11 @@ def test_slots_without_counts_reads_the_whole_list():
     want = [attend_row(_f64(q[r]), K[s], V[s], 128 ** -0.5) for r, s in ((0, np.arange(87)), (1, np.arange(0)))]
     check_rows(_f64(out[:2, :8]), _f64(lse[:2]), want, "bf16", [87, 0], np.abs(V).max())
     assert (out[1, :8] == 0).all() and torch.isneginf(lse[1]).all()
+    out.fill_(-77.0)
+    bst.attn_slots(q, cache, torch.empty((2, 0), dtype=torch.int32, device="cuda"), out[:2, :8], lse=lse[:2],
+                   workspace=bst.attn_workspace("cuda"))         # lists of no entries
+    assert (out[:2, :8] == 0).all() and torch.isneginf(lse[:2]).all()
+    _intact(out, lse, 2, 8)
 
 
 @pytest.mark.parametrize("form", ["kv4", "kv16"])
