@@ -13,7 +13,8 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libblockscore.so")
 SOURCES = ["api.hip", "score_decode.hip", "score_prefill.hip", "topk.hip", "expand.hip", "compress.hip", "kv4.hip",
            "attn.hip", "attn_gather_bf16_kv4.hip", "attn_gather_bf16_kv16.hip", "attn_gather_f16_kv4.hip",
-           "attn_gather_f16_kv16.hip"]
+           "attn_gather_f16_kv16.hip", "attn_prefill_bf16_kv4.hip", "attn_prefill_bf16_kv16.hip",
+           "attn_prefill_f16_kv4.hip", "attn_prefill_f16_kv16.hip"]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -56,24 +56,41 @@ __device__ __forceinline__ uint32_t nonfinite_pair(uint32_t x) {
   return ((x & T::kExpMask) + T::kExpLsb) & 0x80008000u;
 }
 
-// A pair with infinities and NaN replaced by zeros (clean), and 0/1 marks of
-// the halves that are +inf or NaN (plus) and -inf or NaN (minus).
+// All ones in the 16-bit halves whose bit 15 is set.
+__device__ __forceinline__ uint32_t spread_halves(uint32_t x) { return ((x >> 15) & 0x00010001u) * 0xFFFFu; }
+// The bits of a where sel is set, of b elsewhere.
+__device__ __forceinline__ uint32_t bit_select(uint32_t sel, uint32_t a, uint32_t b) { return (a & sel) | (b & ~sel); }
+// All ones if bit i of x is set, else 0.
+__device__ __forceinline__ uint32_t bit_mask(uint32_t x, int i) { return (uint32_t)__builtin_amdgcn_sbfe((int)x, i, 1); }
+
+// A pair with infinities and NaN replaced by zeros (clean), and marks for
+// them: 1 for +inf, 64 for -inf, 65 for NaN, exact in both 16-bit types.  This
+// and what follows are written without comparisons: their lane masks, dozens
+// of them at once, would not fit the scalar registers.
 template <class T>
-__device__ __forceinline__ void split_nonfinite(uint32_t x, uint32_t& clean, uint32_t& plus, uint32_t& minus) {
-  clean = plus = minus = 0;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t v = (x >> (16 * h)) & 0xFFFFu, mag = v & 0x7FFFu;
-    if (mag < T::kInfBits) clean |= v << (16 * h);
-    if (mag > T::kInfBits || v == T::kInfBits) plus |= T::kOne << (16 * h);
-    if (mag > T::kInfBits || v == (T::kInfBits | 0x8000u)) minus |= T::kOne << (16 * h);
-  }
+__device__ __forceinline__ void split_nonfinite(uint32_t x, uint32_t& clean, uint32_t& marks) {
+  constexpr uint32_t mant = 0x7FFF7FFFu & ~T::kExpMask, both = 0x00010001u;
+  const uint32_t bad = spread_halves(nonfinite_pair<T>(x));
+  const uint32_t nan = spread_halves(((x & mant) + 0x7FFF7FFFu) & 0x80008000u);
+  clean = x & ~bad;
+  marks = bad & bit_select(nan, T::k65 * both, bit_select(spread_halves(x), T::k64 * both, T::kOne * both));
 }
 
-// What visible infinities and NaN add to a sum: counts of +inf-or-NaN and of
-// -inf-or-NaN terms.
-__device__ __forceinline__ float nonfinite_term(float plus, float minus) {
-  return plus > 0.f ? (minus > 0.f ? NAN : INFINITY) : (minus > 0.f ? -INFINITY : 0.f);
+// What visible infinities and NaN add to a sum, from the sum of the marks of
+// at most 32 keys: its 64s count -inf and NaN, the rest +inf and NaN.
+__device__ __forceinline__ float nonfinite_term(float n) {
+  const float minus = floorf(n * (1.f / 64)), plus = n - 64.f * minus;
+  const uint32_t p = 0u - (uint32_t)(int)fminf(plus, 1.f), q = 0u - (uint32_t)(int)fminf(minus, 1.f);
+  return __uint_as_float(p & 0x7F800000u) + __uint_as_float(q & 0xFF800000u);
+}
+
+// Bit k (0 .. 63) set where position p0 + k is seen by a row at position t.
+__device__ __forceinline__ uint64_t visible_bits(int p0, int t, int window, int sinks) {
+  auto below = [](int64_t n) -> uint64_t {  // bits 0 .. n-1
+    const int c = (int)(n < 0 ? 0 : n > 64 ? 64 : n);
+    return c == 0 ? 0 : ~0ull >> (64 - c);
+  };
+  return below((int64_t)t + 1 - p0) & (~below((int64_t)t - window + 1 - p0) | below((int64_t)sinks - p0));
 }
 
 __device__ __forceinline__ void wave_fence() {

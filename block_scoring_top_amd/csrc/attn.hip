@@ -1,10 +1,18 @@
 // attn.hip - host side of the attention calls: which kernel, its tiles, and
 // over how many workgroups a row's keys are split.
 #include <algorithm>
+#include <cmath>
+
 
 #include "attn_gather.h"
+#include "attn_prefill.h"
 
 namespace bs {
+
+extern template int launch_attn_prefill<Bf16, true>(const PrefillArgs&, int, uint32_t, hipStream_t);
+extern template int launch_attn_prefill<Bf16, false>(const PrefillArgs&, int, uint32_t, hipStream_t);
+extern template int launch_attn_prefill<F16, true>(const PrefillArgs&, int, uint32_t, hipStream_t);
+extern template int launch_attn_prefill<F16, false>(const PrefillArgs&, int, uint32_t, hipStream_t);
 
 extern template int launch_attn_gather<Bf16, true>(const GatherArgs&, int, int, bool, uint32_t, hipStream_t);
 extern template int launch_attn_gather<Bf16, false>(const GatherArgs&, int, int, bool, uint32_t, hipStream_t);
@@ -15,6 +23,7 @@ namespace {
 
 constexpr int64_t kCounterBytes = 64 << 10;  // first part of the workspace: arrival counters
 constexpr int64_t kPartialBytes = (int64_t)BS_ATTN_WORKSPACE_BYTES - kCounterBytes;
+constexpr int kGatherCols = 64;              // (row, head) pairs a request may have for the gathering kernel
 constexpr int64_t kFillBlocks = 1024;        // workgroups worth splitting for: 4 on each of 256 compute units
 
 GatherArgs common_args(const AttnCall& c) {
@@ -56,6 +65,38 @@ int run_gather(GatherArgs& a, const AttnCall& c, int nt, bool window, int64_t ti
                            : launch_attn_gather<F16, false>(a, c.d, nt, window, blocks, stream);
 }
 
+int run_prefill(const AttnCall& c, const int32_t* page_table, int32_t pt_stride, const int32_t* req_row_ptr,
+                int32_t num_req, const int32_t* row_pos, int32_t max_rows, int32_t window, int32_t sinks,
+                hipStream_t stream) {
+  PrefillArgs a = {};
+  a.q = c.q, a.ld_q = c.ld_q;
+  a.a = static_cast<const uint8_t*>(c.cache0), a.b = static_cast<const uint8_t*>(c.cache1);
+  a.ld_kv = c.ld_cache;
+  a.num_pages = c.num_slots / kPage, a.num_rows = c.num_rows, a.hq = c.hq, a.hkv = c.hkv;
+  const int g = c.hq / c.hkv, cols = prefill_cols(c.d);
+  a.hblocks = (g + cols - 1) / cols;
+  a.gb = (g + a.hblocks - 1) / a.hblocks;
+  a.page_table = page_table, a.req_row_ptr = req_row_ptr, a.row_pos = row_pos, a.pt_stride = pt_stride;
+  a.max_rows = max_rows, a.window = window, a.sinks = sinks;
+  a.rows_per_tile = cols / a.gb;
+  a.tiles_per_req = (int)(((int64_t)max_rows + a.rows_per_tile - 1) / a.rows_per_tile);
+  // The running maximum is of unscaled scores times the scale, so that must
+  // not be negative (q changes sign instead) nor 0 (a masked -inf times 0).
+  const float s = c.scale * kLog2e;
+  a.scale_log2 = std::max(std::fabs(s), 1.1754944e-38f);
+  a.flip = s < 0.f ? 0x80008000u : 0u;
+  a.out = c.out, a.ld_out = c.ld_out, a.lse = c.lse;
+  const int64_t blocks = (int64_t)num_req * a.tiles_per_req * a.hkv * a.hblocks;
+  if (blocks > (int64_t)1 << 21) return BS_ERR_ARG;
+  a.blocks = (uint32_t)blocks;
+  const uint32_t grid = (a.blocks + 7) / 8 * 8;
+  if (c.dtype == BS_BF16)
+    return c.form == BS_KV_4 ? launch_attn_prefill<Bf16, true>(a, c.d, grid, stream)
+                             : launch_attn_prefill<Bf16, false>(a, c.d, grid, stream);
+  return c.form == BS_KV_4 ? launch_attn_prefill<F16, true>(a, c.d, grid, stream)
+                           : launch_attn_prefill<F16, false>(a, c.d, grid, stream);
+}
+
 }  // namespace
 
 int launch_attn_slots(const AttnCall& c, const int32_t* slots, int32_t ld_slots, const int32_t* count,
@@ -70,8 +111,10 @@ int launch_attn_slots(const AttnCall& c, const int32_t* slots, int32_t ld_slots,
 int launch_attn_window(const AttnCall& c, const int32_t* page_table, int32_t pt_stride, const int32_t* req_row_ptr,
                        int32_t num_req, const int32_t* row_pos, int32_t max_rows, int32_t window, int32_t sinks,
                        hipStream_t stream) {
-  GatherArgs a = common_args(c);
   const int g = c.hq / c.hkv, nt = (int64_t)g * max_rows <= 16 ? 1 : 2;
+  if ((int64_t)g * max_rows > kGatherCols)
+    return run_prefill(c, page_table, pt_stride, req_row_ptr, num_req, row_pos, max_rows, window, sinks, stream);
+  GatherArgs a = common_args(c);
   split_heads(a, nt);
   a.page_table = page_table, a.pt_stride = pt_stride, a.req_row_ptr = req_row_ptr, a.row_pos = row_pos;
   a.max_rows = max_rows, a.window = window, a.sinks = sinks;

@@ -333,7 +333,8 @@ __global__ __launch_bounds__(64 * kGaWaves, NT * D > 256 ? 1 : 2) void attn_gath
             if (!(pk[j] <= t && (pk[j] > t - a.window || pk[j] < a.sinks))) vis[nt] &= ~(1u << j);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = (vis[nt] >> j) & 1u ? x[j] : -INFINITY;
+        for (int j = 0; j < 8; ++j)
+          x[j] = __uint_as_float(bit_select(bit_mask(vis[nt], j), __float_as_uint(x[j]), 0xFF800000u));
       }
       float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
       mx = fmaxf(m[nt], rows_max(mx));
@@ -401,25 +402,25 @@ __global__ __launch_bounds__(64 * kGaWaves, NT * D > 256 ? 1 : 2) void attn_gath
         v_pair(pic, f[0], f[1]);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          u32x4_t clean, plus, minus;
+          u32x4_t clean, marks;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            uint32_t x, y, z;
-            split_nonfinite<T>(f[e][i], x, y, z);
-            clean[i] = x, plus[i] = y, minus[i] = z;
+            uint32_t x, y;
+            split_nonfinite<T>(f[e][i], x, y);
+            clean[i] = x, marks[i] = y;
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             u32x4_t see;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              see[i] = ((vis[nt] >> (2 * i)) & 1u ? T::kOne : 0u) | ((vis[nt] >> (2 * i + 1)) & 1u ? T::kOne << 16 : 0u);
-            const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-            const f32x4_t np = T::mfma16(plus, see, zero), nm = T::mfma16(minus, see, zero);
+              see[i] = (bit_mask(vis[nt], 2 * i) & T::kOne) | (bit_mask(vis[nt], 2 * i + 1) & (T::kOne << 16));
+            const f32x4_t cnt = T::mfma16(marks, see, f32x4_t{0.f, 0.f, 0.f, 0.f});
             f32x4_t o = T::mfma16(clean, pfr[nt], acc[nt][2 * pi + e]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] += nonfinite_term(np[i], nm[i]);
+            for (int i = 0; i < 4; ++i) o[i] += nonfinite_term(cnt[i]);
             acc[nt][2 * pi + e] = o;
+            __builtin_amdgcn_sched_barrier(0);  // one channel at a time: this path is rare, its registers are not
           }
         }
       });

@@ -1,0 +1,394 @@
+// attn_prefill.h - attention over a sliding window and the first tokens, for
+// many query rows of a request (attn_window's prefill form).
+//
+// The same sums as attn_gather.h, 4*D flops per (query vector, key): with many
+// rows a key, the matrix cores and the softmax between their two products
+// bound it.  A workgroup takes 32 * NW (row, head) pairs that share a kv head
+// (the heads of a group packed beside the rows, so that a tile spans few
+// positions) and walks the pages of its keys; a page is a tile of 64 keys:
+//   * K and V pages are copied from HBM straight into LDS (16-bit pools), or
+//     loaded into registers, converted and written there (4-bit cache), one
+//     page ahead, two buffers, one barrier a page;
+//   * S^T = K q^T with v_mfma_f32_32x32x16: a lane holds one query vector and
+//     16 of every 32 keys, so the row maximum and sum need one exchange
+//     between the wave's halves;
+//   * O^T += V^T P^T: the accumulator of S^T is the B operand of the second
+//     product with its keys in a fixed order (8*(i/4) + 4*half + i%4), and the
+//     A operand is read from the row-major V tile in that order with the
+//     transposing LDS loads; P never leaves its lane;
+//   * the running maximum moves only when a score exceeds it by more than
+//     kSlack (in log2), so the accumulators are hardly ever rescaled; P stays
+//     below 2^kSlack, far inside FP32 and both 16-bit types;
+//   * P is rounded to the 16-bit operand type for the product (relative
+//     2^-9 in bf16, as the output's own rounding);
+//   * K rows are XOR-swizzled by 16-byte slices with key mod 16, V rows with
+//     2 * (key mod 8), so that both kinds of LDS reads spread over the banks;
+//   * pages that every row of a wave sees are not masked at all, pages that
+//     none sees are skipped by the wave.
+// Consecutive row blocks of one kv head run on one XCD, whose L2 then holds
+// their window.
+#pragma once
+
+#include "attn.h"
+
+namespace bs {
+
+constexpr float kSlack = 8.f;
+
+struct PrefillArgs {
+  const void* q;
+  int64_t ld_q;
+  const uint8_t *a, *b;
+  int64_t ld_kv;
+  int32_t num_pages, num_rows, hq, hkv, gb, hblocks;
+  const int32_t *page_table, *req_row_ptr, *row_pos;
+  int32_t pt_stride, max_rows, rows_per_tile, tiles_per_req, window, sinks;
+  float scale_log2;  // of the scores, not below 0
+  uint32_t flip;     // sign bits to turn in q: the scale was negative
+  void* out;
+  int64_t ld_out;
+  float* lse;
+  uint32_t blocks;
+};
+
+template <class T>
+__device__ __forceinline__ f32x16_t mfma32(const u32x4_t& a, const u32x4_t& b, const f32x16_t& c) {
+  if constexpr (std::is_same<T, Bf16>::value)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+}
+
+typedef int16_t i16x4_t __attribute__((ext_vector_type(4)));
+
+// Four consecutive rows of one 16-bit column: the 16 lanes of a block give the
+// addresses of 4 rows x 16 columns (8 bytes each) and lane c of the block
+// receives column c.
+__device__ __forceinline__ u32x2_t lds_read_tr(const uint8_t* p) {
+  return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                         (__attribute__((address_space(3))) i16x4_t*)(uintptr_t)(uint32_t)(uintptr_t)p));
+}
+
+template <class T, bool FP4, int D, int NW>
+__global__ __launch_bounds__(64 * NW, NW / 4) void attn_prefill_kernel(const PrefillArgs a) {
+  constexpr int ROW = D * 2;                // bytes of a key in LDS
+  constexpr int NS = D / 8;                 // its 16-byte slices
+  constexpr int KSWZ = NS < 16 ? NS - 1 : 15, VSWZ = NS < 16 ? NS - 1 : 15;
+  constexpr int KS = D / 16, DT = D / 32;   // steps of the products
+  constexpr int THREADS = 64 * NW;
+  __shared__ __attribute__((aligned(1024))) uint8_t kv[2][2][kPage * ROW];  // buffer, K or V
+
+  const int tid = threadIdx.x, lane = tid & 63, n32 = lane & 31, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // Block b runs on XCD b mod 8: consecutive ids on one XCD.
+  const uint32_t per = gridDim.x / 8, id = (blockIdx.x % 8) * per + blockIdx.x / 8;
+  if (id >= a.blocks) return;
+  const int i_tile = id % a.tiles_per_req, rest = id / a.tiles_per_req;
+  const int hb = rest % (a.hkv * a.hblocks), b = rest / (a.hkv * a.hblocks);
+  const int kvh = hb / a.hblocks, G = a.hq / a.hkv, hin = (hb % a.hblocks) * a.gb;
+  const int heads = min(a.gb, G - hin), h0 = kvh * G + hin;
+
+  const int ra = max(a.req_row_ptr[b], 0);
+  const int rb = (int)min((int64_t)min(a.req_row_ptr[b + 1], a.num_rows), (int64_t)ra + a.max_rows);
+  const int64_t first = (int64_t)ra + (int64_t)i_tile * a.rows_per_tile;
+  if (first >= rb) return;
+  const int row0 = (int)first, nrows = min(a.rows_per_tile, rb - row0);
+
+  // Positions: of the workgroup's rows, of the wave's, of the lane's.
+  int lo = 0x7FFFFFFF, hi = -1;
+  for (int r = lane; r < nrows; r += 64) {
+    const int t = a.row_pos[row0 + r];
+    lo = min(lo, t < 0 ? 0x7FFFFFFF : t), hi = max(hi, t);
+  }
+  const int col = wave * 32 + n32, rr = col / a.gb, hh = col % a.gb;
+  const bool ok = rr < nrows && hh < heads;
+  const int t = ok ? a.row_pos[row0 + rr] : -1;
+  int wlo = ok ? (t < 0 ? -1 : t) : 0x7FFFFFFF, whi = t, wfirst = t < 0 ? 0x7FFFFFFF : t;
+  for (int o = 32; o > 0; o >>= 1) {
+    lo = min(lo, __shfl_xor(lo, o)), hi = max(hi, __shfl_xor(hi, o));
+    wlo = min(wlo, __shfl_xor(wlo, o)), whi = max(whi, __shfl_xor(whi, o)), wfirst = min(wfirst, __shfl_xor(wfirst, o));
+  }
+  const int tmin = __builtin_amdgcn_readfirstlane(lo), tmax = __builtin_amdgcn_readfirstlane(hi);
+  // The wave's last position that all of its rows see, its last and its first
+  // position.
+  const int w_all = __builtin_amdgcn_readfirstlane(wlo), w_last = __builtin_amdgcn_readfirstlane(whi);
+  const int w_first = __builtin_amdgcn_readfirstlane(wfirst);
+  const int last = (int)min((int64_t)min(tmax, 0x7FFFFF00), (int64_t)a.pt_stride * kPage - 1);
+  const int ns = max(0, min(a.sinks, last + 1)), sink_pages = (ns + kPage - 1) / kPage;
+  const int wp0 = max(max(0, tmin - a.window + 1) / kPage, sink_pages);
+  const int tiles = last < 0 ? 0 : sink_pages + max(0, last / kPage - wp0 + 1);
+  const int32_t* ptab = a.page_table + (int64_t)b * a.pt_stride;
+
+  u32x4_t qf[KS];
+  {
+    const typename T::elem* src = static_cast<const typename T::elem*>(a.q) + (int64_t)(row0 + (ok ? rr : 0)) * a.ld_q +
+                                  (h0 + (ok ? hh : 0)) * D + 8 * half;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const u32x4_t x = *reinterpret_cast<const u32x4_t*>(src + 16 * ks);
+      qf[ks] = ok ? x ^ a.flip : u32x4_t{0, 0, 0, 0};
+    }
+  }
+
+  f32x16_t acc[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[d][i] = 0.f;
+  float m = -INFINITY, l = 0.f;  // running maximum (scaled) and this half's share of the sum
+
+  auto page_pos = [&](int i) { return i < sink_pages ? i : wp0 + (i - sink_pages); };
+  // Next tile from `i` on whose page is one; `page` receives its id.
+  auto next_tile = [&](int i, int& page) {
+    for (; i < tiles; ++i) {
+      page = ptab[page_pos(i)];
+      if (page >= 0 && page < a.num_pages) break;
+    }
+    return i;
+  };
+
+  // 4-bit: what a thread holds of the next page: 32 channels (16 bytes of
+  // codes and their scale) of K or V, UNITS times.
+  constexpr int PIECES = kPage * D / 16, UNITS = FP4 ? (PIECES + THREADS - 1) / THREADS : 1;
+  static_assert(FP4 || kPage * NS % THREADS == 0, "the copies fill whole waves");
+  u32x4_t codes[UNITS];
+  uint32_t scale[UNITS];
+  auto issue = [&](int page, int buf) {
+    if constexpr (FP4) {
+      const uint64_t rec = (uint64_t)a.hkv * D;
+      const uint8_t* c0 = a.a + (uint64_t)page * kPage * rec + kvh * D;
+      const uint8_t* s0 = a.b + (uint64_t)page * kPage * (rec / 16) + kvh * (D / 16);
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) {
+        const int x = u * THREADS + tid, key = x / (D / 16), part = x % (D / 16);
+        if (PIECES % THREADS != 0 && x >= PIECES) continue;
+        codes[u] = *reinterpret_cast<const u32x4_t*>(c0 + (uint64_t)key * rec + part * 16);
+        scale[u] = s0[(uint64_t)key * (rec / 16) + part];
+      }
+    } else {
+      const uint32_t rec = (uint32_t)(a.ld_kv * 2), bytes = rec * (kPage - 1) + D * 2;
+      const uint64_t at = (uint64_t)page * kPage * (uint64_t)a.ld_kv * 2 + kvh * D * 2;
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        const uint64_t p = reinterpret_cast<uint64_t>(which ? a.b : a.a) + at;
+        const u32x4_t rs = {(uint32_t)p, (uint32_t)(p >> 32), bytes, 0};
+        const uint32_t dst = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)(&kv[buf][which][0]);
+#pragma unroll
+        for (int j = 0; j < kPage * NS / THREADS; ++j) {
+          const int x = j * THREADS + tid, key = x / NS, s = x % NS;
+          const int f = which ? (2 * key) & VSWZ : key & KSWZ;
+          lds_dma_b128(rs, key * rec + (uint32_t)(s ^ f) * 16, dst + (j * THREADS + wave * 64) * 16);
+        }
+      }
+    }
+  };
+  auto settle = [&](int buf) {
+    if constexpr (FP4) {
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) {
+        const int x = u * THREADS + tid, key = x / (D / 16), part = x % (D / 16);
+        if (PIECES % THREADS != 0 && x >= PIECES) continue;
+        const int which = part >= D / 32, s = (part % (D / 32)) * 4, f = which ? (2 * key) & VSWZ : key & KSWZ;
+        uint8_t* row = &kv[buf][which][key * ROW];
+        const float sc = kv4_scale(scale[u]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w = codes[u][i];
+          *reinterpret_cast<u32x4_t*>(row + ((s + i) ^ f) * 16) =
+              u32x4_t{T::template from_fp4<0>(w, sc), T::template from_fp4<1>(w, sc), T::template from_fp4<2>(w, sc),
+                      T::template from_fp4<3>(w, sc)};
+        }
+      }
+    } else {
+      wait_vmcnt<0>();
+    }
+  };
+
+  const uint32_t k_row = n32 * ROW, k_swz = n32 & KSWZ;
+  const int v_key = 4 * half + ((lane & 15) >> 2), v_cc = lane & 3;
+  uint32_t v_off[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d) {
+    const int s = 4 * d + 2 * ((lane >> 4) & 1) + (v_cc >> 1);
+    v_off[d] = v_key * ROW + ((s ^ ((2 * v_key) & VSWZ)) * 16) + (v_cc & 1) * 8;
+  }
+  // V^T's fragment of 16 keys from kb on, channels 32*d .. +31.
+  auto v_frag = [&](const uint8_t* vt, int kb, int d) {
+    const u32x2_t x = lds_read_tr(vt + v_off[d] + kb * ROW), y = lds_read_tr(vt + v_off[d] + (kb + 8) * ROW);
+    return u32x4_t{x.x, x.y, y.x, y.y};
+  };
+
+  auto compute = [&](int p0, int buf) {
+    const bool full = p0 + kPage - 1 <= w_all && (p0 > w_last - a.window || p0 + kPage - 1 < a.sinks);
+    const uint8_t *kt = kv[buf][0], *vt = kv[buf][1];
+    f32x16_t s[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[j][i] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const u32x4_t kf = *reinterpret_cast<const u32x4_t*>(kt + j * 32 * ROW + k_row + (((2 * ks + half) ^ k_swz) * 16));
+        s[j] = mfma32<T>(kf, qf[ks], s[j]);
+      }
+    }
+    // Bits of the lane's keys that its row sees: key 32*j + 8*(i/4) +
+    // 4*half + i%4 at bit 8*(i/4) + i%4 of word j.
+    uint32_t vis[2] = {0, 0};
+    if (!full) {
+      const uint64_t v = visible_bits(p0, t, a.window, a.sinks) >> (4 * half);
+      vis[0] = (uint32_t)v, vis[1] = (uint32_t)(v >> 32);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          s[j][i] = __uint_as_float(
+              bit_select(bit_mask(vis[j], 8 * (i >> 2) + (i & 3)), __float_as_uint(s[j][i]), 0xFF800000u));
+    }
+    float mx = fmaxf(s[0][0], s[1][0]);
+#pragma unroll
+    for (int i = 1; i < 16; ++i) mx = fmaxf(fmaxf(mx, s[0][i]), s[1][i]);
+    {
+      const uint32_t u = __float_as_uint(mx);
+      auto x = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+      mx = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])) * a.scale_log2;
+    }
+    if (ballot(mx > m + kSlack)) {
+      const float mn = fmaxf(m, mx);
+      const float f = exp2_fast(m - finite_max(mn));
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) acc[d] *= f;
+      m = mn;
+    }
+    const float mf = finite_max(m);
+    u32x4_t pf[4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float p[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) p[i] = exp2_fast(__builtin_fmaf(s[j][i], a.scale_log2, -mf));
+      float x = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) x += (p[i] + p[i + 1]) + (p[i + 2] + p[i + 3]);
+      l += x;
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+        pf[2 * j + g] = u32x4_t{T::pack(p[8 * g], p[8 * g + 1]), T::pack(p[8 * g + 2], p[8 * g + 3]),
+                                T::pack(p[8 * g + 4], p[8 * g + 5]), T::pack(p[8 * g + 6], p[8 * g + 7])};
+    }
+    // Infinities and NaN in V at positions that only some rows see: 0 * inf is
+    // NaN, so those tiles go a way of their own.
+    bool fix = false;
+    if (!full) {
+      uint32_t bad = 0;
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          const u32x4_t v = v_frag(vt, 16 * g, d);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) bad |= nonfinite_pair<T>(v[i]);
+        }
+      fix = ballot(bad != 0) != 0;
+      asm volatile("" ::: "memory");  // the products read V again: nothing of it is kept
+    }
+    if (!fix) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int d = 0; d < DT; ++d) acc[d] = mfma32<T>(v_frag(vt, 16 * g, d), pf[g], acc[d]);
+    } else {
+#pragma unroll 1
+      for (int g = 0; g < 4; ++g) {
+        u32x4_t see, pg;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w = (g < 2 ? vis[0] : vis[1]) >> (16 * (g & 1));
+          const int k = 2 * i, at = 8 * (k >> 2) + (k & 3);
+          see[i] = (bit_mask(w, at) & T::kOne) | (bit_mask(w, at + 1) & (T::kOne << 16));
+          pg[i] = g == 0 ? pf[0][i] : g == 1 ? pf[1][i] : g == 2 ? pf[2][i] : pf[3][i];
+        }
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          const u32x4_t v = v_frag(vt, 16 * g, d);
+          u32x4_t clean, marks;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t x, y;
+            split_nonfinite<T>(v[i], x, y);
+            clean[i] = x, marks[i] = y;
+          }
+          acc[d] = mfma32<T>(clean, pg, acc[d]);
+          f32x16_t n;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) n[i] = 0.f;
+          n = mfma32<T>(marks, see, n);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[d][i] += nonfinite_term(n[i]);
+          __builtin_amdgcn_sched_barrier(0);  // one channel tile at a time: this path is rare, its registers are not
+        }
+      }
+    }
+  };
+
+  int page = 0, i = next_tile(0, page), buf = 0;
+  if (i < tiles) {
+    issue(page, 0);
+    settle(0);
+  }
+  while (i < tiles) {
+    // The buffer is complete in every wave, and the other one has been read.
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    int page1 = 0;
+    const int i1 = next_tile(i + 1, page1);
+    if (i1 < tiles) issue(page1, buf ^ 1);
+    const int p0 = page_pos(i) * kPage;
+    // Does the wave see any of it?
+    if (p0 <= w_last && (p0 + kPage - 1 > w_first - a.window || p0 < a.sinks)) compute(p0, buf);
+    if (i1 < tiles) settle(buf ^ 1);
+    i = i1, buf ^= 1;
+  }
+
+  {
+    const uint32_t u = __float_as_uint(l);
+    auto x = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    l = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  typename T::elem* dst = static_cast<typename T::elem*>(a.out) + (int64_t)(row0 + rr) * a.ld_out + (h0 + hh) * D;
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int g = 0; g < 4; g += 2) {
+      // Channels 8g + 4*half + 0..3 of the tile and the same of g + 1: the
+      // halves exchange so that each stores 8 channels at once.
+      uint32_t w[2][2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          w[e][k] = T::pack(acc[d][4 * (g + e) + 2 * k] * inv, acc[d][4 * (g + e) + 2 * k + 1] * inv);
+      auto x = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
+      auto y = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
+      if (ok) *reinterpret_cast<u32x4_t*>(dst + 32 * d + 8 * (g + half)) = u32x4_t{x[0], y[0], x[1], y[1]};
+    }
+  if (ok && half == 0 && a.lse != nullptr)
+    a.lse[(int64_t)(row0 + rr) * a.hq + h0 + hh] = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+template <class T, bool FP4>
+int launch_attn_prefill(const PrefillArgs& a, int d, uint32_t grid, hipStream_t stream) {
+  if (d == 64)
+    hipLaunchKernelGGL((attn_prefill_kernel<T, FP4, 64, 8>), dim3(grid), dim3(512), 0, stream, a);
+  else if (d == 128)
+    hipLaunchKernelGGL((attn_prefill_kernel<T, FP4, 128, 8>), dim3(grid), dim3(512), 0, stream, a);
+  else
+    hipLaunchKernelGGL((attn_prefill_kernel<T, FP4, 256, 4>), dim3(grid), dim3(256), 0, stream, a);
+  return hipGetLastError() == hipSuccess ? BS_OK : BS_ERR_LAUNCH;
+}
+
+// (row, head) pairs of a workgroup.
+inline int prefill_cols(int d) { return d == 256 ? 128 : 256; }
+
+}  // namespace bs

@@ -1,0 +1,8 @@
+// attn_prefill_f16_kv4.hip - the prefill attention kernels for f16 queries over the 4-bit cache.
+#include "attn_prefill.h"
+
+namespace bs {
+
+template int launch_attn_prefill<F16, true>(const PrefillArgs&, int, uint32_t, hipStream_t);
+
+}  // namespace bs

@@ -329,6 +329,9 @@ WINDOW_CASES = [  # kind, form, d, hq, hkv, contexts, rows, max_rows, window, si
     ("bf16", "kv4", 128, 8, 2, [500, 90], [300, 70], 300, 129, 4),
     ("f16", "kv4", 128, 12, 4, [260], [200], 200, 100, 13),
     ("bf16", "kv16", 64, 8, 2, [400, 33], [260, 33], 260, 150, 2),
+    ("bf16", "kv4", 64, 16, 2, [400, 33], [260, 33], 260, 150, 2),
+    ("bf16", "kv4", 256, 4, 2, [200], [150], 150, 80, 4),
+    ("f16", "kv16", 256, 4, 4, [200], [150], 150, 80, 4),
     ("f16", "kv4", 64, 4, 1, [300], [290], 290, 70, 4),
     ("bf16", "kv16", 256, 4, 2, [200], [150], 150, 80, 4),
     ("f16", "kv4", 256, 2, 1, [200], [150], 150, 80, 4),
