@@ -63,17 +63,16 @@ __device__ __forceinline__ uint32_t bit_select(uint32_t sel, uint32_t a, uint32_
 // All ones if bit i of x is set, else 0.
 __device__ __forceinline__ uint32_t bit_mask(uint32_t x, int i) { return (uint32_t)__builtin_amdgcn_sbfe((int)x, i, 1); }
 
-// A pair with infinities and NaN replaced by zeros (clean), and marks for
-// them: 1 for +inf, 64 for -inf, 65 for NaN, exact in both 16-bit types.  This
-// and what follows are written without comparisons: their lane masks, dozens
-// of them at once, would not fit the scalar registers.
+// Marks for the infinities and NaN of a pair, 0 for other values: 1 for +inf,
+// 64 for -inf, 65 for NaN, exact in both 16-bit types.  This and what follows
+// are written without comparisons: their lane masks, dozens of them at once,
+// would not fit the scalar registers.
 template <class T>
-__device__ __forceinline__ void split_nonfinite(uint32_t x, uint32_t& clean, uint32_t& marks) {
+__device__ __forceinline__ uint32_t nonfinite_marks(uint32_t x) {
   constexpr uint32_t mant = 0x7FFF7FFFu & ~T::kExpMask, both = 0x00010001u;
-  const uint32_t bad = spread_halves(nonfinite_pair<T>(x));
   const uint32_t nan = spread_halves(((x & mant) + 0x7FFF7FFFu) & 0x80008000u);
-  clean = x & ~bad;
-  marks = bad & bit_select(nan, T::k65 * both, bit_select(spread_halves(x), T::k64 * both, T::kOne * both));
+  return spread_halves(nonfinite_pair<T>(x)) &
+         bit_select(nan, T::k65 * both, bit_select(spread_halves(x), T::k64 * both, T::kOne * both));
 }
 
 // What visible infinities and NaN add to a sum, from the sum of the marks of
@@ -96,6 +95,89 @@ __device__ __forceinline__ uint64_t visible_bits(int p0, int t, int window, int 
 __device__ __forceinline__ void wave_fence() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_wave_barrier();
+}
+
+// A workspace region that splits exchange results through: relaxed
+// device-scope accesses only (performed at the device's coherence point, not
+// in an XCD's L2), so no cache write-back is needed.
+struct SplitBuffer {
+  __amdgpu_buffer_rsrc_t rs;
+  __device__ __forceinline__ SplitBuffer(float* p, uint32_t bytes)
+      : rs(__builtin_amdgcn_make_buffer_rsrc(p, (short)0, bytes, 0x00020000)) {}
+  static constexpr int kSc1 = 16;
+  __device__ __forceinline__ void store4(uint32_t off, const f32x4_t& v) const {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), rs, off, 0, kSc1);
+  }
+  __device__ __forceinline__ void store2(uint32_t off, float x, float y) const {
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{__float_as_uint(x), __float_as_uint(y)}, rs, off, 0, kSc1);
+  }
+  __device__ __forceinline__ f32x4_t load4(uint32_t off) const {
+    return __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, kSc1));
+  }
+  __device__ __forceinline__ float2 load2(uint32_t off) const {
+    const u32x2_t v = __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, kSc1);
+    return make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+  }
+};
+
+// Called by every lane of a workgroup whose partial result is stored: true in
+// the workgroup that is the last of its group's nsplit to arrive (its counter
+// is then zero again).  `arrived` is in LDS.
+__device__ __forceinline__ bool last_of_group(uint32_t* counters, int group, int nsplit, int tid, uint32_t& arrived) {
+  __builtin_amdgcn_s_waitcnt(0);  // this lane's stores have been performed
+  __syncthreads();
+  if (tid == 0) {
+    arrived = __hip_atomic_fetch_add(&counters[group], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (arrived == (uint32_t)nsplit - 1)
+      __hip_atomic_store(&counters[group], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  return arrived == (uint32_t)nsplit - 1;
+}
+
+// Joins the partial results of nsplit workgroups in split order.  A partial
+// (step bytes) holds [cols][D] sums, then [cols] (maximum, sum).  A thread takes
+// 4 channels of a column at a time; BATCH splits' loads are in flight together
+// (past the last split: its own again, with weight 0).
+template <int D, int THREADS, class F>
+__device__ __forceinline__ void join_splits(const SplitBuffer& sb, uint32_t first, uint32_t step, int cols, int ncols,
+                                            int nsplit, int tid, F write) {
+  constexpr int BATCH = 16;
+  for (int u = tid; u < ncols * (D / 4); u += THREADS) {
+    const int cc = u / (D / 4), d = (u % (D / 4)) * 4;
+    const uint32_t ml = first + (cols * D + 2 * cc) * 4, oo = first + (cc * D + d) * 4;
+    float mm = -INFINITY, ll = 0.f;
+    f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < nsplit; i += BATCH) {
+      float2 x[BATCH];
+      f32x4_t y[BATCH];
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        const uint32_t at = min(i + k, nsplit - 1) * step;
+        x[k] = sb.load2(ml + at), y[k] = sb.load4(oo + at);
+      }
+      float nm = mm;
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) nm = fmaxf(nm, x[k].x);
+      const float nf = finite_max(nm), f = exp2_fast(mm - nf);
+      ll *= f, o *= f;
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        const float g = i + k < nsplit ? exp2_fast(x[k].x - nf) : 0.f;
+        ll += x[k].y * g, o += y[k] * g;
+      }
+      mm = nm;
+    }
+    write(cc, d, o, mm, ll);
+  }
+}
+
+// Stores 4 channels of a joined column and (with the first) its lse.
+template <class T>
+__device__ __forceinline__ void write_joined(typename T::elem* dst, int d, const f32x4_t& o, float m, float l, float* lse) {
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  *reinterpret_cast<u32x2_t*>(dst + d) = u32x2_t{T::pack(o.x * inv, o.y * inv), T::pack(o.z * inv, o.w * inv)};
+  if (lse != nullptr && d == 0) *lse = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 }  // namespace bs

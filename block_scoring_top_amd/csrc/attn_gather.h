@@ -86,31 +86,16 @@ __device__ __forceinline__ void load_dwords(uint32_t (&dst)[N], const uint8_t* p
   }
 }
 
-// A workspace region that splits exchange results through: relaxed
-// device-scope accesses only (performed at the device's coherence point, not
-// in an XCD's L2), so no cache write-back is needed.
-struct SplitBuffer {
-  __amdgpu_buffer_rsrc_t rs;
-  __device__ __forceinline__ SplitBuffer(float* p, uint32_t bytes)
-      : rs(__builtin_amdgcn_make_buffer_rsrc(p, (short)0, bytes, 0x00020000)) {}
-  static constexpr int kSc1 = 16;
-  __device__ __forceinline__ void store4(uint32_t off, const f32x4_t& v) const {
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), rs, off, 0, kSc1);
-  }
-  __device__ __forceinline__ void store2(uint32_t off, float x, float y) const {
-    __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{__float_as_uint(x), __float_as_uint(y)}, rs, off, 0, kSc1);
-  }
-  __device__ __forceinline__ f32x4_t load4(uint32_t off) const {
-    return __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, kSc1));
-  }
-  __device__ __forceinline__ float2 load2(uint32_t off) const {
-    const u32x2_t v = __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, kSc1);
-    return make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
-  }
-};
+// Waves a SIMD must hold: one where two would spill registers in the loop
+// (the 16-bit loads of two chunks take 256 registers at D = 256; one such wave
+// keeps 64 KiB in flight).  64 decode rows of 2,051 slots, D = 256, 16-bit
+// pool: 131 us with two, 60 us with one; 64 x 6 verify rows of a 4,096 window,
+// D = 128, two column tiles: 235 and 117 us.  The 4-bit kernels are better off
+// with two (the same verify rows: 65 against 92 us).
+constexpr int gather_waves(bool fp4, int d, int nt) { return nt * d == 256 && !fp4 ? 1 : 2; }
 
 template <class T, bool FP4, int D, int NT, bool WINDOW>
-__global__ __launch_bounds__(64 * kGaWaves, NT * D > 256 ? 1 : 2) void attn_gather_kernel(const GatherArgs a) {
+__global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_gather_kernel(const GatherArgs a) {
   typedef GatherRaw<FP4, D> Raw;
   constexpr int KS = D / 32;       // 32-channel steps of the score product
   constexpr int VD = D / 16;       // channels of the output per lane and accumulator row
@@ -163,11 +148,10 @@ __global__ __launch_bounds__(64 * kGaWaves, NT * D > 256 ? 1 : 2) void attn_gath
   } else {
     row0 = tile, nrows = 1;
     n = a.ld_slots;
-    if (a.count != nullptr) n = min(n, a.count[row0]);
-    n = max(n, 0);
   }
   const int chunks = (int)(((int64_t)n + kGaKeys - 1) / kGaKeys);
-  const int c0 = (int)((int64_t)chunks * split / a.nsplit), c1 = (int)((int64_t)chunks * (split + 1) / a.nsplit);
+  const int c0 = (int)((int64_t)chunks * split / a.nsplit);
+  int c1 = (int)((int64_t)chunks * (split + 1) / a.nsplit);
 
   // This lane's query vectors (column 16*nt + n16 of the tile).
   u32x4_t qf[NT][KS];
@@ -405,9 +389,8 @@ __global__ __launch_bounds__(64 * kGaWaves, NT * D > 256 ? 1 : 2) void attn_gath
           u32x4_t clean, marks;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            uint32_t x, y;
-            split_nonfinite<T>(f[e][i], x, y);
-            clean[i] = x, marks[i] = y;
+            clean[i] = f[e][i] & ~spread_halves(nonfinite_pair<T>(f[e][i]));
+            marks[i] = nonfinite_marks<T>(f[e][i]);
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -431,11 +414,22 @@ __global__ __launch_bounds__(64 * kGaWaves, NT * D > 256 ? 1 : 2) void attn_gath
   // this one's products, its slots one chunk earlier still.
   {
     int c = c0 + wave;
+    // A list's splits go by its storage, so that its first entries are on
+    // their way before its count is known.
+    int sl0 = load_slot(c), sl = load_slot(c + kGaWaves);
+    if constexpr (!WINDOW) {
+      if (a.count != nullptr) {
+        n = max(min(n, a.count[row0]), 0);
+        c1 = (int)min((int64_t)c1, ((int64_t)n + kGaKeys - 1) / kGaKeys);
+        const int i = c * kGaKeys + (lane & 31);
+        sl0 = i < n ? sl0 : -1;
+        sl = i + kGaWaves * kGaKeys < n ? sl : -1;
+      }
+    }
     if (c < c1) {
       Raw r0, r1;
       uint32_t k0, k1;
-      fetch(load_slot(c), r0, k0);
-      int sl = load_slot(c + kGaWaves);
+      fetch(sl0, r0, k0);
       auto step = [&](Raw& cur, uint32_t& kc, Raw& nxt, uint32_t& kn) {
         if (c + kGaWaves < c1) {
           fetch(sl, nxt, kn);
@@ -499,6 +493,7 @@ __global__ __launch_bounds__(64 * kGaWaves, NT * D > 256 ? 1 : 2) void attn_gath
     if (a.nsplit == 1) {
       finish(nt, o, mm, ll);
     } else {
+      if (nt * 16 + col >= nrows * a.gb) continue;  // no such column
       const uint32_t base = blockIdx.x * slot_floats * 4;
 #pragma unroll
       for (int d = 0; d < VD; d += 4)
@@ -508,40 +503,17 @@ __global__ __launch_bounds__(64 * kGaWaves, NT * D > 256 ? 1 : 2) void attn_gath
   }
   if (a.nsplit == 1) return;
 
-  // Every store of this lane is performed before the workgroup arrives.
-  __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();
-  if (tid == 0)
-    arrived = __hip_atomic_fetch_add(&a.counters[group], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __syncthreads();
-  if (arrived != (uint32_t)a.nsplit - 1) return;
-  if (tid == 0) __hip_atomic_store(&a.counters[group], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  const uint32_t first = (uint32_t)group * a.nsplit * slot_floats * 4;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    if (nt * 16 >= nrows * a.gb) break;
-    const uint32_t ml = first + (COLS * D + 2 * (nt * 16 + col)) * 4, oo = first + ((nt * 16 + col) * D + part * VD) * 4;
-    float mm = -INFINITY, ll = 0.f, o[VD];
-#pragma unroll
-    for (int d = 0; d < VD; ++d) o[d] = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < a.nsplit; ++i) {
-      const float2 x = sb.load2(ml + i * slot_floats * 4);
-      const float nm = fmaxf(mm, x.x);
-      const float f = exp2_fast(mm - finite_max(nm)), g = exp2_fast(x.x - finite_max(nm));
-      ll = ll * f + x.y * g;
-#pragma unroll
-      for (int d = 0; d < VD; d += 4) {
-        const f32x4_t y = sb.load4(oo + i * slot_floats * 4 + d * 4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[d + e] = o[d + e] * f + y[e] * g;
-      }
-      mm = nm;
-    }
-    finish(nt, o, mm, ll);
-  }
+  if (!last_of_group(a.counters, group, a.nsplit, tid, arrived)) return;
+  join_splits<D, 64 * kGaWaves>(sb, (uint32_t)group * a.nsplit * slot_floats * 4, slot_floats * 4, COLS,
+                                min(nrows * a.gb, COLS), a.nsplit, tid, [&](int cc, int d, const f32x4_t& o, float mm, float ll) {
+    const int rr = cc / a.gb, hh = cc % a.gb;
+    if (hh < heads)
+      write_joined<T>(static_cast<typename T::elem*>(a.out) + (int64_t)(row0 + rr) * a.ld_out + (h0 + hh) * D, d, o, mm, ll,
+                      a.lse == nullptr ? nullptr : a.lse + (int64_t)(row0 + rr) * a.hq + h0 + hh);
+  });
 }
 
+// nt: column tiles of a workgroup, 1 or (head_dim up to 128: registers) 2.
 template <class T, bool FP4>
 int launch_attn_gather(const GatherArgs& a, int d, int nt, bool window, uint32_t blocks, hipStream_t stream) {
   auto go = [&](auto dim, auto tiles, auto win) {
@@ -555,10 +527,9 @@ int launch_attn_gather(const GatherArgs& a, int d, int nt, bool window, uint32_t
       go(dim, tiles, std::false_type());
   };
   auto by_tiles = [&](auto dim) {
-    if (nt == 1)
-      by_window(dim, std::integral_constant<int, 1>());
-    else
-      by_window(dim, std::integral_constant<int, 2>());
+    if constexpr (decltype(dim)::value <= 128)
+      if (nt == 2) return by_window(dim, std::integral_constant<int, 2>());
+    by_window(dim, std::integral_constant<int, 1>());
   };
   if (d == 64)
     by_tiles(std::integral_constant<int, 64>());

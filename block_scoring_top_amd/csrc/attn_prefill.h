@@ -48,7 +48,25 @@ struct PrefillArgs {
   void* out;
   int64_t ld_out;
   float* lse;
-  uint32_t blocks;
+  uint32_t groups, nsplit;  // row blocks times head blocks; parts that a block's pages are split into
+  float* partial;           // nsplit > 1: per (group, part) [cols][D] sums, then [cols] (maximum, sum)
+};
+
+// Which rows and heads a group is.  False: none.
+struct PrefillGroup {
+  int b, kvh, h0, heads, row0, nrows;
+  __device__ __forceinline__ bool locate(const PrefillArgs& a, uint32_t group) {
+    const int i_tile = group % a.tiles_per_req, rest = group / a.tiles_per_req;
+    const int hb = rest % (a.hkv * a.hblocks), G = a.hq / a.hkv, hin = (hb % a.hblocks) * a.gb;
+    b = rest / (a.hkv * a.hblocks), kvh = hb / a.hblocks;
+    heads = min(a.gb, G - hin), h0 = kvh * G + hin;
+    const int ra = max(a.req_row_ptr[b], 0);
+    const int rb = (int)min((int64_t)min(a.req_row_ptr[b + 1], a.num_rows), (int64_t)ra + a.max_rows);
+    const int64_t first = (int64_t)ra + (int64_t)i_tile * a.rows_per_tile;
+    if (first >= rb) return false;
+    row0 = (int)first, nrows = min(a.rows_per_tile, rb - row0);
+    return true;
+  }
 };
 
 template <class T>
@@ -70,7 +88,7 @@ __device__ __forceinline__ u32x2_t lds_read_tr(const uint8_t* p) {
 }
 
 template <class T, bool FP4, int D, int NW>
-__global__ __launch_bounds__(64 * NW, NW / 4) void attn_prefill_kernel(const PrefillArgs a) {
+__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prefill_kernel(const PrefillArgs a) {
   constexpr int ROW = D * 2;                // bytes of a key in LDS
   constexpr int NS = D / 8;                 // its 16-byte slices
   constexpr int KSWZ = NS < 16 ? NS - 1 : 15, VSWZ = NS < 16 ? NS - 1 : 15;
@@ -80,19 +98,14 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_prefill_kernel(const Pre
 
   const int tid = threadIdx.x, lane = tid & 63, n32 = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  // Block b runs on XCD b mod 8: consecutive ids on one XCD.
-  const uint32_t per = gridDim.x / 8, id = (blockIdx.x % 8) * per + blockIdx.x / 8;
-  if (id >= a.blocks) return;
-  const int i_tile = id % a.tiles_per_req, rest = id / a.tiles_per_req;
-  const int hb = rest % (a.hkv * a.hblocks), b = rest / (a.hkv * a.hblocks);
-  const int kvh = hb / a.hblocks, G = a.hq / a.hkv, hin = (hb % a.hblocks) * a.gb;
-  const int heads = min(a.gb, G - hin), h0 = kvh * G + hin;
-
-  const int ra = max(a.req_row_ptr[b], 0);
-  const int rb = (int)min((int64_t)min(a.req_row_ptr[b + 1], a.num_rows), (int64_t)ra + a.max_rows);
-  const int64_t first = (int64_t)ra + (int64_t)i_tile * a.rows_per_tile;
-  if (first >= rb) return;
-  const int row0 = (int)first, nrows = min(a.rows_per_tile, rb - row0);
+  // Block b runs on XCD b mod 8: eight consecutive ids on one XCD (their rows
+  // share most of their window in its L2), the next eight on the next.
+  const uint32_t id = blockIdx.x / 64 * 64 + blockIdx.x % 8 * 8 + blockIdx.x / 8 % 8;
+  if (id >= a.groups * a.nsplit) return;
+  const uint32_t group = id % a.groups, split = id / a.groups;
+  PrefillGroup w;
+  if (!w.locate(a, group)) return;
+  const int b = w.b, kvh = w.kvh, h0 = w.h0, heads = w.heads, row0 = w.row0, nrows = w.nrows;
 
   // Positions: of the workgroup's rows, of the wave's, of the lane's.
   int lo = 0x7FFFFFFF, hi = -1;
@@ -116,7 +129,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_prefill_kernel(const Pre
   const int last = (int)min((int64_t)min(tmax, 0x7FFFFF00), (int64_t)a.pt_stride * kPage - 1);
   const int ns = max(0, min(a.sinks, last + 1)), sink_pages = (ns + kPage - 1) / kPage;
   const int wp0 = max(max(0, tmin - a.window + 1) / kPage, sink_pages);
-  const int tiles = last < 0 ? 0 : sink_pages + max(0, last / kPage - wp0 + 1);
+  const int all_tiles = last < 0 ? 0 : sink_pages + max(0, last / kPage - wp0 + 1);
+  const int tile0 = (int)((int64_t)all_tiles * split / a.nsplit), tiles = (int)((int64_t)all_tiles * (split + 1) / a.nsplit);
   const int32_t* ptab = a.page_table + (int64_t)b * a.pt_stride;
 
   u32x4_t qf[KS];
@@ -218,8 +232,14 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_prefill_kernel(const Pre
     return u32x4_t{x.x, x.y, y.x, y.y};
   };
 
-  auto compute = [&](int p0, int buf) {
-    const bool full = p0 + kPage - 1 <= w_all && (p0 > w_last - a.window || p0 + kPage - 1 < a.sinks);
+  // Does every row of the wave see all of the page at p0?  Any of it?
+  auto all_seen = [&](int p0) {
+    return p0 + kPage - 1 <= w_all && (p0 > w_last - a.window || p0 + kPage - 1 < a.sinks);
+  };
+  auto any_seen = [&](int p0) { return p0 <= w_last && (p0 + kPage - 1 > w_first - a.window || p0 < a.sinks); };
+
+  auto compute = [&](auto masked_c, int p0, int buf) {
+    constexpr bool MASKED = decltype(masked_c)::value;
     const uint8_t *kt = kv[buf][0], *vt = kv[buf][1];
     f32x16_t s[2];
 #pragma unroll
@@ -235,7 +255,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_prefill_kernel(const Pre
     // Bits of the lane's keys that its row sees: key 32*j + 8*(i/4) +
     // 4*half + i%4 at bit 8*(i/4) + i%4 of word j.
     uint32_t vis[2] = {0, 0};
-    if (!full) {
+    if constexpr (MASKED) {
       const uint64_t v = visible_bits(p0, t, a.window, a.sinks) >> (4 * half);
       vis[0] = (uint32_t)v, vis[1] = (uint32_t)(v >> 32);
 #pragma unroll
@@ -278,82 +298,94 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_prefill_kernel(const Pre
                                 T::pack(p[8 * g + 4], p[8 * g + 5]), T::pack(p[8 * g + 6], p[8 * g + 7])};
     }
     // Infinities and NaN in V at positions that only some rows see: 0 * inf is
-    // NaN, so those tiles go a way of their own.
-    bool fix = false;
-    if (!full) {
-      uint32_t bad = 0;
+    // NaN, so in masked pages they are taken out of the product, and what the
+    // rows that see them must show is added after it.
+    uint32_t bad = 0;
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
+    for (int g = 0; g < 4; ++g)
 #pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          const u32x4_t v = v_frag(vt, 16 * g, d);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) bad |= nonfinite_pair<T>(v[i]);
-        }
-      fix = ballot(bad != 0) != 0;
-      asm volatile("" ::: "memory");  // the products read V again: nothing of it is kept
-    }
-    if (!fix) {
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-#pragma unroll
-        for (int d = 0; d < DT; ++d) acc[d] = mfma32<T>(v_frag(vt, 16 * g, d), pf[g], acc[d]);
-    } else {
-#pragma unroll 1
-      for (int g = 0; g < 4; ++g) {
-        u32x4_t see, pg;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t w = (g < 2 ? vis[0] : vis[1]) >> (16 * (g & 1));
-          const int k = 2 * i, at = 8 * (k >> 2) + (k & 3);
-          see[i] = (bit_mask(w, at) & T::kOne) | (bit_mask(w, at + 1) & (T::kOne << 16));
-          pg[i] = g == 0 ? pf[0][i] : g == 1 ? pf[1][i] : g == 2 ? pf[2][i] : pf[3][i];
-        }
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          const u32x4_t v = v_frag(vt, 16 * g, d);
-          u32x4_t clean, marks;
+      for (int d = 0; d < DT; ++d) {
+        u32x4_t v = v_frag(vt, 16 * g, d);
+        if constexpr (MASKED) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            uint32_t x, y;
-            split_nonfinite<T>(v[i], x, y);
-            clean[i] = x, marks[i] = y;
+            const uint32_t x = nonfinite_pair<T>(v[i]);
+            bad |= x, v[i] &= ~spread_halves(x);
           }
-          acc[d] = mfma32<T>(clean, pg, acc[d]);
-          f32x16_t n;
+        }
+        acc[d] = mfma32<T>(v, pf[g], acc[d]);
+      }
+    if constexpr (MASKED) {
+      if (ballot(bad != 0)) {
+#pragma unroll 1
+        for (int g = 0; g < 4; ++g) {
+          const uint32_t w = (g < 2 ? vis[0] : vis[1]) >> (16 * (g & 1));
+          u32x4_t see;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) n[i] = 0.f;
-          n = mfma32<T>(marks, see, n);
+          for (int i = 0; i < 4; ++i) {
+            const int k = 2 * i, at = 8 * (k >> 2) + (k & 3);
+            see[i] = (bit_mask(w, at) & T::kOne) | (bit_mask(w, at + 1) & (T::kOne << 16));
+          }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[d][i] += nonfinite_term(n[i]);
-          __builtin_amdgcn_sched_barrier(0);  // one channel tile at a time: this path is rare, its registers are not
+          for (int d = 0; d < DT; ++d) {
+            const u32x4_t v = v_frag(vt, 16 * g, d);
+            u32x4_t marks;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) marks[i] = nonfinite_marks<T>(v[i]);
+            f32x16_t n;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) n[i] = 0.f;
+            n = mfma32<T>(marks, see, n);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[d][i] += nonfinite_term(n[i]);
+            __builtin_amdgcn_sched_barrier(0);  // one channel tile at a time: this path is rare, its registers are not
+          }
         }
       }
     }
   };
 
-  int page = 0, i = next_tile(0, page), buf = 0;
+  int page = 0, i = next_tile(tile0, page), buf = 0;
   if (i < tiles) {
     issue(page, 0);
     settle(0);
   }
-  while (i < tiles) {
+  auto step = [&](auto masked_c) {
     // The buffer is complete in every wave, and the other one has been read.
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     int page1 = 0;
     const int i1 = next_tile(i + 1, page1);
     if (i1 < tiles) issue(page1, buf ^ 1);
     const int p0 = page_pos(i) * kPage;
-    // Does the wave see any of it?
-    if (p0 <= w_last && (p0 + kPage - 1 > w_first - a.window || p0 < a.sinks)) compute(p0, buf);
+    if (!decltype(masked_c)::value || any_seen(p0)) compute(masked_c, p0, buf);
     if (i1 < tiles) settle(buf ^ 1);
     i = i1, buf ^= 1;
+  };
+  // Loops of their own for the pages without and with a mask: joined in one,
+  // the accumulators were copied at each join (128 moves a page).
+  while (i < tiles) {
+    while (i < tiles && all_seen(page_pos(i) * kPage)) step(std::false_type());
+    while (i < tiles && !all_seen(page_pos(i) * kPage)) step(std::true_type());
   }
 
   {
     const uint32_t u = __float_as_uint(l);
     auto x = __builtin_amdgcn_permlane32_swap(u, u, false, false);
     l = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+  }
+  if (a.nsplit > 1) {
+    constexpr int COLS = 32 * NW;
+    float* part = a.partial + ((uint64_t)group * a.nsplit + split) * (COLS * (D + 2));
+    if (ok) {
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<f32x4_t*>(part + col * D + 32 * d + 8 * g + 4 * half) =
+              f32x4_t{acc[d][4 * g], acc[d][4 * g + 1], acc[d][4 * g + 2], acc[d][4 * g + 3]};
+      if (half == 0) *reinterpret_cast<f32x2_t*>(part + COLS * D + 2 * col) = f32x2_t{m, l};
+    }
+    return;
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   typename T::elem* dst = static_cast<typename T::elem*>(a.out) + (int64_t)(row0 + rr) * a.ld_out + (h0 + hh) * D;
@@ -377,18 +409,54 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attn_prefill_kernel(const Pre
     a.lse[(int64_t)(row0 + rr) * a.hq + h0 + hh] = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-template <class T, bool FP4>
-int launch_attn_prefill(const PrefillArgs& a, int d, uint32_t grid, hipStream_t stream) {
-  if (d == 64)
-    hipLaunchKernelGGL((attn_prefill_kernel<T, FP4, 64, 8>), dim3(grid), dim3(512), 0, stream, a);
-  else if (d == 128)
-    hipLaunchKernelGGL((attn_prefill_kernel<T, FP4, 128, 8>), dim3(grid), dim3(512), 0, stream, a);
-  else
-    hipLaunchKernelGGL((attn_prefill_kernel<T, FP4, 256, 4>), dim3(grid), dim3(256), 0, stream, a);
-  return hipGetLastError() == hipSuccess ? BS_OK : BS_ERR_LAUNCH;
+// Joins the parts of every group, in their order: a lane takes 4 channels of a
+// column.  A launch of its own: one workgroup a group, the last of its parts
+// to arrive, would read its 66 KiB a part alone (50 rows over 64 pages in 16
+// parts: 40 us in place of 22).
+template <class T, int D, int COLS>
+__global__ __launch_bounds__(256) void attn_join_kernel(const PrefillArgs a) {
+  constexpr int PIECES = COLS * D / 4 / 256;
+  const uint32_t group = blockIdx.x / PIECES, u = blockIdx.x % PIECES * 256 + threadIdx.x;
+  PrefillGroup w;
+  if (!w.locate(a, group)) return;
+  const int col = u / (D / 4), d = u % (D / 4) * 4, rr = col / a.gb, hh = col % a.gb;
+  if (rr >= w.nrows || hh >= w.heads) return;
+  const float* part = a.partial + (uint64_t)group * a.nsplit * (COLS * (D + 2));
+  float m = -INFINITY, l = 0.f;
+  f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+  for (uint32_t i = 0; i < a.nsplit; ++i, part += COLS * (D + 2)) {
+    const f32x2_t x = *reinterpret_cast<const f32x2_t*>(part + COLS * D + 2 * col);
+    const f32x4_t y = *reinterpret_cast<const f32x4_t*>(part + col * D + d);
+    const float nm = fmaxf(m, x.x), nf = finite_max(nm), f = exp2_fast(m - nf), g = exp2_fast(x.x - nf);
+    l = l * f + x.y * g, o = o * f + y * g, m = nm;
+  }
+  write_joined<T>(static_cast<typename T::elem*>(a.out) + (int64_t)(w.row0 + rr) * a.ld_out + (w.h0 + hh) * D, d, o, m, l,
+                  a.lse == nullptr ? nullptr : a.lse + (int64_t)(w.row0 + rr) * a.hq + w.h0 + hh);
 }
 
-// (row, head) pairs of a workgroup.
-inline int prefill_cols(int d) { return d == 256 ? 128 : 256; }
+template <class T, bool FP4>
+int launch_attn_prefill(const PrefillArgs& a, int d, int waves, uint32_t grid, hipStream_t stream) {
+  auto go = [&](auto dim, auto nw) {
+    constexpr int NW = decltype(nw)::value;
+    constexpr int D = decltype(dim)::value, COLS = 32 * NW;
+    hipLaunchKernelGGL((attn_prefill_kernel<T, FP4, D, NW>), dim3(grid), dim3(64 * NW), 0, stream, a);
+    if (a.nsplit > 1)
+      hipLaunchKernelGGL((attn_join_kernel<T, D, COLS>), dim3(a.groups * (COLS * D / 4 / 256)), dim3(256), 0, stream, a);
+  };
+  auto by_waves = [&](auto dim) {
+    if (waves == 8)
+      go(dim, std::integral_constant<int, 8>());
+    else
+      go(dim, std::integral_constant<int, 4>());
+  };
+  if (d == 64)
+    by_waves(std::integral_constant<int, 64>());
+  else if (d == 128)
+    by_waves(std::integral_constant<int, 128>());
+  else  // the registers hold one wave a SIMD
+    go(std::integral_constant<int, 256>(), std::integral_constant<int, 4>());
+  return hipGetLastError() == hipSuccess ? BS_OK : BS_ERR_LAUNCH;
+}
 
 }  // namespace bs

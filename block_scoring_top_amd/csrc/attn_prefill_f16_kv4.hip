@@ -3,6 +3,6 @@
 
 namespace bs {
 
-template int launch_attn_prefill<F16, true>(const PrefillArgs&, int, uint32_t, hipStream_t);
+template int launch_attn_prefill<F16, true>(const PrefillArgs&, int, int, uint32_t, hipStream_t);
 
 }  // namespace bs
