@@ -270,7 +270,7 @@ inline int check_attn_args(const void* q, int32_t dtype, int64_t ld_q, int32_t n
   if (q_heads % kv_heads != 0 || !std::isfinite(scale)) return BS_ERR_ARG;
   const int64_t qw = (int64_t)q_heads * head_dim, kvw = (int64_t)kv_heads * head_dim;
   if (qw > (1 << 20) || !row_stride_ok(ld_q, qw) || !row_stride_ok(ld_out, qw)) return BS_ERR_ARG;
-  if (cache_form == BS_KV_16 && !row_stride_ok(ld_cache, kvw)) return BS_ERR_ARG;
+  if (cache_form == BS_KV_16 && (!row_stride_ok(ld_cache, kvw) || ld_cache > (1 << 24))) return BS_ERR_ARG;
   if (num_rows == 0) return BS_OK;
   if (!q || !cache0 || !cache1 || !out) return BS_ERR_NULL;
   if (num_pages < 1) return BS_ERR_ARG;

@@ -10,6 +10,8 @@
 
 namespace bs {
 
+// How far (in log2) a score may exceed the running maximum before that moves.
+constexpr float kSlack = 8.f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <class F, int... I>
@@ -123,7 +125,7 @@ struct SplitBuffer {
 // Called by every lane of a workgroup whose partial result is stored: true in
 // the workgroup that is the last of its group's nsplit to arrive (its counter
 // is then zero again).  `arrived` is in LDS.
-__device__ __forceinline__ bool last_of_group(uint32_t* counters, int group, int nsplit, int tid, uint32_t& arrived) {
+__device__ __forceinline__ bool last_of_group(uint32_t* counters, uint32_t group, int nsplit, int tid, uint32_t& arrived) {
   __builtin_amdgcn_s_waitcnt(0);  // this lane's stores have been performed
   __syncthreads();
   if (tid == 0) {

@@ -20,8 +20,9 @@
 //     the B operand of a 32-key product whose key order is chosen to match.
 //     The A operand needs 8 keys of one channel: a lane loads D/16 channels
 //     of 8 keys, converts, and transposes pairs of keys with byte permutes;
-//   * one maximum and rescaling per chunk; the rescaling is skipped when no
-//     maximum of the wave grew;
+//   * the running maximum moves only when a score exceeds it by more than
+//     kSlack (in log2): the accumulators are hardly ever rescaled, and P stays
+//     below 2^kSlack, far inside FP32 and both 16-bit types;
 //   * P is rounded to the 16-bit operand type for the product (relative
 //     2^-9 in bf16, as the output's own rounding); its sum is of the FP32
 //     values.
@@ -52,13 +53,16 @@ struct GatherArgs {
   // a window
   const int32_t *page_table, *req_row_ptr, *row_pos;
   int32_t pt_stride, max_rows, rows_per_tile, tiles_per_req, window, sinks;
-  float scale_log2;
+  float scale_log2;  // of the scores, above 0
+  uint32_t flip;     // sign bits to turn in q: the scale was negative
   void* out;
   int64_t ld_out;
   float* lse;
   uint32_t* counters;  // one per group of splits, zero between calls
   float* partial;
   int32_t nsplit;
+  int32_t tiles;     // row tiles; xcd_rows: eight consecutive ones on one XCD
+  bool xcd_rows;
 };
 
 template <bool FP4, int D>
@@ -103,7 +107,7 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
   constexpr int OLD = D + 4;       // LDS row of the join, in floats
   __shared__ union {
     struct {
-      __attribute__((aligned(16))) int32_t slot[kGaWaves][kGaKeys];
+      __attribute__((aligned(16))) uint64_t at[kGaWaves][kGaKeys];  // byte offsets of a chunk's keys
       __attribute__((aligned(16))) uint8_t scale[kGaWaves][kGaKeys][D / 16];
     } st;
     struct {
@@ -115,8 +119,12 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
 
   const int tid = threadIdx.x, lane = tid & 63, n16 = lane & 15, qd = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int split = blockIdx.x % a.nsplit, group = blockIdx.x / a.nsplit;
-  const int hb = group % (a.hkv * a.hblocks), tile = group / (a.hkv * a.hblocks);
+  // Grid: row tiles, head blocks, splits; so the chip works on one kv head at a
+  // time, whose keys then come from a cache more often.
+  const int split = blockIdx.z, hb = blockIdx.y, bx = blockIdx.x;
+  const int tile = a.xcd_rows ? bx / 64 * 64 + bx % 8 * 8 + bx / 8 % 8 : bx;
+  if (tile >= a.tiles) return;
+  const uint32_t group = (uint32_t)hb * a.tiles + tile;
   const int kvh = hb / a.hblocks, G = a.hq / a.hkv, hin = (hb % a.hblocks) * a.gb;
   const int heads = min(a.gb, G - hin), h0 = kvh * G + hin;
 
@@ -149,9 +157,9 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
     row0 = tile, nrows = 1;
     n = a.ld_slots;
   }
-  const int chunks = (int)(((int64_t)n + kGaKeys - 1) / kGaKeys);
-  const int c0 = (int)((int64_t)chunks * split / a.nsplit);
-  int c1 = (int)((int64_t)chunks * (split + 1) / a.nsplit);
+  const uint32_t chunks = ((uint32_t)n + kGaKeys - 1) / kGaKeys, per = (chunks + a.nsplit - 1) / a.nsplit;
+  const int c0 = (int)min(per * split, chunks);
+  int c1 = (int)min(per * (split + 1), chunks);
 
   // This lane's query vectors (column 16*nt + n16 of the tile).
   u32x4_t qf[NT][KS];
@@ -165,7 +173,7 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       const u32x4_t x = *reinterpret_cast<const u32x4_t*>(src + 8 * ks);
-      qf[nt][ks] = ok ? x : u32x4_t{0, 0, 0, 0};
+      qf[nt][ks] = ok ? x ^ a.flip : u32x4_t{0, 0, 0, 0};
     }
     tcol[nt] = WINDOW && ok ? a.row_pos[row0 + rr] : -1;
   }
@@ -196,37 +204,33 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
   auto fetch = [&](int sl, Raw& r, uint32_t& mask) {
     const bool ok = sl >= 0 && sl < a.num_slots;
     mask = (uint32_t)ballot(ok);
-    sl = ok ? sl : 0;
+    // A key's byte offset is computed by one lane and read by those that load
+    // from it.
+    const uint32_t rec = FP4 ? (uint32_t)a.hkv * D : (uint32_t)a.ld_kv * 2;
+    const uint64_t at = (uint64_t)(uint32_t)(ok ? sl : 0) * rec;
     wave_fence();
-    if (lane < kGaKeys) sh.st.slot[wave][lane] = sl;
+    if (lane < kGaKeys) sh.st.at[wave][lane] = at;
     wave_fence();
-    const int32_t* ls = sh.st.slot[wave];
-    const int32_t ka = ls[n16], kb = ls[16 + n16];
-    const int4 va = reinterpret_cast<const int4*>(ls)[qd], vb = reinterpret_cast<const int4*>(ls)[4 + qd];
-    const int32_t vs[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
-    if constexpr (FP4) {
-      const uint32_t rec = (uint32_t)a.hkv * D;
-      const uint8_t* base = a.a + kvh * D;
-      load_dwords(r.k[0], base + (uint64_t)(uint32_t)ka * rec + qd * (D / 8));
-      load_dwords(r.k[1], base + (uint64_t)(uint32_t)kb * rec + qd * (D / 8));
-      if (lane < kGaKeys)
-        load_dwords(r.s, a.b + (uint64_t)(uint32_t)sl * ((uint32_t)a.hkv * (D / 16)) + kvh * (D / 16));
+    const uint64_t* ls = sh.st.at[wave];
+    const uint64_t ka = ls[n16], kb = ls[16 + n16];
+    uint64_t va[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint8_t* p = base + (uint64_t)(uint32_t)vs[j] * rec + D / 2 + n16 * (D / 32);
-        if constexpr (D == 64)
-          r.v[j][0] = *reinterpret_cast<const uint16_t*>(p);
-        else
-          load_dwords(r.v[j], p);
-      }
-    } else {
-      const int64_t rec = a.ld_kv * 2;
-      const uint8_t* kb0 = a.a + kvh * D * 2;
-      const uint8_t* vb0 = a.b + kvh * D * 2 + n16 * (D / 8);
-      load_dwords(r.k[0], kb0 + ka * rec + qd * (D / 2));
-      load_dwords(r.k[1], kb0 + kb * rec + qd * (D / 2));
+    for (int j = 0; j < 8; j += 2) {
+      const ulonglong2 x = reinterpret_cast<const ulonglong2*>(ls)[(j >> 2) * 8 + 2 * qd + (j >> 1 & 1)];
+      va[j] = x.x, va[j + 1] = x.y;
+    }
+    const uint8_t* kp = a.a + kvh * (FP4 ? D : 2 * D) + qd * (FP4 ? D / 8 : D / 2);
+    const uint8_t* vp = FP4 ? a.a + kvh * D + D / 2 + n16 * (D / 32) : a.b + kvh * 2 * D + n16 * (D / 8);
+    load_dwords(r.k[0], kp + ka);
+    load_dwords(r.k[1], kp + kb);
+    if constexpr (FP4)
+      if (lane < kGaKeys) load_dwords(r.s, a.b + kvh * (D / 16) + (at >> 4));
 #pragma unroll
-      for (int j = 0; j < 8; ++j) load_dwords(r.v[j], vb0 + vs[j] * rec);
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (FP4 && D == 64)
+        r.v[j][0] = *reinterpret_cast<const uint16_t*>(vp + va[j]);
+      else
+        load_dwords(r.v[j], vp + va[j]);
     }
   };
 
@@ -307,7 +311,7 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
     for (int nt = 0; nt < NT; ++nt) {
       float x[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = s[nt][j >> 2][j & 3] * a.scale_log2;
+      for (int j = 0; j < 8; ++j) x[j] = s[nt][j >> 2][j & 3];
       if (masked) {
         vis[nt] = have;
         if constexpr (WINDOW) {
@@ -321,18 +325,19 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
           x[j] = __uint_as_float(bit_select(bit_mask(vis[nt], j), __float_as_uint(x[j]), 0xFF800000u));
       }
       float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-      mx = fmaxf(m[nt], rows_max(mx));
-      if (ballot(mx > m[nt])) {
+      mx = rows_max(mx) * a.scale_log2;
+      if (ballot(mx > m[nt] + kSlack)) {
+        mx = fmaxf(m[nt], mx);
         const float f = exp2_fast(m[nt] - finite_max(mx));
         l[nt] *= f;
 #pragma unroll
         for (int d = 0; d < VD; ++d) acc[nt][d] *= f;
         m[nt] = mx;
       }
-      const float mf = finite_max(mx);
+      const float mf = finite_max(m[nt]);
       float p[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) p[j] = exp2_fast(x[j] - mf);
+      for (int j = 0; j < 8; ++j) p[j] = exp2_fast(__builtin_fmaf(x[j], a.scale_log2, -mf));
       l[nt] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
       pfr[nt] = u32x4_t{T::pack(p[0], p[1]), T::pack(p[2], p[3]), T::pack(p[4], p[5]), T::pack(p[6], p[7])};
     }
@@ -420,7 +425,7 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
     if constexpr (!WINDOW) {
       if (a.count != nullptr) {
         n = max(min(n, a.count[row0]), 0);
-        c1 = (int)min((int64_t)c1, ((int64_t)n + kGaKeys - 1) / kGaKeys);
+        c1 = min(c1, (n + kGaKeys - 1) / kGaKeys);
         const int i = c * kGaKeys + (lane & 31);
         sl0 = i < n ? sl0 : -1;
         sl = i + kGaWaves * kGaKeys < n ? sl : -1;
@@ -448,7 +453,7 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
   // part*VD .. +VD of its column.
   const int col = tid >> 4, part = tid & 15;
   const uint32_t slot_floats = COLS * (D + 2);
-  const SplitBuffer sb(a.partial, a.nsplit > 1 ? (uint32_t)(gridDim.x * slot_floats * 4u) : 0u);
+  const SplitBuffer sb(a.partial, a.nsplit > 1 ? (uint32_t)((uint32_t)a.tiles * gridDim.y * a.nsplit * slot_floats * 4u) : 0u);
   auto finish = [&](int nt, const float (&o)[VD], float mm, float ll) {
     const int cc = nt * 16 + col, rr = cc / a.gb, hh = cc % a.gb;
     if (rr >= nrows || hh >= heads) return;
@@ -494,7 +499,7 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
       finish(nt, o, mm, ll);
     } else {
       if (nt * 16 + col >= nrows * a.gb) continue;  // no such column
-      const uint32_t base = blockIdx.x * slot_floats * 4;
+      const uint32_t base = (group * a.nsplit + split) * slot_floats * 4;
 #pragma unroll
       for (int d = 0; d < VD; d += 4)
         sb.store4(base + ((nt * 16 + col) * D + part * VD + d) * 4, f32x4_t{o[d], o[d + 1], o[d + 2], o[d + 3]});
@@ -504,7 +509,7 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
   if (a.nsplit == 1) return;
 
   if (!last_of_group(a.counters, group, a.nsplit, tid, arrived)) return;
-  join_splits<D, 64 * kGaWaves>(sb, (uint32_t)group * a.nsplit * slot_floats * 4, slot_floats * 4, COLS,
+  join_splits<D, 64 * kGaWaves>(sb, group * a.nsplit * slot_floats * 4, slot_floats * 4, COLS,
                                 min(nrows * a.gb, COLS), a.nsplit, tid, [&](int cc, int d, const f32x4_t& o, float mm, float ll) {
     const int rr = cc / a.gb, hh = cc % a.gb;
     if (hh < heads)
@@ -515,10 +520,11 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
 
 // nt: column tiles of a workgroup, 1 or (head_dim up to 128: registers) 2.
 template <class T, bool FP4>
-int launch_attn_gather(const GatherArgs& a, int d, int nt, bool window, uint32_t blocks, hipStream_t stream) {
+int launch_attn_gather(const GatherArgs& a, int d, int nt, bool window, hipStream_t stream) {
+  const dim3 grid(a.xcd_rows ? (a.tiles + 63) / 64 * 64 : a.tiles, a.hkv * a.hblocks, a.nsplit);
   auto go = [&](auto dim, auto tiles, auto win) {
     hipLaunchKernelGGL((attn_gather_kernel<T, FP4, decltype(dim)::value, decltype(tiles)::value, decltype(win)::value>),
-                       dim3(blocks), dim3(64 * kGaWaves), 0, stream, a);
+                       grid, dim3(64 * kGaWaves), 0, stream, a);
   };
   auto by_window = [&](auto dim, auto tiles) {
     if (window)

@@ -33,8 +33,6 @@
 
 namespace bs {
 
-constexpr float kSlack = 8.f;
-
 struct PrefillArgs {
   const void* q;
   int64_t ld_q;

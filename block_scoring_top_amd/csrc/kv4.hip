@@ -96,10 +96,10 @@ __global__ __launch_bounds__(256) void kv4_store_kernel(const typename T::elem* 
                                                         uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   constexpr int kLanes = D / 8;
   const uint32_t half = (uint32_t)hkv * kLanes, per_row = 2 * half;
-  const uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x;
-  const uint32_t t = (uint32_t)(id / per_row);
+  const uint32_t id = blockIdx.x * 256 + threadIdx.x;  // a launch has at most 2^31 lanes
+  const uint32_t t = id / per_row;
   if (t >= (uint32_t)num_tok) return;  // whole rows: a group's 4 lanes leave together
-  uint32_t u = (uint32_t)(id - (uint64_t)t * per_row);
+  uint32_t u = id - t * per_row;
   const int which = u >= half;
   u -= which ? half : 0;
   const int32_t slot = slots[t];
@@ -124,10 +124,10 @@ __global__ __launch_bounds__(256) void kv4_load_kernel(const uint8_t* __restrict
                                                        typename T::elem* __restrict__ v, int64_t ld_k, int64_t ld_v) {
   constexpr int kLanes = D / 8;
   const uint32_t half = (uint32_t)hkv * kLanes, per_row = 2 * half;
-  const uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x;
-  const uint32_t t = (uint32_t)(id / per_row);
+  const uint32_t id = blockIdx.x * 256 + threadIdx.x;  // a launch has at most 2^31 lanes
+  const uint32_t t = id / per_row;
   if (t >= (uint32_t)n) return;
-  uint32_t u = (uint32_t)(id - (uint64_t)t * per_row);
+  uint32_t u = id - t * per_row;
   const int which = u >= half;
   u -= which ? half : 0;
   const int32_t slot = slots[t];

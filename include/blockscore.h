@@ -416,7 +416,7 @@ int idx_compress_store(const uint16_t* k_raw, int32_t num_tok, const int32_t* re
 enum bs_dtype { BS_BF16 = 0, BS_F16 = 1, BS_F32 = 2 };
 enum bs_kv_form {
   BS_KV_16 = 0, /* cache0, cache1: K and V pools of the queries' 16-bit type, [num_pages * 64] slots of
-                   [kv_heads][head_dim], ld_cache elements from a slot to the next (>= kv_heads * head_dim) */
+                   [kv_heads][head_dim], ld_cache elements from a slot to the next (kv_heads * head_dim .. 2^24) */
   BS_KV_4 = 1   /* cache0, cache1: codes and scales as kv4_store writes them; ld_cache is not used */
 };
 
