@@ -46,7 +46,8 @@ def _store_case(T, hkv, d, kind, pad, seed, fused):
 @pytest.mark.parametrize("T,hkv,d,kind,pad,fused", [
     (1, 1, 64, "bf16", 0, False), (1, 8, 256, "f32", 0, True), (3, 5, 64, "f16", 0, True), (64, 2, 128, "bf16", 0, True),
     (65, 3, 128, "f16", 7, False), (257, 1, 256, "bf16", 5, True), (1003, 5, 64, "f32", 11, True), (2050, 2, 128, "f32", 3, False),
-    (513, 7, 128, "bf16", 0, False)])
+    (513, 7, 128, "bf16", 0, False),
+    (16411, 4, 128, "f16", 0, False)])  # enough for the kernel's several-pieces form, and a part of one
 def test_store_and_load_match_the_definition(T, hkv, d, kind, pad, fused):
     say(f"kv4 T={T} hkv={hkv} d={d} {kind} pad={pad} fused={fused}")
     k, v, slots, pages = _store_case(T, hkv, d, kind, pad, T * 7 + hkv, fused)
