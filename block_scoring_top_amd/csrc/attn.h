@@ -41,6 +41,22 @@ __device__ __forceinline__ float rows_sum(float x) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
+// A row's sums of weights, relative to its running maximum: x of the weights in
+// FP32 (for lse), y of the weights as rounded for their product with V.  The
+// output is divided by y: the rounding of a weight that dominates its row then
+// cancels.  Over 52 drawn calls the outputs' error against 64 bits is 1.16
+// times that of an FP32 form rounded once (at most 1.33); with x in y's place
+// it was 1.19 (1.42), for 2% less time in the prefill kernel.
+typedef f32x2_t Sums;
+
+// sums += the rounding of 8 weights packed in p.
+template <class T>
+__device__ __forceinline__ float add_rounded(const u32x4_t& p, float sum) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sum = T::dot2(p[i], T::kOne * 0x00010001u, sum);
+  return sum;
+}
+
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 // A maximum to subtract: 0 in place of -inf, so that -inf scores give 0 and
 // not NaN.
@@ -110,15 +126,8 @@ struct SplitBuffer {
   __device__ __forceinline__ void store4(uint32_t off, const f32x4_t& v) const {
     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), rs, off, 0, kSc1);
   }
-  __device__ __forceinline__ void store2(uint32_t off, float x, float y) const {
-    __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{__float_as_uint(x), __float_as_uint(y)}, rs, off, 0, kSc1);
-  }
   __device__ __forceinline__ f32x4_t load4(uint32_t off) const {
     return __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, kSc1));
-  }
-  __device__ __forceinline__ float2 load2(uint32_t off) const {
-    const u32x2_t v = __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, kSc1);
-    return make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
   }
 };
 
@@ -138,7 +147,7 @@ __device__ __forceinline__ bool last_of_group(uint32_t* counters, uint32_t group
 }
 
 // Joins the partial results of nsplit workgroups in split order.  A partial
-// (step bytes) holds [cols][D] sums, then [cols] (maximum, sum).  A thread takes
+// (step bytes) holds [cols][D] products, then [cols] (maximum, sums, 0).  A thread takes
 // 4 channels of a column at a time; BATCH splits' loads are in flight together
 // (past the last split: its own again, with weight 0).
 template <int D, int THREADS, class F>
@@ -147,16 +156,16 @@ __device__ __forceinline__ void join_splits(const SplitBuffer& sb, uint32_t firs
   constexpr int BATCH = 16;
   for (int u = tid; u < ncols * (D / 4); u += THREADS) {
     const int cc = u / (D / 4), d = (u % (D / 4)) * 4;
-    const uint32_t ml = first + (cols * D + 2 * cc) * 4, oo = first + (cc * D + d) * 4;
-    float mm = -INFINITY, ll = 0.f;
+    const uint32_t ml = first + (cols * D + 4 * cc) * 4, oo = first + (cc * D + d) * 4;
+    float mm = -INFINITY;
+    Sums ll = {0.f, 0.f};
     f32x4_t o = {0.f, 0.f, 0.f, 0.f};
     for (int i = 0; i < nsplit; i += BATCH) {
-      float2 x[BATCH];
-      f32x4_t y[BATCH];
+      f32x4_t x[BATCH], y[BATCH];
 #pragma unroll
       for (int k = 0; k < BATCH; ++k) {
         const uint32_t at = min(i + k, nsplit - 1) * step;
-        x[k] = sb.load2(ml + at), y[k] = sb.load4(oo + at);
+        x[k] = sb.load4(ml + at), y[k] = sb.load4(oo + at);
       }
       float nm = mm;
 #pragma unroll
@@ -166,7 +175,7 @@ __device__ __forceinline__ void join_splits(const SplitBuffer& sb, uint32_t firs
 #pragma unroll
       for (int k = 0; k < BATCH; ++k) {
         const float g = i + k < nsplit ? exp2_fast(x[k].x - nf) : 0.f;
-        ll += x[k].y * g, o += y[k] * g;
+        ll += x[k].yz * g, o += y[k] * g;
       }
       mm = nm;
     }
@@ -174,12 +183,17 @@ __device__ __forceinline__ void join_splits(const SplitBuffer& sb, uint32_t firs
   }
 }
 
+// The natural logarithm of sum * 2^m, -inf for an empty row.
+__device__ __forceinline__ float row_lse(float m, float sum) {
+  return sum == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
 // Stores 4 channels of a joined column and (with the first) its lse.
 template <class T>
-__device__ __forceinline__ void write_joined(typename T::elem* dst, int d, const f32x4_t& o, float m, float l, float* lse) {
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+__device__ __forceinline__ void write_joined(typename T::elem* dst, int d, const f32x4_t& o, float m, const Sums& l, float* lse) {
+  const float inv = l.y == 0.f ? 0.f : 1.f / l.y;
   *reinterpret_cast<u32x2_t*>(dst + d) = u32x2_t{T::pack(o.x * inv, o.y * inv), T::pack(o.z * inv, o.w * inv)};
-  if (lse != nullptr && d == 0) *lse = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+  if (lse != nullptr && d == 0) *lse = row_lse(m, l.x);
 }
 
 }  // namespace bs

@@ -72,7 +72,7 @@ int run_gather(GatherArgs& a, const AttnCall& c, int nt, bool window, int64_t ti
                hipStream_t stream) {
   const int64_t groups = tiles * a.hkv * a.hblocks;
   if (c.workspace != nullptr && groups < kFillBlocks) {
-    const int64_t per = (int64_t)16 * nt * (c.d + 2) * 4;
+    const int64_t per = (int64_t)16 * nt * (c.d + 4) * 4;
     int64_t n = std::min((kFillBlocks + groups - 1) / groups, (max_keys + kSplitKeys - 1) / kSplitKeys);
     n = std::min(n, kPartialBytes / per / groups);
     a.nsplit = (int)std::max<int64_t>(n, 1);
@@ -122,7 +122,7 @@ int run_prefill(const AttnCall& c, const int32_t* page_table, int32_t pt_stride,
   a.nsplit = 1;
   if (c.workspace != nullptr && blocks < kFillBlocks) {
     const int64_t pages = std::min<int64_t>(pt_stride, ((int64_t)window + a.rows_per_tile) / kPage + sinks / kPage + 2);
-    const int64_t per = (int64_t)32 * waves * (c.d + 2) * 4;
+    const int64_t per = (int64_t)32 * waves * (c.d + 4) * 4;
     const int64_t n = std::min(std::min(kFillBlocks / blocks, pages / kSplitPages), kPartialBytes / per / blocks);
     a.nsplit = (uint32_t)std::max<int64_t>(n, 1);
     a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(c.workspace) + kCounterBytes);

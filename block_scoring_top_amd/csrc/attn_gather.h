@@ -112,7 +112,8 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
     } st;
     struct {
       __attribute__((aligned(16))) float o[kGaWaves][16][OLD];
-      float m[kGaWaves][16], l[kGaWaves][16];
+      float m[kGaWaves][16];
+      Sums l[kGaWaves][16];
     } jn;
   } sh;
   __shared__ uint32_t arrived;
@@ -179,10 +180,11 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
   }
 
   f32x4_t acc[NT][VD];
-  float m[NT], l[NT];
+  float m[NT];
+  Sums l[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    m[nt] = -INFINITY, l[nt] = 0.f;
+    m[nt] = -INFINITY, l[nt] = Sums{0.f, 0.f};
 #pragma unroll
     for (int d = 0; d < VD; ++d) acc[nt][d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
@@ -338,8 +340,9 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
       float p[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) p[j] = exp2_fast(__builtin_fmaf(x[j], a.scale_log2, -mf));
-      l[nt] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+      l[nt].x += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
       pfr[nt] = u32x4_t{T::pack(p[0], p[1]), T::pack(p[2], p[3]), T::pack(p[4], p[5]), T::pack(p[6], p[7])};
+      l[nt].y = add_rounded<T>(pfr[nt], l[nt].y);
     }
 
     // A key that some rows of the tile see and others do not may hold
@@ -452,12 +455,12 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
   // Join the waves, 16 columns at a time.  Thread (col, part) owns channels
   // part*VD .. +VD of its column.
   const int col = tid >> 4, part = tid & 15;
-  const uint32_t slot_floats = COLS * (D + 2);
+  const uint32_t slot_floats = COLS * (D + 4);
   const SplitBuffer sb(a.partial, a.nsplit > 1 ? (uint32_t)((uint32_t)a.tiles * gridDim.y * a.nsplit * slot_floats * 4u) : 0u);
-  auto finish = [&](int nt, const float (&o)[VD], float mm, float ll) {
+  auto finish = [&](int nt, const float (&o)[VD], float mm, const Sums& ll) {
     const int cc = nt * 16 + col, rr = cc / a.gb, hh = cc % a.gb;
     if (rr >= nrows || hh >= heads) return;
-    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+    const float inv = ll.y == 0.f ? 0.f : 1.f / ll.y;
     typename T::elem* dst = static_cast<typename T::elem*>(a.out) + (int64_t)(row0 + rr) * a.ld_out + (h0 + hh) * D + part * VD;
     uint32_t w[VD / 2];
 #pragma unroll
@@ -469,11 +472,11 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
       for (int i = 0; i < VD / 2; i += 4) *reinterpret_cast<u32x4_t*>(dst + 2 * i) = u32x4_t{w[i], w[i + 1], w[i + 2], w[i + 3]};
     }
     if (a.lse != nullptr && part == 0)
-      a.lse[(int64_t)(row0 + rr) * a.hq + h0 + hh] = ll == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(ll)) * kLn2;
+      a.lse[(int64_t)(row0 + rr) * a.hq + h0 + hh] = row_lse(mm, ll.x);
   };
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const float ls = rows_sum(l[nt]);
+    const Sums ls = {rows_sum(l[nt].x), rows_sum(l[nt].y)};
     __syncthreads();
     if (qd == 0) sh.jn.m[wave][n16] = m[nt], sh.jn.l[wave][n16] = ls;
 #pragma unroll
@@ -483,7 +486,8 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
         *reinterpret_cast<f32x4_t*>(&sh.jn.o[wave][n16][VD * (4 * qd + i) + d]) =
             f32x4_t{acc[nt][d][i], acc[nt][d + 1][i], acc[nt][d + 2][i], acc[nt][d + 3][i]};
     __syncthreads();
-    float mm = -INFINITY, ll = 0.f, o[VD];
+    float mm = -INFINITY, o[VD];
+    Sums ll = {0.f, 0.f};
 #pragma unroll
     for (int w = 0; w < kGaWaves; ++w) mm = fmaxf(mm, sh.jn.m[w][col]);
 #pragma unroll
@@ -503,14 +507,14 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
 #pragma unroll
       for (int d = 0; d < VD; d += 4)
         sb.store4(base + ((nt * 16 + col) * D + part * VD + d) * 4, f32x4_t{o[d], o[d + 1], o[d + 2], o[d + 3]});
-      if (part == 0) sb.store2(base + (COLS * D + 2 * (nt * 16 + col)) * 4, mm, ll);
+      if (part == 0) sb.store4(base + (COLS * D + 4 * (nt * 16 + col)) * 4, f32x4_t{mm, ll.x, ll.y, 0.f});
     }
   }
   if (a.nsplit == 1) return;
 
   if (!last_of_group(a.counters, group, a.nsplit, tid, arrived)) return;
   join_splits<D, 64 * kGaWaves>(sb, group * a.nsplit * slot_floats * 4, slot_floats * 4, COLS,
-                                min(nrows * a.gb, COLS), a.nsplit, tid, [&](int cc, int d, const f32x4_t& o, float mm, float ll) {
+                                min(nrows * a.gb, COLS), a.nsplit, tid, [&](int cc, int d, const f32x4_t& o, float mm, const Sums& ll) {
     const int rr = cc / a.gb, hh = cc % a.gb;
     if (hh < heads)
       write_joined<T>(static_cast<typename T::elem*>(a.out) + (int64_t)(row0 + rr) * a.ld_out + (h0 + hh) * D, d, o, mm, ll,

@@ -47,7 +47,7 @@ struct PrefillArgs {
   int64_t ld_out;
   float* lse;
   uint32_t groups, nsplit;  // row blocks times head blocks; parts that a block's pages are split into
-  float* partial;           // nsplit > 1: per (group, part) [cols][D] sums, then [cols] (maximum, sum)
+  float* partial;           // nsplit > 1: per (group, part) [cols][D] products, then [cols] (maximum, sums, 0)
 };
 
 // Which rows and heads a group is.  False: none.
@@ -147,7 +147,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prefill_kernel
   for (int d = 0; d < DT; ++d)
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[d][i] = 0.f;
-  float m = -INFINITY, l = 0.f;  // running maximum (scaled) and this half's share of the sum
+  float m = -INFINITY;    // running maximum (scaled)
+  Sums l = {0.f, 0.f};    // this half's share of the sums
 
   auto page_pos = [&](int i) { return i < sink_pages ? i : wp0 + (i - sink_pages); };
   // Next tile from `i` on whose page is one; `page` receives its id.
@@ -289,11 +290,13 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prefill_kernel
       float x = 0.f;
 #pragma unroll
       for (int i = 0; i < 16; i += 4) x += (p[i] + p[i + 1]) + (p[i + 2] + p[i + 3]);
-      l += x;
+      l.x += x;
 #pragma unroll
-      for (int g = 0; g < 2; ++g)
+      for (int g = 0; g < 2; ++g) {
         pf[2 * j + g] = u32x4_t{T::pack(p[8 * g], p[8 * g + 1]), T::pack(p[8 * g + 2], p[8 * g + 3]),
                                 T::pack(p[8 * g + 4], p[8 * g + 5]), T::pack(p[8 * g + 6], p[8 * g + 7])};
+        l.y = add_rounded<T>(pf[2 * j + g], l.y);
+      }
     }
     // Infinities and NaN in V at positions that only some rows see: 0 * inf is
     // NaN, so in masked pages they are taken out of the product, and what the
@@ -366,14 +369,15 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prefill_kernel
     while (i < tiles && !all_seen(page_pos(i) * kPage)) step(std::true_type());
   }
 
-  {
-    const uint32_t u = __float_as_uint(l);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const uint32_t u = __float_as_uint(l[e]);
     auto x = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-    l = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+    l[e] = __uint_as_float(x[0]) + __uint_as_float(x[1]);
   }
   if (a.nsplit > 1) {
     constexpr int COLS = 32 * NW;
-    float* part = a.partial + ((uint64_t)group * a.nsplit + split) * (COLS * (D + 2));
+    float* part = a.partial + ((uint64_t)group * a.nsplit + split) * (COLS * (D + 4));
     if (ok) {
 #pragma unroll
       for (int d = 0; d < DT; ++d)
@@ -381,11 +385,11 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prefill_kernel
         for (int g = 0; g < 4; ++g)
           *reinterpret_cast<f32x4_t*>(part + col * D + 32 * d + 8 * g + 4 * half) =
               f32x4_t{acc[d][4 * g], acc[d][4 * g + 1], acc[d][4 * g + 2], acc[d][4 * g + 3]};
-      if (half == 0) *reinterpret_cast<f32x2_t*>(part + COLS * D + 2 * col) = f32x2_t{m, l};
+      if (half == 0) *reinterpret_cast<f32x4_t*>(part + COLS * D + 4 * col) = f32x4_t{m, l.x, l.y, 0.f};
     }
     return;
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float inv = l.y == 0.f ? 0.f : 1.f / l.y;
   typename T::elem* dst = static_cast<typename T::elem*>(a.out) + (int64_t)(row0 + rr) * a.ld_out + (h0 + hh) * D;
 #pragma unroll
   for (int d = 0; d < DT; ++d)
@@ -404,7 +408,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prefill_kernel
       if (ok) *reinterpret_cast<u32x4_t*>(dst + 32 * d + 8 * (g + half)) = u32x4_t{x[0], y[0], x[1], y[1]};
     }
   if (ok && half == 0 && a.lse != nullptr)
-    a.lse[(int64_t)(row0 + rr) * a.hq + h0 + hh] = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    a.lse[(int64_t)(row0 + rr) * a.hq + h0 + hh] = row_lse(m, l.x);
 }
 
 // Joins the parts of every group, in their order: a lane takes 4 channels of a
@@ -419,15 +423,16 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const PrefillArgs a) {
   if (!w.locate(a, group)) return;
   const int col = u / (D / 4), d = u % (D / 4) * 4, rr = col / a.gb, hh = col % a.gb;
   if (rr >= w.nrows || hh >= w.heads) return;
-  const float* part = a.partial + (uint64_t)group * a.nsplit * (COLS * (D + 2));
-  float m = -INFINITY, l = 0.f;
+  const float* part = a.partial + (uint64_t)group * a.nsplit * (COLS * (D + 4));
+  float m = -INFINITY;
+  Sums l = {0.f, 0.f};
   f32x4_t o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
-  for (uint32_t i = 0; i < a.nsplit; ++i, part += COLS * (D + 2)) {
-    const f32x2_t x = *reinterpret_cast<const f32x2_t*>(part + COLS * D + 2 * col);
+  for (uint32_t i = 0; i < a.nsplit; ++i, part += COLS * (D + 4)) {
+    const f32x4_t x = *reinterpret_cast<const f32x4_t*>(part + COLS * D + 4 * col);
     const f32x4_t y = *reinterpret_cast<const f32x4_t*>(part + col * D + d);
     const float nm = fmaxf(m, x.x), nf = finite_max(nm), f = exp2_fast(m - nf), g = exp2_fast(x.x - nf);
-    l = l * f + x.y * g, o = o * f + y * g, m = nm;
+    l = l * f + x.yz * g, o = o * f + y * g, m = nm;
   }
   write_joined<T>(static_cast<typename T::elem*>(a.out) + (int64_t)(w.row0 + rr) * a.ld_out + (w.h0 + hh) * D, d, o, m, l,
                   a.lse == nullptr ? nullptr : a.lse + (int64_t)(w.row0 + rr) * a.hq + w.h0 + hh);

@@ -54,6 +54,7 @@ struct Bf16 {
   static __device__ __forceinline__ f32x4_t mfma16(const u32x4_t& a, const u32x4_t& b, const f32x4_t& c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(vec8, a), __builtin_bit_cast(vec8, b), c, 0, 0, 0);
   }
+  static __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) { return dot2_bf16(a, b, c); }
   static constexpr uint32_t kExpMask = 0x7F807F80u, kExpLsb = 0x00800080u;  // exponent fields of a pair
   static constexpr uint32_t kOne = 0x3F80u, k64 = 0x4280u, k65 = 0x4282u, kInfBits = 0x7F80u;
   static constexpr float kTopScale = 0x1p125f;  // a larger scale times 6 is not finite
@@ -80,6 +81,9 @@ struct F16 {
   }
   static __device__ __forceinline__ f32x4_t mfma16(const u32x4_t& a, const u32x4_t& b, const f32x4_t& c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(vec8, a), __builtin_bit_cast(vec8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(vec2, a), __builtin_bit_cast(vec2, b), c, false);
   }
   static constexpr uint32_t kExpMask = 0x7C007C00u, kExpLsb = 0x04000400u;
   static constexpr uint32_t kOne = 0x3C00u, k64 = 0x5400u, k65 = 0x5410u, kInfBits = 0x7C00u;

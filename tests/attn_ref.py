@@ -7,8 +7,11 @@ dx = (D + 16) 2^-24 S + |x| 2^-22, S the largest scale * sum |q_d k_d| of the
 row: D products summed in FP32 in any order, the scaling, and exp2's argument.
 Each weight is then off by a factor within 1 +- (dx + 2^-22) before it is
 rounded to the 16-bit type (u; in fp16 also 2^-25 absolutely, below its normal
-range), so with A = sum p |v| / sum p:
-  |out - exact| <= A (u + 2 dx + 2^-21 + 2 N 2^-24) + u |exact| + fp16's
+range).  The sum that the output is divided by is of the rounded weights, so
+their roundings e_i (|e_i| <= u) enter as sum w_i e_i (v_i - out), w_i the
+normalised weights: at most u (A + |out|), A = sum w_i |v_i|.  With the output's
+own rounding, u |out|:
+  |out - exact| <= A (u + 2 dx + 2^-21 + 2 N 2^-24) + 2 u |exact| + fp16's
   absolute terms,  |lse - exact| <= dx + 2^-21 + 2 N 2^-24 + |lse| 2^-22.
 """
 from __future__ import annotations
@@ -74,7 +77,7 @@ def check_rows(got, got_lse, want, kind, n_keys, vmax):
     u = UNIT[kind]
     for r, (out, lse, A, dx) in enumerate(want):
         N = n_keys[r]
-        tol = A * (u + 2 * dx[:, None] + 2.0 ** -21 + 2 * N * 2.0 ** -24) + u * np.abs(out) + 2.0 ** -40
+        tol = A * (u + 2 * dx[:, None] + 2.0 ** -21 + 2 * N * 2.0 ** -24) + 2 * u * np.abs(out) + 2.0 ** -40
         if kind == "f16":
             tol = tol + 2.0 ** -25 * (1 + N * vmax)
         fin = np.isfinite(out)
