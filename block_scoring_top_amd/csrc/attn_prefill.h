@@ -251,6 +251,16 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prefill_kernel
         s[j] = mfma32<T>(kf, qf[ks], s[j]);
       }
     }
+    if constexpr (!MASKED) {
+      // Eight fragments of K in flight: left alone, two are.
+      __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
+#pragma unroll
+      for (int k = 0; k < 2 * KS - 8; ++k) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x008, 8, 0);
+    }
     // Bits of the lane's keys that its row sees: key 32*j + 8*(i/4) +
     // 4*half + i%4 at bit 8*(i/4) + i%4 of word j.
     uint32_t vis[2] = {0, 0};
