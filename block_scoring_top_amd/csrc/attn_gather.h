@@ -162,6 +162,12 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
   const int c0 = (int)min(per * split, chunks);
   int c1 = (int)min(per * (split + 1), chunks);
 
+  // The 8 channels of step ks of the score product in this lane's quarter of
+  // the wave (their order is free): those that its 16-byte loads of a key hold,
+  // which four quarters make 64 contiguous bytes.
+  auto channel = [&](int ks) {
+    return !FP4 ? 32 * ks + 8 * qd : D == 64 ? 16 * qd + 8 * ks : 128 * (ks / 4) + 32 * qd + 8 * (ks % 4);
+  };
   // This lane's query vectors (column 16*nt + n16 of the tile).
   u32x4_t qf[NT][KS];
   int tcol[NT];
@@ -170,10 +176,10 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
     const int col = nt * 16 + n16, rr = col / a.gb, hh = col % a.gb;
     const bool ok = rr < nrows && hh < heads;
     const typename T::elem* src =
-        static_cast<const typename T::elem*>(a.q) + (int64_t)(row0 + (ok ? rr : 0)) * a.ld_q + (h0 + (ok ? hh : 0)) * D + qd * (D / 4);
+        static_cast<const typename T::elem*>(a.q) + (int64_t)(row0 + (ok ? rr : 0)) * a.ld_q + (h0 + (ok ? hh : 0)) * D;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      const u32x4_t x = *reinterpret_cast<const u32x4_t*>(src + 8 * ks);
+      const u32x4_t x = *reinterpret_cast<const u32x4_t*>(src + channel(ks));
       qf[nt][ks] = ok ? x ^ a.flip : u32x4_t{0, 0, 0, 0};
     }
     tcol[nt] = WINDOW && ok ? a.row_pos[row0 + rr] : -1;
@@ -221,10 +227,20 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
       const ulonglong2 x = reinterpret_cast<const ulonglong2*>(ls)[(j >> 2) * 8 + 2 * qd + (j >> 1 & 1)];
       va[j] = x.x, va[j + 1] = x.y;
     }
-    const uint8_t* kp = a.a + kvh * (FP4 ? D : 2 * D) + qd * (FP4 ? D / 8 : D / 2);
+    const uint8_t* kp = a.a + kvh * (FP4 ? D : 2 * D) + qd * (FP4 && D == 64 ? 8 : 16);
     const uint8_t* vp = FP4 ? a.a + kvh * D + D / 2 + n16 * (D / 32) : a.b + kvh * 2 * D + n16 * (D / 8);
-    load_dwords(r.k[0], kp + ka);
-    load_dwords(r.k[1], kp + kb);
+    if constexpr (FP4 && D == 64) {
+      load_dwords(r.k[0], kp + ka);
+      load_dwords(r.k[1], kp + kb);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < Raw::kKDwords; i += 4) {
+          const u32x4_t x = *reinterpret_cast<const u32x4_t*>(kp + (j ? kb : ka) + 16 * i);
+          r.k[j][i] = x.x, r.k[j][i + 1] = x.y, r.k[j][i + 2] = x.z, r.k[j][i + 3] = x.w;
+        }
+    }
     if constexpr (FP4)
       if (lane < kGaKeys) load_dwords(r.s, a.b + kvh * (D / 16) + (at >> 4));
 #pragma unroll
@@ -252,7 +268,7 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
       for (int j = 0; j < 2; ++j) {
         const uint8_t* p = sh.st.scale[wave][16 * j + n16];
         if constexpr (D == 256) {
-          kscale[j][0] = kv4_scale(p[2 * qd]), kscale[j][1] = kv4_scale(p[2 * qd + 1]);
+          kscale[j][0] = kv4_scale(p[qd]), kscale[j][1] = kv4_scale(p[4 + qd]);
         } else {
           kscale[j][0] = kv4_scale(p[qd * D / 128]);
         }
