@@ -25,13 +25,17 @@ __device__ __forceinline__ void static_for(F&& f) {
   static_for_impl(f, std::make_integer_sequence<int, N>());
 }
 
+// The maximum that passes NaN on (v_maximum3_f32).  fmaxf would first have to
+// quieten each operand, one instruction apiece.
+__device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 // Maximum / sum over the four 16-lane rows of a wave, per lane of a row.
 __device__ __forceinline__ float rows_max(float x) {
   const uint32_t u = __float_as_uint(x);
   auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  const uint32_t v = __float_as_uint(fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1])));
+  const uint32_t v = __float_as_uint(max_nan(__uint_as_float(a[0]), __uint_as_float(a[1])));
   auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+  return max_nan(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 __device__ __forceinline__ float rows_sum(float x) {
   const uint32_t u = __float_as_uint(x);

@@ -279,12 +279,18 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
     }
     // Keys without a slot: their K is read from slot 0 and masked below,
     // their V must be zeros (0 * NaN is not 0).
-    const uint32_t own = (mask >> (4 * qd)) & 0xFu, own2 = (mask >> (16 + 4 * qd)) & 0xFu;
-    const uint32_t have = own | (own2 << 4);  // bit j: key of v[j]
+    // Bit j: is there a key of v[j]?  (Opaque, or its eight tests move in front
+    // of the branches that need them.)
+    auto have = [&] {
+      uint32_t b = ((mask >> (4 * qd)) & 0xFu) | (((mask >> (16 + 4 * qd)) & 0xFu) << 4);
+      asm volatile("" : "+v"(b));
+      return b;
+    };
     if (!full) {
+      const uint32_t there = have();
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const bool ok = (have >> j) & 1u;
+        const bool ok = (there >> j) & 1u;
 #pragma unroll
         for (int i = 0; i < Raw::kVDwords; ++i) r.v[j][i] = ok ? r.v[j][i] : 0u;
         if constexpr (FP4) vscale[j] = ok ? vscale[j] : 1.f;
@@ -331,7 +337,7 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] = s[nt][j >> 2][j & 3];
       if (masked) {
-        vis[nt] = have;
+        vis[nt] = have();
         if constexpr (WINDOW) {
           const int t = tcol[nt];
 #pragma unroll
@@ -342,7 +348,9 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
         for (int j = 0; j < 8; ++j)
           x[j] = __uint_as_float(bit_select(bit_mask(vis[nt], j), __float_as_uint(x[j]), 0xFF800000u));
       }
-      float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+      float mx = x[0];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) mx = max_nan(mx, x[j]);
       mx = rows_max(mx) * a.scale_log2;
       if (ballot(mx > m[nt] + kSlack)) {
         mx = fmaxf(m[nt], mx);

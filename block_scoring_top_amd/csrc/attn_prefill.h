@@ -274,13 +274,13 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prefill_kernel
           s[j][i] = __uint_as_float(
               bit_select(bit_mask(vis[j], 8 * (i >> 2) + (i & 3)), __float_as_uint(s[j][i]), 0xFF800000u));
     }
-    float mx = fmaxf(s[0][0], s[1][0]);
+    float mx = max_nan(s[0][0], s[1][0]);
 #pragma unroll
-    for (int i = 1; i < 16; ++i) mx = fmaxf(fmaxf(mx, s[0][i]), s[1][i]);
+    for (int i = 1; i < 16; ++i) mx = max_nan(max_nan(mx, s[0][i]), s[1][i]);
     {
       const uint32_t u = __float_as_uint(mx);
       auto x = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-      mx = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])) * a.scale_log2;
+      mx = max_nan(__uint_as_float(x[0]), __uint_as_float(x[1])) * a.scale_log2;
     }
     if (ballot(mx > m + kSlack)) {
       const float mn = fmaxf(m, mx);
