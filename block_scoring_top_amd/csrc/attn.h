@@ -114,6 +114,11 @@ __device__ __forceinline__ uint64_t visible_bits(int p0, int t, int window, int 
   return below((int64_t)t + 1 - p0) & (~below((int64_t)t - window + 1 - p0) | below((int64_t)sinks - p0));
 }
 
+// The LDS address behind a generic pointer into shared memory.
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)p;
+}
+
 __device__ __forceinline__ void wave_fence() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_wave_barrier();

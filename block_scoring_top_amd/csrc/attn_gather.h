@@ -10,11 +10,11 @@
 // query vectors that share it, 4*G*D flops for 17/16*D bytes (4-bit) or 4*D
 // bytes (16-bit).  So the kernel keeps loads in flight and the rest small:
 //   * a wave works alone on 32-key chunks, the next chunk's K and V in flight
-//     while it computes; no LDS tile, no workgroup barrier in the loop;
-//   * S^T = K q^T with v_mfma_f32_16x16x32: the A operand's lane is a key, so
-//     a lane loads a quarter of one key's row contiguously (16 bytes of codes
-//     hold one group of 32 channels at D = 128: one scale a lane).  The order
-//     of channels inside the product is free as long as q has the same;
+//     while it computes; no workgroup barrier in the loop;
+//   * S^T = K q^T with v_mfma_f32_16x16x32: the A operand's lane is a key and
+//     a quarter of its row (16 bytes of codes hold one group of 32 channels at
+//     D = 128: one scale a lane).  The order of channels inside the product is
+//     free as long as q has the same;
 //   * O^T += V^T P^T: in S^T's accumulator a lane already holds the P of one
 //     query vector and of keys 4*(lane/16)+0..3 of each 16-key tile, which is
 //     the B operand of a 32-key product whose key order is chosen to match.
@@ -71,7 +71,6 @@ struct GatherRaw {
   static constexpr int kVDwords = FP4 ? (D < 128 ? 1 : D / 128) : D / 32;  // D/16 channels of a key
   uint32_t k[2][kKDwords];
   uint32_t v[8][kVDwords];
-  uint32_t s[FP4 ? D / 64 : 1];  // lanes 0..31: the scale bytes of one key
 };
 
 template <int N>
@@ -90,6 +89,49 @@ __device__ __forceinline__ void load_dwords(uint32_t (&dst)[N], const uint8_t* p
   }
 }
 
+// How a chunk of 32 keys travels to the lanes.  A wave's 16-byte loads are
+// served four neighbouring lanes at a time; neighbours in an operand are
+// different keys, so loading operands directly takes an access of the vector
+// cache for each 16 bytes (777 rows over the 16-bit pool, D = 64: 59 million).
+// Staged chunks are copied by neighbours along a key's row (20 million)
+// straight into a buffer of the wave's own in LDS, two chunks in flight, and
+// the operands read from there: 122 -> 117 us there, 22.4 -> 21.6 for 64 decode
+// rows of a 4,096 window (4-bit, D = 128), and 40 registers fewer.  The 16-bit
+// pools are staged at D = 64 only: larger chunks would leave LDS for too few
+// waves.
+//
+// A buffer holds the rows of the 32 keys (4-bit: K and V codes, which lie
+// together, then the scales; 16-bit: K, then V), their 16-byte pieces XOR-ed
+// with a function of the key that spreads the operands' reads over the banks.
+template <bool FP4, int D>
+struct Staging {
+  static constexpr bool kUsed = FP4 || D == 64;
+  static constexpr int kRow = FP4 ? D : 2 * D, kArrays = FP4 ? 1 : 2;
+  static constexpr int kLanes = kRow / 16, kKeysPerCopy = 64 / kLanes, kCopies = kGaKeys / kKeysPerCopy;
+  static constexpr int kScales = kArrays * kGaKeys * kRow, kBytes = kScales + (FP4 ? kGaKeys * D / 16 : 0);
+  static constexpr int kInFlight = kArrays * kCopies + (FP4 ? 1 : 0);  // copy instructions a chunk
+  static __device__ __forceinline__ int swizzle(int key) {
+    return kRow == 64 ? key >> 2 & 3 : kRow == 128 ? (key >> 1 & 3) | (key & 4) : key & 7;
+  }
+  static __device__ __forceinline__ const uint8_t* at(const uint8_t* buf, int key, int byte) {
+    return buf + key * kRow + (((byte >> 4) ^ swizzle(key)) << 4) + (byte & 15);
+  }
+};
+
+// Copies 16 (4) bytes a lane from p to LDS address lds + 16 (4) * lane, counted
+// by vmcnt.  Written as assembly so that the compiler does not wait for every
+// copy in flight before the next LDS read; the kernel waits by count.
+__device__ __forceinline__ void copy_to_lds16(const void* p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(lds) : "memory", "m0");
+}
+__device__ __forceinline__ void copy_to_lds4(const void* p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(p), "s"(lds) : "memory", "m0");
+}
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
 // Waves a SIMD must hold: one where two would spill registers in the loop
 // (the 16-bit loads of two chunks take 256 registers at D = 256; one such wave
 // keeps 64 KiB in flight).  64 decode rows of 2,051 slots, D = 256, 16-bit
@@ -101,6 +143,7 @@ constexpr int gather_waves(bool fp4, int d, int nt) { return nt * d == 256 && !f
 template <class T, bool FP4, int D, int NT, bool WINDOW>
 __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_gather_kernel(const GatherArgs a) {
   typedef GatherRaw<FP4, D> Raw;
+  typedef Staging<FP4, D> Stage;
   constexpr int KS = D / 32;       // 32-channel steps of the score product
   constexpr int VD = D / 16;       // channels of the output per lane and accumulator row
   constexpr int COLS = 16 * NT;    // (row, head) pairs of a tile
@@ -108,7 +151,8 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
   __shared__ union {
     struct {
       __attribute__((aligned(16))) uint64_t at[kGaWaves][kGaKeys];  // byte offsets of a chunk's keys
-      __attribute__((aligned(16))) uint8_t scale[kGaWaves][kGaKeys][D / 16];
+      __attribute__((aligned(16))) uint8_t buf[kGaWaves][2][Stage::kUsed ? Stage::kBytes : 16];
+      __attribute__((aligned(16))) int32_t id[kGaWaves][kGaKeys];   // slots or pages of the chunk after
     } st;
     struct {
       __attribute__((aligned(16))) float o[kGaWaves][16][OLD];
@@ -161,6 +205,7 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
   const uint32_t chunks = ((uint32_t)n + kGaKeys - 1) / kGaKeys, per = (chunks + a.nsplit - 1) / a.nsplit;
   const int c0 = (int)min(per * split, chunks);
   int c1 = (int)min(per * (split + 1), chunks);
+  const int n_listed = n;
 
   // The 8 channels of step ks of the score product in this lane's quarter of
   // the wave (their order is free): those that its 16-byte loads of a key hold,
@@ -241,8 +286,6 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
           r.k[j][i] = x.x, r.k[j][i + 1] = x.y, r.k[j][i + 2] = x.z, r.k[j][i + 3] = x.w;
         }
     }
-    if constexpr (FP4)
-      if (lane < kGaKeys) load_dwords(r.s, a.b + kvh * (D / 16) + (at >> 4));
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       if constexpr (FP4 && D == 64)
@@ -252,21 +295,89 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
     }
   };
 
-  auto compute = [&](Raw& r, uint32_t mask, int c) {
+  // Staged chunks: the copies of a chunk's slot (window: page) numbers, which
+  // are clamped to the list; its keys' slots once they are there; the copies of
+  // its rows; the operands out of the buffer.
+  const uint32_t lds_buf = lds_address(sh.st.buf[wave][0]), lds_id = lds_address(sh.st.id[wave]);
+  auto copy_ids = [&](int c) {
+    // Unsigned: two steps past a list of almost 2^31 entries.
+    const int i = (int)min((uint32_t)c * kGaKeys + lane, (uint32_t)n_listed - 1);
+    const int32_t* p = WINDOW ? ptab + (key_pos(i) >> 6) : a.slots + (int64_t)row0 * a.ld_slots + i;
+    if (lane < kGaKeys) copy_to_lds4(p, lds_id);
+  };
+  auto staged_slot = [&](int c) -> int {
+    const uint32_t i = (uint32_t)c * kGaKeys + (lane & 31);
+    const int x = sh.st.id[wave][lane & 31];
+    if (c >= c1 || i >= (uint32_t)n) return -1;
+    if constexpr (WINDOW) return x < 0 || x > (0x7FFFFFFF >> 6) ? -1 : x * kPage + (key_pos((int)i) & (kPage - 1));
+    return x;
+  };
+  auto copy_rows = [&](int sl, int buf, uint32_t& mask) {
+    const bool ok = sl >= 0 && sl < a.num_slots;
+    mask = (uint32_t)ballot(ok);
+    const uint32_t rec = FP4 ? (uint32_t)a.hkv * D : (uint32_t)a.ld_kv * 2;
+    wave_fence();
+    if (lane < kGaKeys) sh.st.at[wave][lane] = (uint64_t)(uint32_t)(ok ? sl : 0) * rec;
+    wave_fence();
+    const uint64_t* ls = sh.st.at[wave];
+    const uint32_t dst = lds_buf + buf * Stage::kBytes;
+    // The buffer's last operands have been read, and so have the slot numbers.
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < Stage::kCopies; ++i) {
+      const int key = i * Stage::kKeysPerCopy + lane / Stage::kLanes;
+      const uint64_t at = ls[key] + kvh * Stage::kRow + ((lane % Stage::kLanes) ^ Stage::swizzle(key)) * 16;
+      copy_to_lds16(a.a + at, dst + i * 1024);
+      if constexpr (!FP4) copy_to_lds16(a.b + at, dst + kGaKeys * Stage::kRow + i * 1024);
+    }
+    if constexpr (FP4) {
+      const uint8_t* sc = a.b + kvh * (D / 16);
+      if constexpr (D == 64) {
+        const uint8_t* p = sc + (ls[lane & 31] >> 4);
+        if (lane < kGaKeys) copy_to_lds4(p, dst + Stage::kScales);
+      } else if constexpr (D == 128) {
+        copy_to_lds4(sc + (ls[lane >> 1] >> 4) + (lane & 1) * 4, dst + Stage::kScales);
+      } else {
+        const uint8_t* p = sc + (ls[lane & 31] >> 4);
+        if (lane < kGaKeys) copy_to_lds16(p, dst + Stage::kScales);
+      }
+    }
+  };
+  auto read_rows = [&](int buf, Raw& r) {
+    const uint8_t* rows = sh.st.buf[wave][buf];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int key = 16 * j + n16;
+      if constexpr (FP4 && D == 64) {
+        load_dwords(r.k[j], Stage::at(rows, key, qd * 8));
+      } else {
+#pragma unroll
+        for (int i = 0; i < Raw::kKDwords; i += 4) {
+          const u32x4_t x = *reinterpret_cast<const u32x4_t*>(Stage::at(rows, key, 16 * i + qd * 16));
+          r.k[j][i] = x.x, r.k[j][i + 1] = x.y, r.k[j][i + 2] = x.z, r.k[j][i + 3] = x.w;
+        }
+      }
+    }
+    const uint8_t* v = FP4 ? rows : rows + kGaKeys * Stage::kRow;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint8_t* p = Stage::at(v, (j >> 2) * 16 + 4 * qd + (j & 3), FP4 ? D / 2 + n16 * (D / 32) : n16 * (D / 8));
+      if constexpr (FP4 && D == 64)
+        r.v[j][0] = *reinterpret_cast<const uint16_t*>(p);
+      else
+        load_dwords(r.v[j], p);
+    }
+  };
+
+  auto compute = [&](Raw& r, uint32_t mask, int c, int buf) {
     float vscale[8];
     float kscale[2][FP4 && D == 256 ? 2 : 1];
     bool full = mask == 0xFFFFFFFFu;
     if constexpr (FP4) {
-      wave_fence();
-      if (lane < kGaKeys) {
-        uint32_t* dst = reinterpret_cast<uint32_t*>(sh.st.scale[wave][lane]);
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) dst[i] = r.s[i];
-      }
-      wave_fence();
+      const uint8_t* sc = sh.st.buf[wave][buf] + Stage::kScales;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const uint8_t* p = sh.st.scale[wave][16 * j + n16];
+        const uint8_t* p = sc + (16 * j + n16) * (D / 16);
         if constexpr (D == 256) {
           kscale[j][0] = kv4_scale(p[qd]), kscale[j][1] = kv4_scale(p[4 + qd]);
         } else {
@@ -275,7 +386,7 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        vscale[j] = kv4_scale(sh.st.scale[wave][(j >> 2) * 16 + 4 * qd + (j & 3)][D / 32 + n16 * D / 512]);
+        vscale[j] = kv4_scale(sc[((j >> 2) * 16 + 4 * qd + (j & 3)) * (D / 16) + D / 32 + n16 * D / 512]);
     }
     // Keys without a slot: their K is read from slot 0 and masked below,
     // their V must be zeros (0 * NaN is not 0).
@@ -442,22 +553,55 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
     }
   };
 
-  // Chunks c0 + wave, + 4, ...: the loads of the next chunk are issued before
-  // this one's products, its slots one chunk earlier still.
-  {
-    int c = c0 + wave;
-    // A list's splits go by its storage, so that its first entries are on
-    // their way before its count is known.
-    int sl0 = load_slot(c), sl = load_slot(c + kGaWaves);
-    if constexpr (!WINDOW) {
-      if (a.count != nullptr) {
-        n = max(min(n, a.count[row0]), 0);
-        c1 = min(c1, (n + kGaKeys - 1) / kGaKeys);
-        const int i = c * kGaKeys + (lane & 31);
-        sl0 = i < n ? sl0 : -1;
-        sl = i + kGaWaves * kGaKeys < n ? sl : -1;
+  // Chunks c0 + wave, + 4, ...  A list's splits go by its storage, so that its
+  // first entries are on their way before its count is known.
+  int c = c0 + wave;
+  auto count = [&] {
+    if constexpr (!WINDOW)
+      if (a.count != nullptr) n = max(min(n, a.count[row0]), 0), c1 = min(c1, (n + kGaKeys - 1) / kGaKeys);
+  };
+  if constexpr (Stage::kUsed) {
+    if (c < c1) {
+      copy_ids(c);
+      count();
+      wait_vmcnt<0>();  // the builtin: it also tells the compiler that q is there
+      asm volatile("" ::: "memory");
+      if (c < c1) {
+        uint32_t kc, kn = 0;
+        int buf = 0;
+        const int sl = staged_slot(c);
+        wave_fence();
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        copy_ids(c + kGaWaves);
+        copy_rows(sl, 0, kc);
+        for (;;) {
+          const bool more = c + kGaWaves < c1;
+          if (more) {
+            wait_copies<Stage::kInFlight>();  // the next chunk's slot numbers
+            const int sn = staged_slot(c + kGaWaves);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            copy_ids(c + 2 * kGaWaves);
+            copy_rows(sn, buf ^ 1, kn);
+            wait_copies<Stage::kInFlight + 1>();  // this chunk's rows
+          } else {
+            wait_copies<0>();
+          }
+          Raw r;
+          read_rows(buf, r);
+          compute(r, kc, c, buf);
+          if (!more) break;
+          c += kGaWaves, kc = kn, buf ^= 1;
+        }
       }
     }
+  } else {
+    // The loads of the next chunk are issued before this one's products, its
+    // slots one chunk earlier still.
+    int sl0 = load_slot(c), sl = load_slot(c + kGaWaves);
+    count();
+    const int i = c * kGaKeys + (lane & 31);
+    sl0 = i < n ? sl0 : -1;
+    sl = i + kGaWaves * kGaKeys < n ? sl : -1;
     if (c < c1) {
       Raw r0, r1;
       uint32_t k0, k1;
@@ -467,7 +611,7 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
           fetch(sl, nxt, kn);
           sl = load_slot(c + 2 * kGaWaves);
         }
-        compute(cur, kc, c);
+        compute(cur, kc, c, 0);
         c += kGaWaves;
         return c < c1;
       };
