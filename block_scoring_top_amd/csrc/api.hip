@@ -242,15 +242,14 @@ namespace {
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 inline bool head_dim_ok(int32_t d) { return d == 64 || d == 128 || d == 256; }
 inline bool row_stride_ok(int64_t ld, int64_t width) { return ld >= width && (ld & 7) == 0; }
-// Slots are int32: a pool past 2^31 slots admits every non-negative one.
-inline int32_t slots_of_pages(int64_t num_pages) {
-  return num_pages > (0x7FFFFFFF / BS_PAGE_TOKENS) ? 0x7FFFFFFF : (int32_t)(num_pages * BS_PAGE_TOKENS);
-}
+// Slots are int32: so many pages at most.
+constexpr int64_t kMaxPages = 0x7FFFFFFF / BS_PAGE_TOKENS;
+inline int32_t slots_of_pages(int64_t num_pages) { return (int32_t)(num_pages * BS_PAGE_TOKENS); }
 
 inline int check_kv4_args(const void* k, const void* v, int32_t dtype, int64_t ld_k, int64_t ld_v,
                           const int32_t* slots, int32_t rows, int32_t kv_heads, int32_t head_dim,
                           const uint8_t* codes, const uint8_t* scales, int64_t num_pages) {
-  if (rows < 0 || num_pages < 0 || kv_heads < 1 || !head_dim_ok(head_dim)) return BS_ERR_ARG;
+  if (rows < 0 || num_pages < 0 || num_pages > kMaxPages || kv_heads < 1 || !head_dim_ok(head_dim)) return BS_ERR_ARG;
   if (dtype != BS_BF16 && dtype != BS_F16 && dtype != BS_F32) return BS_ERR_ARG;
   const int64_t width = (int64_t)kv_heads * head_dim;
   if (width > (1 << 20) || !row_stride_ok(ld_k, width) || !row_stride_ok(ld_v, width)) return BS_ERR_ARG;
@@ -264,7 +263,8 @@ inline int check_attn_args(const void* q, int32_t dtype, int64_t ld_q, int32_t n
                            int32_t kv_heads, int32_t head_dim, const void* cache0, const void* cache1,
                            int32_t cache_form, int64_t ld_cache, int64_t num_pages, float scale, const void* out,
                            int64_t ld_out, const void* workspace, size_t workspace_bytes) {
-  if (num_rows < 0 || num_pages < 0 || kv_heads < 1 || q_heads < 1 || !head_dim_ok(head_dim)) return BS_ERR_ARG;
+  if (num_rows < 0 || num_pages < 0 || num_pages > kMaxPages || kv_heads < 1 || q_heads < 1 || !head_dim_ok(head_dim))
+    return BS_ERR_ARG;
   if (dtype != BS_BF16 && dtype != BS_F16) return BS_ERR_ARG;
   if (cache_form != BS_KV_16 && cache_form != BS_KV_4) return BS_ERR_ARG;
   if (q_heads % kv_heads != 0 || !std::isfinite(scale)) return BS_ERR_ARG;

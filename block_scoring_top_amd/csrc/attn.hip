@@ -40,6 +40,8 @@ constexpr int64_t kSplitPages = 4;
 // 8 and 4 waves: 512 workgroups (8,192 rows, window 4,096) 279 and 294; 360 (5
 // ragged requests) 98 and 56; 256 (1,024 rows, 8 kv heads) 43 and 34.
 constexpr int64_t kEightWaves = 512;
+// Row tiles times head blocks of a launch: 2^30 lanes.
+constexpr int64_t kMaxGroups = (int64_t)1 << 21;
 
 // The running maximum is of unscaled scores times the scale, which then must
 // not be negative (q changes sign instead) nor 0 (a masked -inf times 0).
@@ -79,7 +81,7 @@ int run_gather(GatherArgs& a, const AttnCall& c, int nt, bool window, int64_t ti
     a.counters = static_cast<uint32_t*>(c.workspace);
     a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(c.workspace) + kCounterBytes);
   }
-  if (groups * a.nsplit > (int64_t)1 << 23) return BS_ERR_ARG;  // 2^31 lanes
+  if (groups > kMaxGroups) return BS_ERR_ARG;
   a.tiles = (int32_t)tiles;
   // Rows of a request read many of the same keys: 64 x 6 verify rows of 2,051
   // slots (4-bit) 42.0 us with eight neighbours on an XCD, 44.8 without.
@@ -127,7 +129,7 @@ int run_prefill(const AttnCall& c, const int32_t* page_table, int32_t pt_stride,
     a.nsplit = (uint32_t)std::max<int64_t>(n, 1);
     a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(c.workspace) + kCounterBytes);
   }
-  if (blocks > (int64_t)1 << 21) return BS_ERR_ARG;
+  if (blocks > kMaxGroups) return BS_ERR_ARG;
   a.groups = (uint32_t)blocks;
   const uint32_t grid = (a.groups * a.nsplit + 63) / 64 * 64;
   if (c.dtype == BS_BF16)

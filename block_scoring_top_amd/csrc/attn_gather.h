@@ -73,6 +73,11 @@ struct GatherRaw {
   uint32_t v[8][kVDwords];
 };
 
+__device__ __forceinline__ void load_4dwords(uint32_t* dst, const uint8_t* p) {
+  const u32x4_t x = *reinterpret_cast<const u32x4_t*>(p);
+  dst[0] = x.x, dst[1] = x.y, dst[2] = x.z, dst[3] = x.w;
+}
+
 template <int N>
 __device__ __forceinline__ void load_dwords(uint32_t (&dst)[N], const uint8_t* p) {
   if constexpr (N == 1) {
@@ -82,10 +87,7 @@ __device__ __forceinline__ void load_dwords(uint32_t (&dst)[N], const uint8_t* p
     dst[0] = x.x, dst[1] = x.y;
   } else {
 #pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const u32x4_t x = *reinterpret_cast<const u32x4_t*>(p + 4 * i);
-      dst[i] = x.x, dst[i + 1] = x.y, dst[i + 2] = x.z, dst[i + 3] = x.w;
-    }
+    for (int i = 0; i < N; i += 4) load_4dwords(dst + i, p + 4 * i);
   }
 }
 
@@ -253,46 +255,34 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
       return a.slots[(int64_t)row0 * a.ld_slots + i];
     }
   };
-  // Issues the loads of a chunk; mask: its keys whose slot is one.
-  auto fetch = [&](int sl, Raw& r, uint32_t& mask) {
+  // A key's byte offset is computed by one lane and read by those that load from
+  // it; mask: the keys whose slot is one.
+  auto put_offsets = [&](int sl, uint32_t& mask) {
     const bool ok = sl >= 0 && sl < a.num_slots;
     mask = (uint32_t)ballot(ok);
-    // A key's byte offset is computed by one lane and read by those that load
-    // from it.
     const uint32_t rec = FP4 ? (uint32_t)a.hkv * D : (uint32_t)a.ld_kv * 2;
-    const uint64_t at = (uint64_t)(uint32_t)(ok ? sl : 0) * rec;
     wave_fence();
-    if (lane < kGaKeys) sh.st.at[wave][lane] = at;
+    if (lane < kGaKeys) sh.st.at[wave][lane] = (uint64_t)(uint32_t)(ok ? sl : 0) * rec;
     wave_fence();
+  };
+  // Not staged (16-bit): issues the loads of a chunk.
+  auto fetch = [&](int sl, Raw& r, uint32_t& mask) {
+    put_offsets(sl, mask);
     const uint64_t* ls = sh.st.at[wave];
-    const uint64_t ka = ls[n16], kb = ls[16 + n16];
     uint64_t va[8];
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
       const ulonglong2 x = reinterpret_cast<const ulonglong2*>(ls)[(j >> 2) * 8 + 2 * qd + (j >> 1 & 1)];
       va[j] = x.x, va[j + 1] = x.y;
     }
-    const uint8_t* kp = a.a + kvh * (FP4 ? D : 2 * D) + qd * (FP4 && D == 64 ? 8 : 16);
-    const uint8_t* vp = FP4 ? a.a + kvh * D + D / 2 + n16 * (D / 32) : a.b + kvh * 2 * D + n16 * (D / 8);
-    if constexpr (FP4 && D == 64) {
-      load_dwords(r.k[0], kp + ka);
-      load_dwords(r.k[1], kp + kb);
-    } else {
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < 2; ++j) {
+      const uint8_t* p = a.a + kvh * 2 * D + qd * 16 + ls[16 * j + n16];
 #pragma unroll
-        for (int i = 0; i < Raw::kKDwords; i += 4) {
-          const u32x4_t x = *reinterpret_cast<const u32x4_t*>(kp + (j ? kb : ka) + 16 * i);
-          r.k[j][i] = x.x, r.k[j][i + 1] = x.y, r.k[j][i + 2] = x.z, r.k[j][i + 3] = x.w;
-        }
+      for (int i = 0; i < Raw::kKDwords; i += 4) load_4dwords(&r.k[j][i], p + 16 * i);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if constexpr (FP4 && D == 64)
-        r.v[j][0] = *reinterpret_cast<const uint16_t*>(vp + va[j]);
-      else
-        load_dwords(r.v[j], vp + va[j]);
-    }
+    for (int j = 0; j < 8; ++j) load_dwords(r.v[j], a.b + kvh * 2 * D + n16 * (D / 8) + va[j]);
   };
 
   // Staged chunks: the copies of a chunk's slot (window: page) numbers, which
@@ -313,12 +303,7 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
     return x;
   };
   auto copy_rows = [&](int sl, int buf, uint32_t& mask) {
-    const bool ok = sl >= 0 && sl < a.num_slots;
-    mask = (uint32_t)ballot(ok);
-    const uint32_t rec = FP4 ? (uint32_t)a.hkv * D : (uint32_t)a.ld_kv * 2;
-    wave_fence();
-    if (lane < kGaKeys) sh.st.at[wave][lane] = (uint64_t)(uint32_t)(ok ? sl : 0) * rec;
-    wave_fence();
+    put_offsets(sl, mask);
     const uint64_t* ls = sh.st.at[wave];
     const uint32_t dst = lds_buf + buf * Stage::kBytes;
     // The buffer's last operands have been read, and so have the slot numbers.
@@ -352,10 +337,7 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
         load_dwords(r.k[j], Stage::at(rows, key, qd * 8));
       } else {
 #pragma unroll
-        for (int i = 0; i < Raw::kKDwords; i += 4) {
-          const u32x4_t x = *reinterpret_cast<const u32x4_t*>(Stage::at(rows, key, 16 * i + qd * 16));
-          r.k[j][i] = x.x, r.k[j][i + 1] = x.y, r.k[j][i + 2] = x.z, r.k[j][i + 3] = x.w;
-        }
+        for (int i = 0; i < Raw::kKDwords; i += 4) load_4dwords(&r.k[j][i], Stage::at(rows, key, 16 * i + qd * 16));
       }
     }
     const uint8_t* v = FP4 ? rows : rows + kGaKeys * Stage::kRow;

@@ -453,8 +453,8 @@ enum bs_kv_form {
  *
  * Both return BS_OK (also when there are no rows), BS_ERR_NULL, BS_ERR_ARG
  * (dtype, head_dim, kv_heads < 1, kv_heads * head_dim > 2^20, negative counts,
- * num_pages < 1, a stride too small or no multiple of 8, a pointer that is not
- * 16-byte aligned) or BS_ERR_LAUNCH.
+ * num_pages outside 1 .. 2^25 - 1, a stride too small or no multiple of 8, a
+ * pointer that is not 16-byte aligned) or BS_ERR_LAUNCH.
  */
 int kv4_store(const void* k, const void* v, int32_t dtype, int64_t ld_k, int64_t ld_v, const int32_t* slots,
               int32_t num_tok, int32_t kv_heads, int32_t head_dim, uint8_t* codes, uint8_t* scales,
@@ -506,9 +506,9 @@ int kv4_load(const uint8_t* codes, const uint8_t* scales, int64_t num_pages, con
  *
  * Both return BS_OK (also when there are no rows), BS_ERR_NULL, BS_ERR_ARG
  * (dtype not bf16 or fp16, an unknown form, head_dim, head counts, negative
- * counts, num_pages or pt_stride < 1, a stride too small or no multiple of 8,
- * a pointer that is not 16-byte aligned, a scale that is not finite, more than
- * 2^23 workgroups), BS_ERR_WORKSPACE (a workspace smaller than
+ * counts, num_pages outside 1 .. 2^25 - 1, pt_stride < 1, a stride too small or
+ * no multiple of 8, a pointer that is not 16-byte aligned, a scale that is not
+ * finite, more than 2^21 tiles of rows times kv heads), BS_ERR_WORKSPACE (a workspace smaller than
  * BS_ATTN_WORKSPACE_BYTES) or BS_ERR_LAUNCH.
  */
 #define BS_ATTN_WORKSPACE_BYTES (((size_t)32 << 20) + ((size_t)64 << 10))

@@ -33,7 +33,7 @@ def test_kv4_refusals(call):
     assert call(n=0) == OK
     for kw in (dict(n=-1), dict(dtype=3), dict(dtype=-1), dict(d=96), dict(d=32, ld_k=64, ld_v=64), dict(hkv=0),
                dict(ld_k=255), dict(ld_v=248), dict(ld_k=260), dict(ld_v=258), dict(pages=0), dict(pages=-1),
-               dict(hkv=1 << 14, ld_k=1 << 22, ld_v=1 << 22), dict(k=ODD), dict(v=ODD), dict(codes=ODD),
+               dict(hkv=1 << 14, ld_k=1 << 22, ld_v=1 << 22), dict(pages=1 << 25), dict(k=ODD), dict(v=ODD), dict(codes=ODD),
                dict(scales=ODD)):
         assert call(**kw) == ERR_ARG, kw
     for name in ("k", "v", "slots", "codes", "scales"):
@@ -61,9 +61,9 @@ def test_attention_refusals(call):
     assert call(rows=0) == OK
     for kw in (dict(rows=-1), dict(dtype=2), dict(dtype=-1), dict(form=2), dict(form=-1), dict(d=80), dict(hq=0),
                dict(hkv=0), dict(hq=7), dict(ld_q=1023), dict(ld_q=1028), dict(ld_out=1016), dict(ld_out=1025),
-               dict(pages=0), dict(pages=-1), dict(scale=float("nan")), dict(scale=float("inf")), dict(q=ODD),
+               dict(pages=0), dict(pages=-1), dict(pages=1 << 25), dict(scale=float("nan")), dict(scale=float("inf")), dict(q=ODD),
                dict(out=ODD), dict(c0=ODD), dict(c1=ODD), dict(ws=ODD, ws_bytes=WS),
-               dict(hq=1 << 14, ld_q=1 << 21, ld_out=1 << 21), dict(form=0, ld_c=255), dict(form=0, ld_c=260)):
+               dict(hq=1 << 14, ld_q=1 << 21, ld_out=1 << 21), dict(form=0, ld_c=255), dict(form=0, ld_c=260), dict(form=0, ld_c=(1 << 24) + 8)):
         assert call(**kw) == ERR_ARG, kw
     for name in ("q", "c0", "c1", "out"):
         assert call(**{name: NULL}) == ERR_NULL, name
@@ -74,7 +74,7 @@ def test_attention_refusals(call):
 def test_slots_refusals():
     assert _slots(ld_slots=-1) == ERR_ARG
     assert _slots(slots=NULL) == ERR_NULL
-    assert _slots(rows=(1 << 22) + 1) == ERR_ARG  # more than 2^23 workgroups
+    assert _slots(rows=(1 << 20) + 1) == ERR_ARG  # more than 2^21 rows times kv heads
 
 
 def test_window_refusals():

@@ -267,6 +267,19 @@ def test_slots_extreme_scores():
     check_rows(_f64(out[:3, :4]), _f64(lse[:3]), want, "bf16", [n, 40, n], np.abs(V).max())
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.3, -1e-30, 3.0])
+@pytest.mark.parametrize("rows", [2, 40])
+def test_any_finite_scale(scale, rows):
+    say(f"scale {scale} rows={rows}")
+    pt, ptr, pos, pages = _batch([200], [rows], 4)
+    cache, K, V = _cache("kv4", "bf16", pages, 2, 128, 12)
+    q, out, lse = _queries(rows, 8, 128, "bf16", 3)
+    res, n = _window_want(_f64(q), K, V, pt, ptr, pos, pages, rows, 70, 3, scale)
+    bst.attn_window(q, cache, *[torch.from_numpy(x).cuda() for x in (pt, ptr, pos)], rows, 70, 3, out[:rows, :8], scale=scale,
+                    lse=lse[:rows], workspace=bst.attn_workspace("cuda"))
+    check_rows(_f64(out[:rows, :8]), _f64(lse[:rows]), res, "bf16", n, np.abs(V).max())
+
+
 def _batch(ctx, rows_per_req, seed, extra_rows=0, stride_extra=1):
     """page_table (random pages, -1 behind a request's), req_row_ptr, positions at the end of each context, pages."""
     rng = np.random.default_rng(seed)
@@ -540,6 +553,28 @@ def test_captured_calls_replay_like_eager(case):
             torch.cuda.synchronize()
             for a, b in zip(result(), want[i]):
                 assert torch.equal(a, b), (rep, i)
+
+
+def test_two_streams_with_workspaces_of_their_own():
+    """Split calls on two streams at once, each with its own workspace."""
+    cache, _, _ = _cache("kv4", "bf16", 60, 2, 128, 5)
+    lists = torch.randint(0, 60 * 64, (2, 3000), generator=_gen(1), device="cuda", dtype=torch.int32)
+    qs = [_queries(1, 16, 128, "bf16", 20 + i)[0].clone() for i in range(2)]
+    want = []
+    for i in range(2):
+        o = torch.empty_like(qs[i])
+        bst.attn_slots(qs[i], cache, lists[i:i + 1], o, workspace=bst.attn_workspace("cuda"))
+        want.append(o)
+    streams, wss = [torch.cuda.Stream() for _ in range(2)], [bst.attn_workspace("cuda") for _ in range(2)]
+    outs = [[torch.empty_like(qs[i]) for _ in range(20)] for i in range(2)]
+    torch.cuda.synchronize()
+    for k in range(20):
+        for i in range(2):
+            bst.attn_slots(qs[i], cache, lists[i:i + 1], outs[i][k], workspace=wss[i], stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o in outs[i]:
+            assert torch.equal(o, want[i])
 
 
 def test_prepared_and_bound_calls():
