@@ -114,6 +114,13 @@ __device__ __forceinline__ uint64_t visible_bits(int p0, int t, int window, int 
   return below((int64_t)t + 1 - p0) & (~below((int64_t)t - window + 1 - p0) | below((int64_t)sinks - p0));
 }
 
+// Where part i of n items in `parts` parts begins, the sizes differing by one at
+// most (32-bit: a 64-bit division is a hundred scalar instructions).
+__device__ __forceinline__ int part_start(uint32_t n, uint32_t parts, uint32_t i) {
+  const uint32_t q = n / parts, r = n - q * parts;
+  return (int)(q * i + min(i, r));
+}
+
 // The LDS address behind a generic pointer into shared memory.
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)p;

@@ -204,9 +204,9 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_
     row0 = tile, nrows = 1;
     n = a.ld_slots;
   }
-  const uint32_t chunks = ((uint32_t)n + kGaKeys - 1) / kGaKeys, per = (chunks + a.nsplit - 1) / a.nsplit;
-  const int c0 = (int)min(per * split, chunks);
-  int c1 = (int)min(per * (split + 1), chunks);
+  const uint32_t chunks = ((uint32_t)n + kGaKeys - 1) / kGaKeys;
+  const int c0 = part_start(chunks, a.nsplit, split);
+  int c1 = part_start(chunks, a.nsplit, split + 1);
   const int n_listed = n;
 
   // The 8 channels of step ks of the score product in this lane's quarter of

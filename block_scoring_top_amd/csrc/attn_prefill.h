@@ -128,7 +128,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prefill_kernel
   const int ns = max(0, min(a.sinks, last + 1)), sink_pages = (ns + kPage - 1) / kPage;
   const int wp0 = max(max(0, tmin - a.window + 1) / kPage, sink_pages);
   const int all_tiles = last < 0 ? 0 : sink_pages + max(0, last / kPage - wp0 + 1);
-  const int tile0 = (int)((int64_t)all_tiles * split / a.nsplit), tiles = (int)((int64_t)all_tiles * (split + 1) / a.nsplit);
+  const int tile0 = part_start(all_tiles, a.nsplit, split), tiles = part_start(all_tiles, a.nsplit, split + 1);
   const int32_t* ptab = a.page_table + (int64_t)b * a.pt_stride;
 
   u32x4_t qf[KS];
@@ -237,8 +237,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prefill_kernel
   };
   auto any_seen = [&](int p0) { return p0 <= w_last && (p0 + kPage - 1 > w_first - a.window || p0 < a.sinks); };
 
-  auto compute = [&](auto masked_c, int p0, int buf) {
-    constexpr bool MASKED = decltype(masked_c)::value;
+  auto compute = [&](auto masked_c, auto careful_c, int p0, int buf) {
+    constexpr bool MASKED = decltype(masked_c)::value, CAREFUL = MASKED && decltype(careful_c)::value;
     const uint8_t *kt = kv[buf][0], *vt = kv[buf][1];
     f32x16_t s[2];
 #pragma unroll
@@ -308,16 +308,16 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prefill_kernel
         l.y = add_rounded<T>(pf[2 * j + g], l.y);
       }
     }
-    // Infinities and NaN in V at positions that only some rows see: 0 * inf is
-    // NaN, so in masked pages they are taken out of the product, and what the
-    // rows that see them must show is added after it.
+    // Careful: infinities and NaN in V at positions that only some rows see are
+    // taken out of the product (0 * inf is NaN), and what the rows that see them
+    // must show is added after it.
     uint32_t bad = 0;
 #pragma unroll
     for (int g = 0; g < 4; ++g)
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
         u32x4_t v = v_frag(vt, 16 * g, d);
-        if constexpr (MASKED) {
+        if constexpr (CAREFUL) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint32_t x = nonfinite_pair<T>(v[i]);
@@ -326,7 +326,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prefill_kernel
         }
         acc[d] = mfma32<T>(v, pf[g], acc[d]);
       }
-    if constexpr (MASKED) {
+    if constexpr (CAREFUL) {
       if (ballot(bad != 0)) {
 #pragma unroll 1
         for (int g = 0; g < 4; ++g) {
@@ -356,27 +356,57 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prefill_kernel
     }
   };
 
-  int page = 0, i = next_tile(tile0, page), buf = 0;
-  if (i < tiles) {
-    issue(page, 0);
-    settle(0);
-  }
-  auto step = [&](auto masked_c) {
+  int page, i, buf;
+  auto step = [&](auto masked_c, auto careful_c) {
     // The buffer is complete in every wave, and the other one has been read.
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     int page1 = 0;
     const int i1 = next_tile(i + 1, page1);
     if (i1 < tiles) issue(page1, buf ^ 1);
     const int p0 = page_pos(i) * kPage;
-    if (!decltype(masked_c)::value || any_seen(p0)) compute(masked_c, p0, buf);
+    if (!decltype(masked_c)::value || any_seen(p0)) compute(masked_c, careful_c, p0, buf);
     if (i1 < tiles) settle(buf ^ 1);
     i = i1, buf ^= 1;
   };
-  // Loops of their own for the pages without and with a mask: joined in one,
-  // the accumulators were copied at each join (128 moves a page).
-  while (i < tiles) {
-    while (i < tiles && all_seen(page_pos(i) * kPage)) step(std::false_type());
-    while (i < tiles && !all_seen(page_pos(i) * kPage)) step(std::true_type());
+  auto run = [&](auto careful_c) {
+    page = 0, i = next_tile(tile0, page), buf = 0;
+    if (i < tiles) {
+      issue(page, 0);
+      settle(0);
+    }
+    // Loops of their own for the pages without and with a mask: joined in one,
+    // the accumulators were copied at each join (128 moves a page).
+    while (i < tiles) {
+      while (i < tiles && all_seen(page_pos(i) * kPage)) step(std::false_type(), careful_c);
+      while (i < tiles && !all_seen(page_pos(i) * kPage)) step(std::true_type(), careful_c);
+    }
+  };
+  run(std::false_type());
+  // A masked weight is 0, and 0 times an infinity or a NaN of V is NaN in rows
+  // that do not see it.  Such values show in the result: if a wave's is not
+  // finite, the workgroup starts over with masked pages done carefully.  (Care
+  // from the start made a masked page cost 2.8 times an unmasked one.)
+  {
+    float top = l.x;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int k = 0; k < 16; k += 2) top = max_nan(max_nan(top, fabsf(acc[d][k])), fabsf(acc[d][k + 1]));
+    __shared__ uint32_t not_finite[NW];
+    const bool bad = ballot(!(top < INFINITY)) != 0;
+    if (lane == 0) not_finite[wave] = bad;
+    __syncthreads();
+    uint32_t any = 0;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) any |= not_finite[k];
+    if (any) {
+      m = -INFINITY, l = Sums{0.f, 0.f};
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) acc[d][k] = 0.f;
+      run(std::true_type());
+    }
   }
 
 #pragma unroll
