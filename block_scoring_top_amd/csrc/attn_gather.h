@@ -134,16 +134,17 @@ __device__ __forceinline__ void wait_copies() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// Waves a SIMD must hold: one where two would spill registers in the loop
-// (the 16-bit loads of two chunks take 256 registers at D = 256; one such wave
-// keeps 64 KiB in flight).  64 decode rows of 2,051 slots, D = 256, 16-bit
-// pool: 131 us with two, 60 us with one; 64 x 6 verify rows of a 4,096 window,
-// D = 128, two column tiles: 235 and 117 us.  The 4-bit kernels are better off
-// with two (the same verify rows: 65 against 92 us).
-constexpr int gather_waves(bool fp4, int d, int nt) { return nt * d == 256 && !fp4 ? 1 : 2; }
+// Waves a SIMD must hold.  One where the registers of two would spill in the
+// loop (the 16-bit loads of two chunks take 256 at D = 256; one such wave keeps
+// 64 KiB in flight): 64 decode rows of 2,051 slots, D = 256, 16-bit pool 60 us,
+// 131 with two.  Four where two registers decide between three and four: 1,024
+// rows of 2,051 slots, 4-bit, D = 128: 71 us, 75 with three.
+constexpr int gather_waves(bool fp4, int d, int nt, bool window) {
+  return nt * d == 256 && !fp4 ? 1 : fp4 && nt * d == 128 && !window ? 4 : 2;
+}
 
 template <class T, bool FP4, int D, int NT, bool WINDOW>
-__global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT)) void attn_gather_kernel(const GatherArgs a) {
+__global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT, WINDOW)) void attn_gather_kernel(const GatherArgs a) {
   typedef GatherRaw<FP4, D> Raw;
   typedef Staging<FP4, D> Stage;
   constexpr int KS = D / 32;       // 32-channel steps of the score product
