@@ -23,22 +23,23 @@ constexpr int64_t kCounterBytes = 64 << 10;  // first part of the workspace: arr
 constexpr int64_t kPartialBytes = (int64_t)BS_ATTN_WORKSPACE_BYTES - kCounterBytes;
 // (row, head) pairs that a request may have for the gathering kernel to take
 // an attn_window call; the prefill kernel takes those with more.  64 requests,
-// window 4,096, D = 128, 48 pairs: 4-bit 64 us gathered, 62 otherwise; 16-bit
-// 118 and 68.  8 pairs, 4-bit: 24 and 59 us.
-constexpr int kGatherCols = 32;
-// Keys are split over workgroups up to this many in all, with at least
-// kSplitKeys each (two chunks a wave).  us, with 256 / 512 / 1,024 workgroups:
-// 16 rows x 4 kv heads of 2,048 slots 11.7 / 11.7 / 20.5, 64 decode rows x 2
-// heads of a 4,096 window 29.8 / 23.4 / 33.1 (4-bit, D = 128); one row of 2,050
-// slots with at least 128 / 256 / 512 keys a split 8.2 / 7.9 / 9.6.
+// window 4,096, D = 128, 48 pairs: 4-bit 46 us gathered, 61 otherwise; 16-bit
+// 102 and 68 (two gathered tiles read each key twice, four times the bytes).  8
+// pairs: 4-bit 21 and 59 us, 16-bit 49 and 64.
+int gather_cols(const AttnCall& c) { return c.form == BS_KV_4 && c.d <= 128 ? 64 : 32; }
+// Keys are split over workgroups up to kFillBlocks in all, with at least
+// kSplitKeys keys each (two chunks a wave).  us, 512 / 768 / 1,024 workgroups:
+// 64 decode rows x 2 kv heads of a 4,096 window (4-bit, D = 128) 20.9 / 23.0 /
+// 25.9, of 2,051 slots (D = 256) 23.7 / 28.9 / 28.4.  One row of 2,050 slots with
+// at least 128 / 256 / 512 keys a split: 8.8 / 8.1 / 9.8.
 constexpr int64_t kFillBlocks = 512, kSplitKeys = 256;
-// The prefill kernel: 50 rows x 2 kv heads of 8 over 65 pages, with at least
-// 2 / 4 / 8 pages a part: 28.6 / 21.7 / 25 us (93 unsplit).
+// The prefill kernel's pages: 50 rows x 2 kv heads of 8 over 65 pages, with at
+// least 2 / 4 / 8 pages a part: 28.0 / 21.5 / 23.4 us (93 unsplit).
 constexpr int64_t kSplitPages = 4;
 // Its workgroups have 8 waves if there are this many of them, else 4: 4 fill
 // the chip with less work, 8 read a page of K and V for twice the rows.  us,
-// 8 and 4 waves: 512 workgroups (8,192 rows, window 4,096) 279 and 294; 360 (5
-// ragged requests) 98 and 56; 256 (1,024 rows, 8 kv heads) 43 and 34.
+// 8 and 4 waves: 512 workgroups (8,192 rows, window 4,096) 279 and 293; 360 (5
+// ragged requests) 87 and 51; 256 (1,024 rows, 8 kv heads) 40 and 32.
 constexpr int64_t kEightWaves = 512;
 // Row tiles times head blocks of a launch: 2^30 lanes.
 constexpr int64_t kMaxGroups = (int64_t)1 << 21;
@@ -154,7 +155,7 @@ int launch_attn_window(const AttnCall& c, const int32_t* page_table, int32_t pt_
                        int32_t num_req, const int32_t* row_pos, int32_t max_rows, int32_t window, int32_t sinks,
                        hipStream_t stream) {
   const int g = c.hq / c.hkv, nt = (int64_t)g * max_rows <= 16 || c.d == 256 ? 1 : 2;
-  if ((int64_t)g * max_rows > kGatherCols)
+  if ((int64_t)g * max_rows > gather_cols(c))
     return run_prefill(c, page_table, pt_stride, req_row_ptr, num_req, row_pos, max_rows, window, sinks, stream);
   GatherArgs a = common_args(c);
   split_heads(a, nt);
