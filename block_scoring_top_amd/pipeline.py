@@ -134,6 +134,11 @@ class IndexerPath:
         head_dim] over the slots of the last ``run``, read from ``cache``
         (``KV4Cache`` or ``KV16Cache``) into ``out``."""
         if self.attn_ws is None:
-            self.attn_ws = attn_workspace(q.device)
+            # Cleared on the stream of its first use; a captured clearing
+            # would leave it as it was until the first replay.
+            with torch.cuda.stream(stream):
+                if torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("attend() must have run once before it is captured")
+                self.attn_ws = attn_workspace(q.device)
         attn_slots(q, cache, self.slots, out, count=self.out_count, scale=scale, lse=lse, workspace=self.attn_ws,
                    stream=stream)

@@ -473,6 +473,8 @@ int kv4_load(const uint8_t* codes, const uint8_t* scales, int64_t num_pages, con
  * [0, 64 * num_pages):
  *   x_i = scale * <q[r][h], K[slot_i][g]>,
  *   out[r][h] = sum_i exp(x_i - lse) V[slot_i][g],  lse[r][h] = log sum_i exp(x_i).
+ * Values of a 4-bit cache are converted to the queries' type: exact in bf16;
+ * in fp16 rounded where that type's range ends.
  * A slot listed twice counts twice.  A row without a slot gives zeros and lse
  * -inf.  Scores, running maximum, sums and outputs are held in FP32; the
  * weights are rounded to the queries' type for their product with V, and the
@@ -487,7 +489,7 @@ int kv4_load(const uint8_t* codes, const uint8_t* scales, int64_t num_pages, con
  *              first use (every call leaves its first 64 KiB zero again), or
  *              NULL with workspace_bytes 0: one size serves every call.  With
  *              it, few rows have their keys split over workgroups; without it
- *              they are not, which gives the same results slower.  Calls that
+ *              they are not: slower, and the same up to rounding.  Calls that
  *              share a workspace must not overlap in time.
  * q_heads is a multiple of kv_heads; head_dim is 64, 128 or 256.
  *

@@ -124,6 +124,12 @@ def test_binding_checks_cpu_tensors_and_shapes():
         bst.KV16Cache(torch.zeros(64, 2, 64), torch.zeros(64, 2, 128))
 
 
+def test_bounds_past_32_bits_are_the_largest():
+    """A bound on positions or rows is not wrapped to 32 bits; negative ones stay refused."""
+    got = [bst._int32(x) for x in (0, 5, 2**31 - 1, 2**31, 1 << 32, 1 << 40, -1, -(1 << 32))]
+    assert got == [0, 5, 2**31 - 1, 2**31 - 1, 2**31 - 1, 2**31 - 1, -1, -1]
+
+
 def test_the_reference_rounds_to_the_nearest_code():
     """The tests' own quantiser, at the halfway points and the ends."""
     import numpy as np

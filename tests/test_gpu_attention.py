@@ -496,6 +496,63 @@ def test_the_path_from_store_to_attention():
     check_rows(_f64(out[:inp.num_rows, :hq]), _f64(lse[:inp.num_rows]), want, "bf16", m, np.abs(V).max())
 
 
+def test_the_path_attends_first_on_another_stream(monkeypatch):
+    """The path's attention workspace is made by the first attend(): cleared on
+    the stream that the call goes to, while the current stream is still busy
+    and the memory at hand is dirty; refused while that stream captures."""
+    import synth
+    from block_scoring_top_amd.pipeline import IndexerPath
+    from synth.device import upload
+    inp = synth.qsa_verify_64req(B=2, lo=300, hi=3000)
+    say(f"attend first on another stream, rows={inp.num_rows}")
+    dev = upload(inp, "cuda")
+    cache, _, _ = _cache("kv4", "bf16", inp.num_pages, 2, 128, 11)
+    q, want, _ = _queries(inp.num_rows, 16, 128, "bf16", 12)
+    p = IndexerPath(dev, "decode")
+    with monkeypatch.context() as m:
+        m.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+        with pytest.raises(RuntimeError, match="captured"):
+            p.attend(q, cache, want[:inp.num_rows, :16])
+    assert p.attn_ws is None
+    p.run()
+    p.attend(q, cache, want[:inp.num_rows, :16])
+    got = torch.full_like(want, -77.0)
+    p.attn_ws = None
+    dirty = torch.full((bst.ATTN_WORKSPACE_BYTES,), 0x55, dtype=torch.uint8, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    del dirty
+    x = torch.randn((4096, 4096), device="cuda")
+    for _ in range(20):  # keeps the current stream busy for some ms
+        x = x @ x * 1e-3
+    p.attend(q, cache, got[:inp.num_rows, :16], stream=s)
+    s.synchronize()
+    assert torch.equal(got[:inp.num_rows, :16], want[:inp.num_rows, :16])
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("rows", [[1, 1, 1], [150, 70, 2]])
+def test_bounds_past_32_bits_mean_no_bound(rows):
+    """window, sinks and max_rows larger than any position or row count."""
+    ctx = [700, 130, 2]
+    pt, ptr, pos, pages = _batch(ctx, rows, 31)
+    say(f"bounds past 32 bits, rows={rows}")
+    cache, _, V = _cache("kv16", "bf16", pages, 2, 128, 32)
+    q, _, _ = _queries(len(pos), 8, 128, "bf16", 33)
+    args = [torch.from_numpy(x).cuda() for x in (pt, ptr, pos)]
+    ws = bst.attn_workspace("cuda")
+    outs = []
+    for max_rows, window, sinks in ((max(rows), 2**31 - 1, 0), (1 << 40, 1 << 32, 0), (2**31 - 1, 0, 1 << 33)):
+        out = torch.full((len(pos), 8, 128), -77.0, dtype=torch.bfloat16, device="cuda")
+        bst.attn_window(q, cache, *args, max_rows, window, sinks, out, workspace=ws)
+        outs.append(out)
+    torch.cuda.synchronize()
+    # The calls may take different kernels.  In each, the weights and their sum
+    # are rounded by at most 2^-8 of the result, and so is the output.
+    for o in outs[1:]:
+        assert (o.float() - outs[0].float()).abs().max().item() <= 2 * 3 * 2**-8 * np.abs(V).max()
+
+
 @pytest.mark.parametrize("case", ["slots", "window_decode", "window_prefill", "store"])
 def test_captured_calls_replay_like_eager(case):
     """Captured once, replayed with new inputs between eager work, each replay
