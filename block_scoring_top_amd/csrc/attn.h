@@ -164,38 +164,75 @@ __device__ __forceinline__ bool last_of_group(uint32_t* counters, uint32_t group
 
 // Joins the partial results of nsplit workgroups in split order.  A partial
 // (step bytes) holds [cols][D] products, then [cols] (maximum, sums, 0).  A thread takes
-// 4 channels of a column at a time; BATCH splits' loads are in flight together
-// (past the last split: its own again, with weight 0).
-template <int D, int THREADS, class F>
-__device__ __forceinline__ void join_splits(const SplitBuffer& sb, uint32_t first, uint32_t step, int cols, int ncols,
-                                            int nsplit, int tid, F write) {
-  constexpr int BATCH = 16;
-  for (int u = tid; u < ncols * (D / 4); u += THREADS) {
-    const int cc = u / (D / 4), d = (u % (D / 4)) * 4;
-    const uint32_t ml = first + (cols * D + 4 * cc) * 4, oo = first + (cc * D + d) * 4;
-    float mm = -INFINITY;
-    Sums ll = {0.f, 0.f};
-    f32x4_t o = {0.f, 0.f, 0.f, 0.f};
-    for (int i = 0; i < nsplit; i += BATCH) {
-      f32x4_t x[BATCH], y[BATCH];
+// 4 channels of UNITS columns at a time, the loads of BATCH splits of each in
+// flight together (past the last split or column: their own again, with weight
+// 0 or not written).
+template <int D, int THREADS, int UNITS, int BATCH, class F>
+__device__ __forceinline__ void join_batches(const SplitBuffer& sb, uint32_t first, uint32_t step, int cols, int ncols,
+                                             int nsplit, int tid, F write) {
+  const int n = ncols * (D / 4);
+  for (int u0 = tid; u0 < n; u0 += THREADS * UNITS) {
+    uint32_t ml[UNITS], oo[UNITS];
+    float mm[UNITS];
+    Sums ll[UNITS];
+    f32x4_t o[UNITS];
 #pragma unroll
-      for (int k = 0; k < BATCH; ++k) {
-        const uint32_t at = min(i + k, nsplit - 1) * step;
-        x[k] = sb.load4(ml + at), y[k] = sb.load4(oo + at);
-      }
-      float nm = mm;
-#pragma unroll
-      for (int k = 0; k < BATCH; ++k) nm = fmaxf(nm, x[k].x);
-      const float nf = finite_max(nm), f = exp2_fast(mm - nf);
-      ll *= f, o *= f;
-#pragma unroll
-      for (int k = 0; k < BATCH; ++k) {
-        const float g = i + k < nsplit ? exp2_fast(x[k].x - nf) : 0.f;
-        ll += x[k].yz * g, o += y[k] * g;
-      }
-      mm = nm;
+    for (int v = 0; v < UNITS; ++v) {
+      const int u = u0 + v * THREADS < n ? u0 + v * THREADS : u0;
+      const int cc = u / (D / 4), d = (u % (D / 4)) * 4;
+      ml[v] = first + (cols * D + 4 * cc) * 4, oo[v] = first + (cc * D + d) * 4;
+      mm[v] = -INFINITY, ll[v] = Sums{0.f, 0.f}, o[v] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
-    write(cc, d, o, mm, ll);
+    for (int i = 0; i < nsplit; i += BATCH) {
+      f32x4_t x[UNITS][BATCH], y[UNITS][BATCH];
+#pragma unroll
+      for (int v = 0; v < UNITS; ++v)
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+          const uint32_t at = min(i + k, nsplit - 1) * step;
+          x[v][k] = sb.load4(ml[v] + at), y[v][k] = sb.load4(oo[v] + at);
+        }
+#pragma unroll
+      for (int v = 0; v < UNITS; ++v) {
+        float nm = mm[v];
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) nm = fmaxf(nm, x[v][k].x);
+        const float nf = finite_max(nm), f = exp2_fast(mm[v] - nf);
+        ll[v] *= f, o[v] *= f;
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+          const float g = i + k < nsplit ? exp2_fast(x[v][k].x - nf) : 0.f;
+          ll[v] += x[v][k].yz * g, o[v] += y[v][k] * g;
+        }
+        mm[v] = nm;
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < UNITS; ++v) {
+      const int u = u0 + v * THREADS;
+      if (u < n) write(u / (D / 4), (u % (D / 4)) * 4, o[v], mm[v], ll[v]);
+    }
+  }
+}
+
+// A pass over the columns is a memory latency: 2 or 4 go at once where that many
+// are needed and have few splits each.
+template <int D, int THREADS, int COLS, class F>
+__device__ __forceinline__ void join_splits(const SplitBuffer& sb, uint32_t first, uint32_t step, int ncols, int nsplit,
+                                            int tid, F write) {
+  constexpr int MOST = COLS * (D / 4) / THREADS;
+  const bool passes = ncols * (D / 4) > THREADS;
+  if (nsplit > 8) {
+    join_batches<D, THREADS, 1, 16>(sb, first, step, COLS, ncols, nsplit, tid, write);
+  } else if (MOST > 1 && passes) {
+    if (MOST > 2 && nsplit <= 4)
+      join_batches<D, THREADS, (MOST > 2 ? 4 : 1), 4>(sb, first, step, COLS, ncols, nsplit, tid, write);
+    else
+      join_batches<D, THREADS, (MOST > 1 ? 2 : 1), 8>(sb, first, step, COLS, ncols, nsplit, tid, write);
+  } else if (nsplit > 4) {
+    join_batches<D, THREADS, 1, 8>(sb, first, step, COLS, ncols, nsplit, tid, write);
+  } else {
+    join_batches<D, THREADS, 1, 4>(sb, first, step, COLS, ncols, nsplit, tid, write);
   }
 }
 

@@ -21,21 +21,40 @@ namespace {
 
 constexpr int64_t kCounterBytes = 64 << 10;  // first part of the workspace: arrival counters
 constexpr int64_t kPartialBytes = (int64_t)BS_ATTN_WORKSPACE_BYTES - kCounterBytes;
-// (row, head) pairs that a request may have for the gathering kernel to take
-// an attn_window call; the prefill kernel takes those with more.  64 requests,
-// window 4,096, D = 128, 48 pairs: 4-bit 46 us gathered, 61 otherwise; 16-bit
-// 102 and 68 (two gathered tiles read each key twice, four times the bytes).  8
-// pairs: 4-bit 21 and 59 us, 16-bit 49 and 64.
-int gather_cols(const AttnCall& c) { return c.form == BS_KV_4 && c.d <= 128 ? 64 : 32; }
-// Keys are split over workgroups up to kFillBlocks in all, with at least
-// kSplitKeys keys each (two chunks a wave).  us, 512 / 768 / 1,024 workgroups:
-// 64 decode rows x 2 kv heads of a 4,096 window (4-bit, D = 128) 20.9 / 23.0 /
-// 25.9, of 2,051 slots (D = 256) 23.7 / 28.9 / 28.4.  One row of 2,050 slots with
-// at least 128 / 256 / 512 keys a split: 8.8 / 8.1 / 9.8.
-constexpr int64_t kFillBlocks = 512, kSplitKeys = 256;
-// The prefill kernel's pages: 50 rows x 2 kv heads of 8 over 65 pages, with at
-// least 2 / 4 / 8 pages a part: 28.0 / 21.5 / 23.4 us (93 unsplit).
-constexpr int64_t kSplitPages = 4;
+// Does the gathering kernel take an attn_window call, or the prefill kernel?  The
+// first is quicker to start and splits the keys of few rows well; it reads them
+// once for 16 or 32 (row, head) pairs where the other reads them for 128.  It takes
+//   * calls of at most `most` row tiles times keys, which latency bounds.  us,
+//     gathered and not: 4-bit, D = 128, 6 rows x 8 heads, window 700 12.0 and 13.1,
+//     36 requests of them 14.8 and 21.2; 700 rows, 700,000 tiles times keys, 40.5
+//     and 43.3, 1.4 million 65.2 and 50.6.  16-bit, D = 128, 100 rows, window 1,200
+//     (60,000) 16.0 and 17.3, 4,000 29.2 and 23.8;
+//   * requests whose pairs are one tile, or (`ratio`) whose tiles read the keys no
+//     more than that many times for the other's once: half of its pairs would
+//     be padding.  64 requests, window 4,000: 1 row, 16-bit 46 and 59; 6 rows,
+//     4-bit 40 and 60;
+//   * the 4-bit cache at D = 256, where one wave a SIMD is all that the other's
+//     registers allow: 8,192 rows, window 4,000 848 and 961, 500 211 and 206; 64 x 6
+//     rows 74 and 265.
+bool gathers(const AttnCall& c, int64_t tiles, int64_t keys, int64_t pairs, int64_t num_req) {
+  const bool kv4 = c.form == BS_KV_4;
+  if (pairs <= 16 || (kv4 && c.d == 256)) return true;
+  const double most = kv4 ? (c.d == 64 ? 550e3 : 700e3) : c.d == 64 ? 500e3 : c.d == 128 ? 60e3 : 80e3;
+  const int64_t ratio = kv4 || c.d == 64 ? 2 : 0;
+  return (double)tiles * keys <= most || tiles <= ratio * num_req * c.hkv * ((pairs + 127) / 128);
+}
+// Keys are split over up to kFillBlocks workgroups in all.  us, 512 / 768 / 1,024:
+// 64 decode rows x 2 kv heads of a 4,096 window (4-bit, D = 128) 20.9 / 23.0 / 25.9,
+// of 2,051 slots (D = 256) 23.7 / 28.9 / 28.4.
+constexpr int64_t kFillBlocks = 512;
+// What splitting the prefill kernel's pages costs, in the time of a page (1.27
+// us at D = 128, D to that): kJoinPages for the launch that joins, a page for
+// every kPartsPerPage parts written and read again, kPartPages for each part
+// that a joining lane goes through.  us, D = 128, 8 heads a group of 4: a window
+// of 800 in 1 / 2 / 3 / 4 / 8 parts, 8 blocks 25.6 / 20.3 / 16.9 / 15.9 / 14.7, 100
+// blocks 26.3 / 27.7 / 27.4 / 28.0 / 28.0; 4,096, 28 blocks 91.8 / 52.6 / 40.2 /
+// 34.6 / 27.4 (16 parts: 30.5).
+constexpr double kJoinPages = 2.5, kPartsPerPage = 42, kPartPages = 1. / 6;
 // Its workgroups have 8 waves if there are this many of them, else 4: 4 fill
 // the chip with less work, 8 read a page of K and V for twice the rows.  us,
 // 8 and 4 waves: 512 workgroups (8,192 rows, window 4,096) 279 and 293; 360 (5
@@ -71,14 +90,41 @@ void split_heads(GatherArgs& a, int nt) {
   a.gb = (g + a.hblocks - 1) / a.hblocks;
 }
 
+// Over how many workgroups a group of the gathering kernel has its keys split:
+// of 1, 2, 4 .. `most` the number whose estimated time is least.  In us: a chunk of
+// each of the 4 waves after the other (workgroups past one a compute unit slow each
+// other down), but no less than the keys' bytes take; a join of 4 us, the parts
+// that are written and read again (1.3 MB a us), and 3 for each round of loads that
+// a joining lane waits for after the first.  (`cols`: columns in use.)  Over 106
+// sweeps of 1 to 128 parts (1 to 240 groups of 250 to 64,000 keys, both caches, all
+// head dims) the number chosen is 1.6% slower than the best one; as many as 512
+// workgroups and 256 keys a part allow, 11%: 1 row of 256 slots 5.5 and 8.0 us, 30
+// requests x 2 rows x 8 heads of D = 256 over 4,096 keys 24 and 42.
+int gather_splits(const AttnCall& c, int nt, int cols, int64_t groups, int64_t keys, int64_t most) {
+  const bool kv4 = c.form == BS_KV_4;
+  const double chunk = 0.6 + 0.7 * nt * c.d / 128 + (kv4 || c.d == 64 ? 0. : c.d == 256 ? 3. : 1.1);
+  const double read = groups * keys * c.d * (kv4 ? 17. / 16 : 4.) / 4.5e6;
+  const double part = cols * (c.d + 4) * 4e-6 * groups, rounds = cols * c.d / 16384.;
+  int64_t best = 1;
+  double least = 0;
+  for (int64_t n = 1; n <= most; n *= 2) {
+    const int64_t chunks = ((keys + kGaKeys - 1) / kGaKeys + kGaWaves * n - 1) / (kGaWaves * n);
+    const int64_t layers = (groups * n + 255) / 256;
+    double t = std::max(chunks * chunk * (layers == 1 ? 1. : 0.6 * layers), read) + (layers - 1);
+    if (n > 1) t += 4 + 0.75 * n * part + 3 * std::max(0., n * rounds - 1);
+    if (n == 1 || t < least) best = n, least = t;
+    if (chunks <= 1) break;
+  }
+  return (int)best;
+}
+
 int run_gather(GatherArgs& a, const AttnCall& c, int nt, bool window, int64_t tiles, int64_t max_keys,
                hipStream_t stream) {
   const int64_t groups = tiles * a.hkv * a.hblocks;
   if (c.workspace != nullptr && groups < kFillBlocks) {
     const int64_t per = (int64_t)16 * nt * (c.d + 4) * 4;
-    int64_t n = std::min((kFillBlocks + groups - 1) / groups, (max_keys + kSplitKeys - 1) / kSplitKeys);
-    n = std::min(n, kPartialBytes / per / groups);
-    a.nsplit = (int)std::max<int64_t>(n, 1);
+    const int64_t most = std::min(kFillBlocks / groups, kPartialBytes / per / groups);
+    a.nsplit = gather_splits(c, nt, window ? std::min(16 * nt, a.rows_per_tile * a.gb) : a.gb, groups, max_keys, most);
     a.counters = static_cast<uint32_t*>(c.workspace);
     a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(c.workspace) + kCounterBytes);
   }
@@ -126,8 +172,10 @@ int run_prefill(const AttnCall& c, const int32_t* page_table, int32_t pt_stride,
   if (c.workspace != nullptr && blocks < kFillBlocks) {
     const int64_t pages = std::min<int64_t>(pt_stride, ((int64_t)window + a.rows_per_tile) / kPage + sinks / kPage + 2);
     const int64_t per = (int64_t)32 * waves * (c.d + 4) * 4;
-    const int64_t n = std::min(std::min(kFillBlocks / blocks, pages / kSplitPages), kPartialBytes / per / blocks);
-    a.nsplit = (uint32_t)std::max<int64_t>(n, 1);
+    const double part = blocks / kPartsPerPage + kPartPages;
+    const int64_t best = (int64_t)std::sqrt(pages / part);
+    const int64_t n = std::min(std::min(kFillBlocks / blocks, best), kPartialBytes / per / blocks);
+    if (n > 1 && pages - pages / (double)n > kJoinPages + n * part) a.nsplit = (uint32_t)n;
     a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(c.workspace) + kCounterBytes);
   }
   if (blocks > kMaxGroups) return BS_ERR_ARG;
@@ -155,16 +203,17 @@ int launch_attn_window(const AttnCall& c, const int32_t* page_table, int32_t pt_
                        int32_t num_req, const int32_t* row_pos, int32_t max_rows, int32_t window, int32_t sinks,
                        hipStream_t stream) {
   const int g = c.hq / c.hkv, nt = (int64_t)g * max_rows <= 16 || c.d == 256 ? 1 : 2;
-  if ((int64_t)g * max_rows > gather_cols(c))
-    return run_prefill(c, page_table, pt_stride, req_row_ptr, num_req, row_pos, max_rows, window, sinks, stream);
   GatherArgs a = common_args(c);
   split_heads(a, nt);
-  a.page_table = page_table, a.pt_stride = pt_stride, a.req_row_ptr = req_row_ptr, a.row_pos = row_pos;
-  a.max_rows = max_rows, a.window = window, a.sinks = sinks;
   a.rows_per_tile = std::max(1, 16 * nt / a.gb);
   a.tiles_per_req = (int)(((int64_t)max_rows + a.rows_per_tile - 1) / a.rows_per_tile);
   const int64_t keys = std::min<int64_t>((int64_t)pt_stride * kPage, (int64_t)window + sinks + a.rows_per_tile - 1);
-  return run_gather(a, c, nt, true, (int64_t)num_req * a.tiles_per_req, keys, stream);
+  const int64_t tiles = (int64_t)num_req * a.tiles_per_req;
+  if (!gathers(c, tiles * c.hkv * a.hblocks, keys, (int64_t)g * max_rows, num_req))
+    return run_prefill(c, page_table, pt_stride, req_row_ptr, num_req, row_pos, max_rows, window, sinks, stream);
+  a.page_table = page_table, a.pt_stride = pt_stride, a.req_row_ptr = req_row_ptr, a.row_pos = row_pos;
+  a.max_rows = max_rows, a.window = window, a.sinks = sinks;
+  return run_gather(a, c, nt, true, tiles, keys, stream);
 }
 
 }  // namespace bs

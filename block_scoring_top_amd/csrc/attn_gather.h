@@ -33,7 +33,7 @@
 //
 // Measured: 64 x 6 rows of 2,051 slots, 16 query / 2 kv heads of 128, 4-bit
 // cache: 43 us, 225 MB fetched at 5.1 TB/s (a large copy: 4.8), the vector units
-// busy for 54% of it.  16 rows of 2,048 slots, 4 kv heads: 11.9 us; one row: 8.1
+// busy for 54% of it.  16 rows of 2,048 slots, 4 kv heads: 10.1 us; one row: 7.9
 // us.  777 rows of 2,051 slots over a 25 MB 16-bit pool, 3 kv heads of 64: 111 us,
 // 1.2 GB gathered, of which the L2s let 731 MB through at 6.4 TB/s.
 #pragma once
@@ -103,7 +103,7 @@ __device__ __forceinline__ void load_dwords(uint32_t (&dst)[N], const uint8_t* p
 // cache for each 16 bytes (777 rows over the 16-bit pool, D = 64: 59 million).
 // Staged chunks are copied by neighbours along a key's row (20 million)
 // straight into a buffer of the wave's own in LDS, two chunks in flight, and
-// the operands read from there: 122 -> 117 us there, 22.4 -> 21.6 for 64 decode
+// the operands read from there: 122 -> 117 us there, 22.4 -> 21.6 (19.6 now) for 64 decode
 // rows of a 4,096 window (4-bit, D = 128), and 40 registers fewer.  The 16-bit
 // pools are staged at D = 64 only: larger chunks would leave LDS for too few
 // waves.
@@ -670,8 +670,8 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT, WINDOW)) vo
   if (a.nsplit == 1) return;
 
   if (!last_of_group(a.counters, group, a.nsplit, tid, arrived)) return;
-  join_splits<D, 64 * kGaWaves>(sb, group * a.nsplit * slot_floats * 4, slot_floats * 4, COLS,
-                                min(nrows * a.gb, COLS), a.nsplit, tid, [&](int cc, int d, const f32x4_t& o, float mm, const Sums& ll) {
+  join_splits<D, 64 * kGaWaves, COLS>(sb, group * a.nsplit * slot_floats * 4, slot_floats * 4, min(nrows * a.gb, COLS),
+                                      a.nsplit, tid, [&](int cc, int d, const f32x4_t& o, float mm, const Sums& ll) {
     const int rr = cc / a.gb, hh = cc % a.gb;
     if (hh < heads)
       write_joined<T>(static_cast<typename T::elem*>(a.out) + (int64_t)(row0 + rr) * a.ld_out + (h0 + hh) * D, d, o, mm, ll,

@@ -406,6 +406,101 @@ def test_window_masked_infinite_values(rows):
     check_rows(_f64(out[:rows, :4]), _f64(lse[:rows]), res, "bf16", n, np.max(np.abs(V[np.isfinite(V)])))
 
 
+# Small batches of many rows are gathered.  What follows makes the same batches
+# long enough for the prefill kernel: with requests that have no rows, or with a
+# page table much wider than the contexts (whose pages the kernel then splits).
+
+def _with_empty_requests(pt, ptr, max_rows, hq, hkv, window, sinks):
+    """At least 800,000 row tiles (of 32 pairs) times keys, which the kernels' rule puts on the prefill side."""
+    tiles = -(-max_rows * hq // 32)
+    n = 800_000 // (tiles * min(pt.shape[1] * 64, window + sinks + 1)) + 1
+    return np.concatenate([pt, np.full((n, pt.shape[1]), -1, np.int32)]), np.concatenate([ptr, np.full(n, ptr[-1], np.int32)])
+
+
+@pytest.mark.parametrize("kind,form,d,hq,hkv,ctx,rows,max_rows,window,sinks",
+                         [c for c in WINDOW_CASES if c[7] >= 130 and not (c[1] == "kv4" and c[2] == 256)])
+def test_window_prefill_matches_the_definition(kind, form, d, hq, hkv, ctx, rows, max_rows, window, sinks):
+    say(f"attn_window prefill {kind} {form} d={d} hq={hq} hkv={hkv} ctx={ctx} rows={rows} window={window} sinks={sinks}")
+    pt, ptr, pos, pages = _batch(ctx, rows, d + hq, extra_rows=2)
+    pt, ptr = _with_empty_requests(pt, ptr, max_rows, hq, hkv, window, sinks)
+    _check_window(kind, form, d, hq, hkv, pt, ptr, pos, pages, max_rows, window, sinks, 3 * d + hq)
+
+
+@pytest.mark.parametrize("kind,form,d,hq,hkv,ctx,rows", [
+    ("bf16", "kv16", 128, 4, 1, [333, 64], [200, 64]), ("f16", "kv4", 128, 7, 1, [700], [150]),
+    ("bf16", "kv4", 64, 16, 2, [400, 33], [260, 33]), ("f16", "kv16", 64, 8, 8, [300], [290]),
+    ("bf16", "kv16", 256, 4, 2, [900, 1], [50, 1]), ("bf16", "kv4", 128, 8, 2, [1500], [170])])
+@pytest.mark.parametrize("window,sinks", [(2**31 - 1, 0), (0, 1 << 30), (1 << 24, 3)])
+def test_window_prefill_split_pages(kind, form, d, hq, hkv, ctx, rows, window, sinks):
+    """Pages split over workgroups, most of whose parts are empty."""
+    say(f"attn_window prefill split {kind} {form} d={d} hq={hq} hkv={hkv} ctx={ctx} rows={rows} window={window} sinks={sinks}")
+    pt, ptr, pos, pages = _batch(ctx, rows, d + hq, extra_rows=2, stride_extra=30000)
+    _check_window(kind, form, d, hq, hkv, pt, ptr, pos, pages, max(rows), window, sinks, 3 * d + hq)
+
+
+def test_window_prefill_odd_rows():
+    """test_window_odd_rows by the prefill kernel."""
+    say("attn_window prefill odd rows")
+    pt, ptr, pos, pages = _batch([400, 300, 260], [7, 203, 4], 5, extra_rows=1, stride_extra=0)
+    rng = np.random.default_rng(2)
+    pos[:7] = [399, -1, 20, 20, 150, 5000, 0]
+    pos[7:210] = rng.integers(-3, 300, 203)
+    pt[0, 1], pt[1, 2], pt[2, 0] = -1, pages, 2 ** 30            # no such pages
+    pt, ptr = _with_empty_requests(pt, ptr, 200, 8, 2, 90, 70)
+    for form in ("kv16", "kv4"):
+        _check_window("bf16", form, 128, 8, 2, pt, ptr, pos, pages, 200, 90, 70, 17)
+
+
+@pytest.mark.parametrize("form,bad", [("kv16", float("nan")), ("kv16", float("inf")), ("kv16", -float("inf")),
+                                      ("kv4", float("nan"))])
+@pytest.mark.parametrize("split", [False, True])
+def test_window_prefill_masked_infinities_and_nan(form, bad, split):
+    say(f"attn_window prefill masked {form} {bad} split={split}")
+    pt, ptr, pos, pages = _batch([200], [150], 8, stride_extra=30000 if split else 1)
+    window, sinks = (2**31 - 1, 0) if split else (60, 4)
+    if not split:
+        pt, ptr = _with_empty_requests(pt, ptr, 150, 4, 1, window, sinks)
+    at = np.array([pt[0, p // 64] * 64 + p % 64 for p in (198, 199, 90)])
+    _check_window("bf16", form, 128, 4, 1, pt, ptr, pos, pages, 150, window, sinks, 23, poison=(at, bad))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("split", [False, True])
+def test_window_prefill_masked_infinite_values(kind, split):
+    """Finite keys: an infinity in V reaches the rows that see it as that infinity, both signs as NaN."""
+    say(f"attn_window prefill infinite values {kind} split={split}")
+    pt, ptr, pos, pages = _batch([200], [150], 8, stride_extra=30000 if split else 1)
+    window, sinks = (2**31 - 1, 0) if split else (60, 4)
+    if not split:
+        pt, ptr = _with_empty_requests(pt, ptr, 150, 4, 1, window, sinks)
+    cache, K, V = _cache("kv16", kind, pages, 1, 128, 31)
+    for p, ch, x in ((199, 3, np.inf), (198, 3, -np.inf), (197, 64, np.inf), (60, 100, -np.inf), (197, 127, np.nan)):
+        s = int(pt[0, p // 64]) * 64 + p % 64
+        cache.v[s, 0, ch] = x
+        V[s, 0, ch] = x
+    q, out, lse = _queries(150, 4, 128, kind, 2)
+    res, n = _window_want(_f64(q), K, V, pt, ptr, pos, pages, 150, window, sinks, 0.09)
+    bst.attn_window(q, cache, *[torch.from_numpy(x).cuda() for x in (pt, ptr, pos)], 150, window, sinks, out[:150, :4], scale=0.09,
+                    lse=lse[:150], workspace=bst.attn_workspace("cuda"))
+    check_rows(_f64(out[:150, :4]), _f64(lse[:150]), res, kind, n, np.max(np.abs(V[np.isfinite(V)])))
+
+
+def test_long_split_lists_join_in_rounds():
+    """Rows of few heads and many, whose parts are joined 16, 8 and 4 at a time (one part's columns short of its tile's)."""
+    for hq, hkv, d, k in ((28, 1, 128, 600), (28, 1, 128, 2100), (13, 1, 256, 2100), (5, 1, 64, 9000), (28, 1, 128, 40000),
+                          (16, 1, 256, 40000)):
+        say(f"attn_slots split hq={hq} d={d} k={k}")
+        cache, K, V = _cache("kv4", "bf16", 40, hkv, d, 3)
+        rng = np.random.default_rng(k)
+        lists = rng.integers(0, 2560, (2, k)).astype(np.int32)
+        lists[1, ::3] = -1
+        q, out, lse = _queries(2, hq, d, "bf16", 5)
+        want = [attend_row(_f64(q[r]), K[x[x >= 0]], V[x[x >= 0]], d ** -0.5) for r, x in enumerate(lists)]
+        bst.attn_slots(q, cache, torch.from_numpy(lists).cuda(), out[:2, :hq], lse=lse[:2], workspace=bst.attn_workspace("cuda"))
+        torch.cuda.synchronize()
+        check_rows(_f64(out[:2, :hq]), _f64(lse[:2]), want, "bf16", [k, k - -(-k // 3)], np.abs(V).max())
+
+
 @pytest.mark.parametrize("form", ["kv4", "kv16"])
 def test_pools_past_4_gib(form):
     """Slots whose byte offsets pass 32 bits."""
