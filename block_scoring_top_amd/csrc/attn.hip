@@ -166,6 +166,11 @@ int run_prefill(const AttnCall& c, const int32_t* page_table, int32_t pt_stride,
   }
   a.page_table = page_table, a.req_row_ptr = req_row_ptr, a.row_pos = row_pos, a.pt_stride = pt_stride;
   a.max_rows = max_rows, a.window = window, a.sinks = sinks;
+  // Without a window a request's later rows see more keys, and workgroups that
+  // start last should not be the longest: 8,192 rows from position 0, 16 query / 2
+  // kv heads of 128, 16-bit 310 us so, 406 in order; 4,096 rows of 256 237 and 323.
+  // Under a window all are about as long, and in order is up to 6% quicker.
+  a.latest_first = window >= (int64_t)pt_stride * kPage;
   set_scale(c, a.scale_log2, a.flip);
   a.out = c.out, a.ld_out = c.ld_out, a.lse = c.lse;
   a.nsplit = 1;

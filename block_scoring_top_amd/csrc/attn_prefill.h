@@ -51,6 +51,7 @@ struct PrefillArgs {
   void* out;
   int64_t ld_out;
   float* lse;
+  bool latest_first;        // a request's last rows start first
   uint32_t groups, nsplit;  // row blocks times head blocks; parts that a block's pages are split into
   float* partial;           // nsplit > 1: per (group, part) [cols][D] products, then [cols] (maximum, sums, 0)
 };
@@ -65,9 +66,9 @@ struct PrefillGroup {
     heads = min(a.gb, G - hin), h0 = kvh * G + hin;
     const int ra = max(a.req_row_ptr[b], 0);
     const int rb = (int)min((int64_t)min(a.req_row_ptr[b + 1], a.num_rows), (int64_t)ra + a.max_rows);
-    const int64_t first = (int64_t)ra + (int64_t)i_tile * a.rows_per_tile;
-    if (first >= rb) return false;
-    row0 = (int)first, nrows = min(a.rows_per_tile, rb - row0);
+    const int last = ((rb > ra ? rb - ra : 0) + a.rows_per_tile - 1) / a.rows_per_tile - 1;
+    if (i_tile > last) return false;
+    row0 = ra + (a.latest_first ? last - i_tile : i_tile) * a.rows_per_tile, nrows = min(a.rows_per_tile, rb - row0);
     return true;
   }
 };
