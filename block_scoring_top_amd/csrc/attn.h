@@ -139,6 +139,9 @@ struct SplitBuffer {
   __device__ __forceinline__ SplitBuffer(float* p, uint32_t bytes)
       : rs(__builtin_amdgcn_make_buffer_rsrc(p, (short)0, bytes, 0x00020000)) {}
   static constexpr int kSc1 = 16;
+  // Past every workspace (32 MiB): a load from there is refused by the
+  // buffer's bounds and gives zeros.
+  static constexpr uint32_t kNowhere = 1u << 30;
   __device__ __forceinline__ void store4(uint32_t off, const f32x4_t& v) const {
     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), rs, off, 0, kSc1);
   }
@@ -165,8 +168,8 @@ __device__ __forceinline__ bool last_of_group(uint32_t* counters, uint32_t group
 // Joins the partial results of nsplit workgroups in split order.  A partial
 // (step bytes) holds [cols][D] products, then [cols] (maximum, sums, 0).  A thread takes
 // 4 channels of UNITS columns at a time, the loads of BATCH splits of each in
-// flight together (past the last split or column: their own again, with weight
-// 0 or not written).
+// flight together (past the last split: zeros, as a split read again with weight
+// 0 might hold infinities; past the last column: its own again, not written).
 template <int D, int THREADS, int UNITS, int BATCH, class F>
 __device__ __forceinline__ void join_batches(const SplitBuffer& sb, uint32_t first, uint32_t step, int cols, int ncols,
                                              int nsplit, int tid, F write) {
@@ -189,8 +192,10 @@ __device__ __forceinline__ void join_batches(const SplitBuffer& sb, uint32_t fir
       for (int v = 0; v < UNITS; ++v)
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
-          const uint32_t at = min(i + k, nsplit - 1) * step;
+          const bool there = i + k < nsplit;
+          const uint32_t at = there ? (i + k) * step : SplitBuffer::kNowhere;
           x[v][k] = sb.load4(ml[v] + at), y[v][k] = sb.load4(oo[v] + at);
+          x[v][k].x = there ? x[v][k].x : -INFINITY;
         }
 #pragma unroll
       for (int v = 0; v < UNITS; ++v) {
@@ -201,7 +206,7 @@ __device__ __forceinline__ void join_batches(const SplitBuffer& sb, uint32_t fir
         ll[v] *= f, o[v] *= f;
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
-          const float g = i + k < nsplit ? exp2_fast(x[v][k].x - nf) : 0.f;
+          const float g = exp2_fast(x[v][k].x - nf);
           ll[v] += x[v][k].yz * g, o[v] += y[v][k] * g;
         }
         mm[v] = nm;
