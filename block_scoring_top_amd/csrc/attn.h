@@ -45,7 +45,8 @@ __device__ __forceinline__ float rows_sum(float x) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-// A row's sums of weights, relative to its running maximum: x of the weights in
+// A row's sums of weights, relative to its running maximum and raised by
+// 2^T::kRaise, which the output's division cancels: x of the weights in
 // FP32 (for lse), y of the weights as rounded for their product with V.  The
 // output is divided by y: the rounding of a weight that dominates its row then
 // cancels.  Over 52 drawn calls the outputs' error against 64 bits is 1.16
@@ -241,9 +242,11 @@ __device__ __forceinline__ void join_splits(const SplitBuffer& sb, uint32_t firs
   }
 }
 
-// The natural logarithm of sum * 2^m, -inf for an empty row.
+// The natural logarithm of a row's sum of weights, -inf for an empty row: m is
+// its maximum (log2), the sum relative to that and raised.
+template <class T>
 __device__ __forceinline__ float row_lse(float m, float sum) {
-  return sum == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(sum)) * kLn2;
+  return sum == 0.f ? -INFINITY : (m + (__builtin_amdgcn_logf(sum) - T::kRaise)) * kLn2;
 }
 
 // Stores 4 channels of a joined column and (with the first) its lse.
@@ -251,7 +254,7 @@ template <class T>
 __device__ __forceinline__ void write_joined(typename T::elem* dst, int d, const f32x4_t& o, float m, const Sums& l, float* lse) {
   const float inv = l.y == 0.f ? 0.f : 1.f / l.y;
   *reinterpret_cast<u32x2_t*>(dst + d) = u32x2_t{T::pack(o.x * inv, o.y * inv), T::pack(o.z * inv, o.w * inv)};
-  if (lse != nullptr && d == 0) *lse = row_lse(m, l.x);
+  if (lse != nullptr && d == 0) *lse = row_lse<T>(m, l.x);
 }
 
 }  // namespace bs

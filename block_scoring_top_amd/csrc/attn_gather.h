@@ -22,7 +22,8 @@
 //     of 8 keys, converts, and transposes pairs of keys with byte permutes;
 //   * the running maximum moves only when a score exceeds it by more than
 //     kSlack (in log2): the accumulators are hardly ever rescaled, and P stays
-//     below 2^kSlack, far inside FP32 and both 16-bit types;
+//     below 2^(kSlack + kRaise), inside FP32 and both 16-bit types (fp16's are
+//     raised by 2^kRaise = 2^7, which keeps small weights out of its subnormals);
 //   * P is rounded to the 16-bit operand type for the product (relative
 //     2^-8 in bf16, as the output's own rounding); the output is divided by the
 //     FP32 sum of the rounded values, lse is of the FP32 values' own.
@@ -460,7 +461,7 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT, WINDOW)) vo
         for (int d = 0; d < VD; ++d) acc[nt][d] *= f;
         m[nt] = mx;
       }
-      const float mf = finite_max(m[nt]);
+      const float mf = finite_max(m[nt]) - T::kRaise;
       float p[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) p[j] = exp2_fast(__builtin_fmaf(x[j], a.scale_log2, -mf));
@@ -629,7 +630,7 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT, WINDOW)) vo
       for (int i = 0; i < VD / 2; i += 4) *reinterpret_cast<u32x4_t*>(dst + 2 * i) = u32x4_t{w[i], w[i + 1], w[i + 2], w[i + 3]};
     }
     if (a.lse != nullptr && part == 0)
-      a.lse[(int64_t)(row0 + rr) * a.hq + h0 + hh] = row_lse(mm, ll.x);
+      a.lse[(int64_t)(row0 + rr) * a.hq + h0 + hh] = row_lse<T>(mm, ll.x);
   };
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {

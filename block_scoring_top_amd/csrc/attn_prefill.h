@@ -18,7 +18,7 @@
 //     transposing LDS loads; P never leaves its lane;
 //   * the running maximum moves only when a score exceeds it by more than
 //     kSlack (in log2), so the accumulators are hardly ever rescaled; P stays
-//     below 2^kSlack, far inside FP32 and both 16-bit types;
+//     below 2^(kSlack + kRaise), inside FP32 and both 16-bit types;
 //   * P is rounded to the 16-bit operand type for the product (relative
 //     2^-8 in bf16, as the output's own rounding);
 //   * K rows are XOR-swizzled by 16-byte slices with key mod 16, V rows with
@@ -296,7 +296,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prefill_kernel
       for (int d = 0; d < DT; ++d) acc[d] *= f;
       m = mn;
     }
-    const float mf = finite_max(m);
+    const float mf = finite_max(m) - T::kRaise;
     u32x4_t pf[4];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -454,7 +454,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prefill_kernel
       if (ok) *reinterpret_cast<u32x4_t*>(dst + 32 * d + 8 * (g + half)) = u32x4_t{x[0], y[0], x[1], y[1]};
     }
   if (ok && half == 0 && a.lse != nullptr)
-    a.lse[(int64_t)(row0 + rr) * a.hq + h0 + hh] = row_lse(m, l.x);
+    a.lse[(int64_t)(row0 + rr) * a.hq + h0 + hh] = row_lse<T>(m, l.x);
 }
 
 // Joins the parts of every group, in their order: a lane takes 4 channels of a

@@ -58,6 +58,7 @@ struct Bf16 {
   static constexpr uint32_t kExpMask = 0x7F807F80u, kExpLsb = 0x00800080u;  // exponent fields of a pair
   static constexpr uint32_t kOne = 0x3F80u, k64 = 0x4280u, k65 = 0x4282u;
   static constexpr float kTopScale = 0x1p125f;  // a larger scale times 6 is not finite
+  static constexpr float kRaise = 0.f;          // log2 of what attention weights are multiplied by
 };
 
 struct F16 {
@@ -88,6 +89,12 @@ struct F16 {
   static constexpr uint32_t kExpMask = 0x7C007C00u, kExpLsb = 0x04000400u;
   static constexpr uint32_t kOne = 0x3C00u, k64 = 0x5400u, k65 = 0x5410u;
   static constexpr float kTopScale = 0x1p13f;
+  // A weight of 1 relative to the running maximum is held as 2^7: with weights
+  // up to 2^8 (kSlack) still in range, weights keep all their bits down to
+  // 2^-21 of the maximum and vanish below 2^-32.  With a 1 held as 1 these
+  // would be 2^-14 and 2^-25: beside a dominating key whose values are 0, 32,768
+  // others at 2^-26 then add up to nothing.
+  static constexpr float kRaise = 7.f;
 };
 
 struct F32 {

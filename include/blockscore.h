@@ -478,8 +478,9 @@ int kv4_load(const uint8_t* codes, const uint8_t* scales, int64_t num_pages, con
  * A slot listed twice counts twice.  A row without a slot gives zeros and lse
  * -inf.  Scores, running maximum, sums and outputs are held in FP32; the
  * weights are rounded to the queries' type for their product with V, and the
- * output once.  An infinity in V is passed on with the weight that its key has;
- * a weight that is rounded to 0 may make it a NaN.
+ * output once (in fp16 a weight below 2^-32 of the largest may count as 0).  An
+ * infinity in V is passed on with the weight that its key has; a weight that is
+ * rounded to 0 may make it a NaN.
  *   q          [num_rows] rows of [q_heads][head_dim], bf16 or fp16 (dtype),
  *              ld_q elements apart (a multiple of 8, >= q_heads * head_dim).
  *   slots      [num_rows][ld_slots] int32 (NULL if ld_slots is 0); count [num_rows] int32 or NULL (all

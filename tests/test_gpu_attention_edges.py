@@ -7,9 +7,9 @@ import pytest
 import torch
 
 import block_scoring_top_amd as bst
-from attn_ref import attend_row, check_rows
+from attn_ref import attend_row, check_rows, dequantise, quantise
 from gpu_util import say
-from test_gpu_attention import _cache, _f64, _queries
+from test_gpu_attention import TYPES, _cache, _f64, _queries
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +80,116 @@ def test_split_keys_pass_an_infinity_on(kind, form, d, hq, hkv, rows, n, window)
                 bst.attn_slots(q, c2, torch.from_numpy(lists).cuda(), out[:rows, :hq], scale=scale, lse=lse[:rows], workspace=ws)
             torch.cuda.synchronize()
             check_rows(_f64(out[some, :hq]), _f64(lse[some]), want, kind, [n] * 3, vmax)
+
+# ---------------------------------------------------------------- small weights
+
+def _attend_counted(q, k, v, times, scale):
+    """attend_row over keys of which key i counts times[i] times.  Returns out, lse, A, dx and W, the sum of the weights
+    relative to the largest one."""
+    hq, d = q.shape
+    g = hq // k.shape[1]
+    out, lse, A, dx, W = np.zeros((hq, d)), np.zeros(hq), np.zeros((hq, d)), np.zeros(hq), np.zeros(hq)
+    for h in range(hq):
+        x = scale * (k[:, h // g] @ q[h])
+        p = np.exp(x - x.max()) * times
+        W[h] = p.sum()
+        out[h], A[h] = p @ v[:, h // g] / W[h], p @ np.abs(v[:, h // g]) / W[h]
+        lse[h] = x.max() + np.log(W[h])
+        S = abs(scale) * (np.abs(k[:, h // g]) @ np.abs(q[h]))
+        dx[h] = (d + 16) * 2.0 ** -24 * S.max() + np.abs(x).max() * 2.0 ** -22
+    return out, lse, A, dx, W
+
+
+def _check_counted(got, got_lse, want, kind, n, v):
+    """The bounds of attn_ref.py, fp16's term made sharper: a weight is held as
+    2^7 times its ratio to the running maximum, which is never above the row's.
+    Below 2^-14 that is off by 2^-25 at most, 2^-32 of the largest weight; n such
+    errors, in the products (times max |v|) and in the sum (times |out|), over W.
+    The output's own rounding below fp16's normal range: 2^-25."""
+    u = 2.0 ** -11 if kind == "f16" else 2.0 ** -8
+    vmax = np.abs(v).max()
+    for r, (out, lse, A, dx, W) in enumerate(want):
+        tol = A * (u + 2 * dx[:, None] + 2.0 ** -21 + 2 * n * 2.0 ** -24) + 2 * u * np.abs(out) + 2.0 ** -40
+        if kind == "f16":
+            tol = tol + 2.0 ** -25 + n * 2.0 ** -32 * (vmax + np.abs(out)) / W[:, None]
+        err = np.abs(got[r] - out)
+        assert (err <= tol).all(), f"row {r}: worst {(err / tol).max()} tolerances, error {err.max()} of {np.abs(out).max()}"
+        el = np.abs(got_lse[r] - lse)
+        assert (el <= dx + 2.0 ** -21 + 2 * n * 2.0 ** -24 + np.abs(lse) * 2.0 ** -22).all(), f"row {r}: lse {el.max()}"
+
+
+def _tail_inputs(form, kind, d, hq, hkv, bits, seed):
+    """Two pages of keys whose scores lie about `bits` * ln 2 below that of key 64,
+    with values near 1,024 (key 64: 0, so that the result is the others' share).
+    Channel 0 makes the distance, in numbers that both types hold exactly; the
+    rest is noise."""
+    rng = np.random.default_rng(seed)
+    k = rng.choice([-0.25, 0.0, 0.25], (128, hkv, d))
+    k[:, :, 0] = np.where(np.arange(128) == 64, 4.0, 0.0)[:, None]
+    k[:, :, 32:64] = np.round(rng.uniform(-1, 1, (128, hkv, 32)) * 2) / 2
+    v = np.where(np.arange(128) == 64, 0.0, 1024.0)[:, None, None] * rng.choice([0.5, 1.0, 1.5], (128, hkv, d))
+    q = rng.choice([-1.0, 0.0, 1.0], (1, hq, d)) / 64
+    q[:, :, 0] = np.round(bits * np.log(2) / 4 * 32) / 32
+    if form == "kv16":
+        t = TYPES[kind]
+        pool = torch.from_numpy(np.stack([k, v], 1)).to(t).cuda()
+        return q, k, v, lambda pages: bst.KV16Cache(pool[:, 0], pool[:, 1])
+    c, s = zip(quantise(k), quantise(v))
+    kq, vq = (dequantise(a, b) for a, b in zip(c, s))
+    cache = bst.KV4Cache(torch.from_numpy(np.stack(c, 2)).cuda(), torch.from_numpy(np.stack(s, 2)).cuda())
+    return q, kq, vq, lambda pages: cache
+
+
+@pytest.mark.parametrize("kind,form,d,hq,hkv", [
+    ("f16", "kv16", 64, 8, 2), ("f16", "kv16", 128, 20, 1), ("f16", "kv16", 256, 2, 1), ("f16", "kv4", 64, 4, 4),
+    ("f16", "kv4", 128, 16, 2), ("f16", "kv4", 256, 4, 1), ("bf16", "kv16", 128, 8, 1), ("bf16", "kv4", 128, 8, 1)])
+@pytest.mark.parametrize("bits,log_n", [(13, 10), (15, 12), (18, 13), (22, 14), (26, 15), (30, 15)])
+def test_slots_count_small_weights(kind, form, d, hq, hkv, bits, log_n):
+    """A dominating key beside very many whose weights are far below fp16's normal range: their share, of the output
+    as of lse, is not lost."""
+    say(f"small weights {kind} {form} d={d} hq={hq} bits={bits} n=2^{log_n}")
+    q, K, V, make = _tail_inputs(form, kind, d, hq, hkv, bits, d + hq)
+    n = (1 << log_n) + 77
+    rng = np.random.default_rng(bits)
+    lists = rng.integers(0, 64, n).astype(np.int32)
+    for at in (0, n // 2, n - 1):
+        x = lists.copy()
+        x[at] = 64
+        times = np.bincount(x, minlength=128)
+        want = _attend_counted(q[0], K[:65], V[:65], times[:65], 1.0)
+        qd = torch.from_numpy(q).to(TYPES[kind]).cuda()
+        out, lse = torch.empty_like(qd), torch.empty((1, hq), dtype=torch.float32, device="cuda")
+        for ws in (bst.attn_workspace("cuda"), None):            # split, no wave has all of the tail beside the key
+            bst.attn_slots(qd, make(2), torch.from_numpy(x).cuda().view(1, -1), out, scale=1.0, lse=lse, workspace=ws)
+            torch.cuda.synchronize()
+            _check_counted(_f64(out), _f64(lse), [want], kind, n, V[:65])
+
+
+@pytest.mark.parametrize("kind,form,d,hq,hkv,rows", [
+    ("f16", "kv16", 64, 8, 2, 60), ("f16", "kv16", 128, 8, 1, 70), ("f16", "kv16", 256, 4, 1, 40), ("f16", "kv4", 64, 8, 4, 120),
+    ("f16", "kv4", 128, 16, 2, 48), ("f16", "kv4", 256, 4, 1, 3), ("bf16", "kv16", 128, 8, 1, 70), ("f16", "kv16", 128, 8, 1, 1)])
+@pytest.mark.parametrize("bits,log_n", [(15, 13), (22, 15), (26, 15), (30, 15)])
+def test_windows_count_small_weights(kind, form, d, hq, hkv, rows, bits, log_n):
+    """The same through a page table that names the tail's page again and again."""
+    say(f"small weights, window {kind} {form} d={d} hq={hq} rows={rows} bits={bits} n=2^{log_n}")
+    q, K, V, make = _tail_inputs(form, kind, d, hq, hkv, bits, d + hq)
+    pages = (1 << log_n) // 64
+    q = np.tile(q, (rows, 1, 1))
+    q[:, :, 1:] *= np.random.default_rng(1).choice([-1, 1], (rows, 1, 1))
+    qd = torch.from_numpy(q).to(TYPES[kind]).cuda()
+    pos = np.arange(pages * 64 - rows, pages * 64, dtype=np.int32) - 64
+    some = [0, rows // 2, rows - 1]
+    for at in (0, pages // 2, pages - 4):
+        pt = np.zeros((1, pages), np.int32)
+        pt[0, at] = 1
+        times = np.zeros((len(some), 128))
+        for i, r in enumerate(some):
+            p = np.arange(int(pos[r]) + 1)
+            times[i] = np.bincount(pt[0, p // 64] * 64 + p % 64, minlength=128)
+        want = [_attend_counted(q[r], K, V, times[i], 1.0) for i, r in enumerate(some)]
+        out, lse = torch.empty_like(qd), torch.empty((rows, hq), dtype=torch.float32, device="cuda")
+        for ws in (bst.attn_workspace("cuda"), None):
+            bst.attn_window(qd, make(2), *[torch.from_numpy(x).cuda() for x in (pt, np.array([0, rows], np.int32), pos)], rows,
+                            1 << 40, 0, out, scale=1.0, lse=lse, workspace=ws)
+            torch.cuda.synchronize()
+            _check_counted(_f64(out[some]), _f64(lse[some]), want, kind, pages * 64, V)
