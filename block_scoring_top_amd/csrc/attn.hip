@@ -2,6 +2,8 @@
 // over how many workgroups a row's keys are split.
 #include <algorithm>
 #include <cmath>
+#include <limits>
+
 #include "attn_gather.h"
 #include "attn_prefill.h"
 
@@ -64,10 +66,12 @@ constexpr int64_t kEightWaves = 512;
 constexpr int64_t kMaxGroups = (int64_t)1 << 21;
 
 // The running maximum is of unscaled scores times the scale, which then must
-// not be negative (q changes sign instead) nor 0 (a masked -inf times 0).
+// not be negative (q changes sign instead) nor 0 (a masked -inf times 0): the
+// least positive number stands for that, under which the largest score that
+// FP32 holds is 5e-7.  (The kernels compute with subnormal numbers.)
 void set_scale(const AttnCall& c, float& scale_log2, uint32_t& flip) {
   const float s = c.scale * kLog2e;
-  scale_log2 = std::max(std::fabs(s), 1.1754944e-38f);
+  scale_log2 = std::max(std::fabs(s), std::numeric_limits<float>::denorm_min());
   flip = s < 0.f ? 0x80008000u : 0u;
 }
 

@@ -9,7 +9,7 @@ import torch
 import block_scoring_top_amd as bst
 from attn_ref import attend_row, check_rows, dequantise, quantise
 from gpu_util import say
-from test_gpu_attention import TYPES, _cache, _f64, _queries
+from test_gpu_attention import TYPES, _batch, _cache, _f64, _queries, _window_want
 
 pytestmark = pytest.mark.gpu
 
@@ -193,3 +193,27 @@ def test_windows_count_small_weights(kind, form, d, hq, hkv, rows, bits, log_n):
                             1 << 40, 0, out, scale=1.0, lse=lse, workspace=ws)
             torch.cuda.synchronize()
             _check_counted(_f64(out[some]), _f64(lse[some]), want, kind, pages * 64, V)
+
+
+# ---------------------------------------------------------------- scales
+
+@pytest.mark.parametrize("kind,big", [("bf16", 1e18), ("bf16", 1e14), ("f16", 1e3)])
+@pytest.mark.parametrize("scale", [0.0, -0.0, 1e-44, -1e-41, 3e-39, 1e-37])
+@pytest.mark.parametrize("rows", [2, 40])
+def test_small_scales_of_large_scores(kind, big, scale, rows):
+    """Large queries and keys under tiny scales and a scale of 0."""
+    say(f"scale {scale} {kind} {big} rows={rows}")
+    pt, ptr, pos, pages = _batch([200], [rows], 4)
+    cache, K, V = _cache("kv16", kind, pages, 2, 128, 12)
+    q, out, lse = _queries(rows, 8, 128, kind, 3)
+    pool = torch.stack([cache.k * big, cache.v], 1)
+    cache = bst.KV16Cache(pool[:, 0], pool[:, 1])
+    q = (q * big).contiguous()
+    assert torch.isfinite(q).all() and torch.isfinite(pool).all()
+    res, n = _window_want(_f64(q), _f64(cache.k), V, pt, ptr, pos, pages, rows, 70, 3, float(np.float32(scale)))
+    args = [torch.from_numpy(x).cuda() for x in (pt, ptr, pos)]
+    for wide in (False, True):
+        if wide:
+            args[0] = torch.nn.functional.pad(args[0], (0, 30000), value=-1)
+        bst.attn_window(q, cache, *args, rows, 70, 3, out[:rows, :8], scale=scale, lse=lse[:rows], workspace=bst.attn_workspace("cuda"))
+        check_rows(_f64(out[:rows, :8]), _f64(lse[:rows]), res, kind, n, np.abs(V).max())
