@@ -268,7 +268,8 @@ inline int check_attn_args(const void* q, int32_t dtype, int64_t ld_q, int32_t n
     return BS_ERR_ARG;
   if (dtype != BS_BF16 && dtype != BS_F16) return BS_ERR_ARG;
   if (cache_form != BS_KV_16 && cache_form != BS_KV_4) return BS_ERR_ARG;
-  if (q_heads % kv_heads != 0 || !std::isfinite(scale)) return BS_ERR_ARG;
+  // The kernels multiply by scale * log2(e), which has to be finite too.
+  if (q_heads % kv_heads != 0 || !(std::fabs(scale) <= 0x1p127f)) return BS_ERR_ARG;
   const int64_t qw = (int64_t)q_heads * head_dim, kvw = (int64_t)kv_heads * head_dim;
   if (qw > (1 << 20) || !row_stride_ok(ld_q, qw) || !row_stride_ok(ld_out, qw)) return BS_ERR_ARG;
   if (cache_form == BS_KV_16 && (!row_stride_ok(ld_cache, kvw) || ld_cache > (1 << 24))) return BS_ERR_ARG;

@@ -511,9 +511,10 @@ int kv4_load(const uint8_t* codes, const uint8_t* scales, int64_t num_pages, con
  * Both return BS_OK (also when there are no rows), BS_ERR_NULL, BS_ERR_ARG
  * (dtype not bf16 or fp16, an unknown form, head_dim, head counts, negative
  * counts, num_pages outside 1 .. 2^25 - 1, pt_stride < 1, a stride too small or
- * no multiple of 8, a pointer that is not 16-byte aligned, a scale that is not
- * finite, more than 2^21 tiles of rows times kv heads), BS_ERR_WORKSPACE (a workspace smaller than
- * BS_ATTN_WORKSPACE_BYTES) or BS_ERR_LAUNCH.
+ * no multiple of 8, a pointer that is not 16-byte aligned, a scale that is NaN
+ * or beyond 2^127 either way, more than 2^21 tiles of rows times kv heads),
+ * BS_ERR_WORKSPACE (a workspace smaller than BS_ATTN_WORKSPACE_BYTES) or
+ * BS_ERR_LAUNCH.
  */
 #define BS_ATTN_WORKSPACE_BYTES (((size_t)32 << 20) + ((size_t)64 << 10))
 int attn_slots(const void* q, int32_t dtype, int64_t ld_q, int32_t num_rows, int32_t q_heads, int32_t kv_heads,

@@ -217,3 +217,21 @@ def test_small_scales_of_large_scores(kind, big, scale, rows):
             args[0] = torch.nn.functional.pad(args[0], (0, 30000), value=-1)
         bst.attn_window(q, cache, *args, rows, 70, 3, out[:rows, :8], scale=scale, lse=lse[:rows], workspace=bst.attn_workspace("cuda"))
         check_rows(_f64(out[:rows, :8]), _f64(lse[:rows]), res, kind, n, np.abs(V).max())
+
+
+@pytest.mark.parametrize("rows", [2, 40])
+@pytest.mark.parametrize("scale", [2.0 ** 127, -(2.0 ** 127)])
+def test_the_largest_scale_of_zero_scores(rows, scale):
+    """Queries of zeros weigh all keys alike under any scale that is taken."""
+    say(f"scale {scale} rows={rows}")
+    pt, ptr, pos, pages = _batch([200], [rows], 4)
+    cache, K, V = _cache("kv4", "f16", pages, 2, 128, 12)
+    q, out, lse = _queries(rows, 8, 128, "f16", 3)
+    q = torch.zeros_like(q).contiguous()
+    res, n = _window_want(_f64(q), K, V, pt, ptr, pos, pages, rows, 70, 3, scale)
+    args = [torch.from_numpy(x).cuda() for x in (pt, ptr, pos)]
+    for wide in (False, True):
+        if wide:
+            args[0] = torch.nn.functional.pad(args[0], (0, 30000), value=-1)
+        bst.attn_window(q, cache, *args, rows, 70, 3, out[:rows, :8], scale=scale, lse=lse[:rows], workspace=bst.attn_workspace("cuda"))
+        check_rows(_f64(out[:rows, :8]), _f64(lse[:rows]), res, "f16", n, np.abs(V).max())
