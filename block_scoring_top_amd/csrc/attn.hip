@@ -218,6 +218,9 @@ int launch_attn_window(const AttnCall& c, const int32_t* page_table, int32_t pt_
   a.tiles_per_req = (int)(((int64_t)max_rows + a.rows_per_tile - 1) / a.rows_per_tile);
   const int64_t keys = std::min<int64_t>((int64_t)pt_stride * kPage, (int64_t)window + sinks + a.rows_per_tile - 1);
   const int64_t tiles = (int64_t)num_req * a.tiles_per_req;
+  // The other kernel's tiles are at most 256 times as many rows: too many for
+  // both, and for the products with heads below.
+  if (tiles > kMaxGroups * 256) return BS_ERR_ARG;
   if (!gathers(c, tiles * c.hkv * a.hblocks, keys, (int64_t)g * max_rows, num_req))
     return run_prefill(c, page_table, pt_stride, req_row_ptr, num_req, row_pos, max_rows, window, sinks, stream);
   a.page_table = page_table, a.pt_stride = pt_stride, a.req_row_ptr = req_row_ptr, a.row_pos = row_pos;
