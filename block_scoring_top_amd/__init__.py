@@ -477,7 +477,7 @@ def _kv4_store_args(k, v, slots, cache):
 
 def kv4_store(k, v, slots, cache: KV4Cache, stream=None):
     """Quantise new K/V rows into the 4-bit cache.  See ``kv4_store`` in blockscore.h."""
-    PreparedCall("kv4_store", _kv4_store_args(k, v, slots, cache), cache.device)(stream)
+    PreparedCall("kv4_store", _kv4_store_args(k, v, slots, cache), cache.device, once=True)(stream)
 
 
 def _kv4_load_args(cache, slots, k, v):
@@ -497,7 +497,7 @@ def _kv4_load_args(cache, slots, k, v):
 
 def kv4_load(cache: KV4Cache, slots, k, v, stream=None):
     """Read rows of the 4-bit cache back.  See ``kv4_load`` in blockscore.h."""
-    PreparedCall("kv4_load", _kv4_load_args(cache, slots, k, v), cache.device)(stream)
+    PreparedCall("kv4_load", _kv4_load_args(cache, slots, k, v), cache.device, once=True)(stream)
 
 
 def attn_workspace(device) -> torch.Tensor:
@@ -538,7 +538,8 @@ def _attn_slots_args(q, cache, slots, out, count=None, scale=None, lse=None, wor
 def attn_slots(q, cache, slots, out, count=None, scale=None, lse=None, workspace=None, stream=None):
     """Attention of each row over its slots (``scale`` defaults to
     1/sqrt(head_dim)).  See ``attn_slots`` in blockscore.h."""
-    PreparedCall("attn_slots", _attn_slots_args(q, cache, slots, out, count, scale, lse, workspace), q.device)(stream)
+    PreparedCall("attn_slots", _attn_slots_args(q, cache, slots, out, count, scale, lse, workspace), q.device,
+                 once=True)(stream)
 
 
 def _int32(x) -> int:
@@ -569,7 +570,7 @@ def attn_window(q, cache, page_table, req_row_ptr, row_pos, max_rows, window, si
     (``scale`` defaults to 1/sqrt(head_dim)).  See ``attn_window`` in
     blockscore.h."""
     PreparedCall("attn_window", _attn_window_args(q, cache, page_table, req_row_ptr, row_pos, max_rows, window, sinks,
-                                                  out, scale, lse, workspace), q.device)(stream)
+                                                  out, scale, lse, workspace), q.device, once=True)(stream)
 
 
 class PreparedCall:
@@ -577,14 +578,14 @@ class PreparedCall:
     behind the pointers must outlive it); ``__call__`` adds the stream and
     checks the status.  For loops that issue the same call many times."""
 
-    def __init__(self, fn: str, args: tuple, device):
+    def __init__(self, fn: str, args: tuple, device, once: bool = False):
         self.fn = fn
         self.args = args
         self.device = device
         self._f = getattr(lib(), fn)
         # Arguments as instances of their declared C types, so that a call
-        # converts nothing but the stream.
-        self._args = tuple(a if isinstance(a, t) else t(a) for a, t in zip(args, self._f.argtypes))
+        # converts nothing but the stream (worth it for more than one call).
+        self._args = args if once else tuple(a if isinstance(a, t) else t(a) for a, t in zip(args, self._f.argtypes))
 
     def __call__(self, stream=None):
         # The current stream and device are asked for by their index: about

@@ -9,9 +9,10 @@ from __future__ import annotations
 
 import torch
 
-from . import (attn_slots, attn_workspace, idx_expand_translate, idx_score_decode, idx_score_prefill, idx_select_translate,
-               idx_select_translate_planned, prepare_score, prepare_select_translate, topk_plan, topk_plan_rows,
-               topk_planned_workspace, topk_select_rows, topk_workspace)
+from . import (ATTN_WORKSPACE_BYTES, attn_slots, attn_workspace, idx_expand_translate, idx_score_decode,
+               idx_score_prefill, idx_select_translate, idx_select_translate_planned, prepare_score,
+               prepare_select_translate, topk_plan, topk_plan_rows, topk_planned_workspace, topk_select_rows,
+               topk_workspace)
 
 
 class IndexerPath:
@@ -42,7 +43,7 @@ class IndexerPath:
         self.workspace = topk_workspace(R, int(inp.max_vis), inp.k, dev)
         self.plan_buf = None          # planned selection: allocated on first use
         self.planned_workspace = None
-        self.attn_ws = None           # attention over the chosen slots: allocated on first use
+        self.attn_ws = None           # attention over the chosen slots: {stream: workspace}, allocated on first use
         self._prepared = None
 
     def _prepare(self):
@@ -132,13 +133,32 @@ class IndexerPath:
     def attend(self, q, cache, out, scale=None, lse=None, stream=None):
         """Attention of the main query heads ``q`` [num_rows, q_heads,
         head_dim] over the slots of the last ``run``, read from ``cache``
-        (``KV4Cache`` or ``KV16Cache``) into ``out``."""
-        if self.attn_ws is None:
-            # Cleared on the stream of its first use; a captured clearing
-            # would leave it as it was until the first replay.
+        (``KV4Cache`` or ``KV16Cache``) into ``out``.
+
+        Calls on different streams may overlap: each stream has a workspace of
+        its own (32 MiB, kept with the path), and so has each captured call.
+        ``run`` and the calls that read its slots are the caller's to order."""
+        if stream is None:
+            ws = self._attn_workspace(q.device)
+        else:
             with torch.cuda.stream(stream):
-                if torch.cuda.is_current_stream_capturing():
-                    raise RuntimeError("attend() must have run once before it is captured")
-                self.attn_ws = attn_workspace(q.device)
-        attn_slots(q, cache, self.slots, out, count=self.out_count, scale=scale, lse=lse, workspace=self.attn_ws,
-                   stream=stream)
+                ws = self._attn_workspace(q.device)
+        attn_slots(q, cache, self.slots, out, count=self.out_count, scale=scale, lse=lse, workspace=ws, stream=stream)
+
+    def _attn_workspace(self, device):
+        """The workspace of an attention call on the current stream."""
+        if torch.cuda.is_current_stream_capturing():
+            if self.attn_ws is None:
+                raise RuntimeError("attend() must have run once before it is captured")
+            # The graph's own memory, its counters cleared at each replay:
+            # replays may overlap with other graphs and with eager calls.
+            ws = torch.empty(ATTN_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+            ws[:64 << 10].zero_()
+            return ws
+        if self.attn_ws is None:
+            self.attn_ws = {}
+        stream = torch._C._cuda_getCurrentRawStream(device.index)
+        ws = self.attn_ws.get(stream)
+        if ws is None:
+            ws = self.attn_ws[stream] = attn_workspace(device)
+        return ws

@@ -235,3 +235,100 @@ def test_the_largest_scale_of_zero_scores(rows, scale):
             args[0] = torch.nn.functional.pad(args[0], (0, 30000), value=-1)
         bst.attn_window(q, cache, *args, rows, 70, 3, out[:rows, :8], scale=scale, lse=lse[:rows], workspace=bst.attn_workspace("cuda"))
         check_rows(_f64(out[:rows, :8]), _f64(lse[:rows]), res, "f16", n, np.abs(V).max())
+
+
+# ---------------------------------------------------------------- the path's attention on several streams
+
+def _path(B=2, hi=3000):
+    import synth
+    from block_scoring_top_amd.pipeline import IndexerPath
+    from synth.device import upload
+    inp = synth.qsa_verify_64req(B=B, lo=300, hi=hi)
+    p = IndexerPath(upload(inp, "cuda"), "decode")
+    p.run()
+    torch.cuda.synchronize()
+    return inp, p
+
+
+def _spy_on_workspaces(monkeypatch):
+    """A list to which every attend() adds its stream and its workspace's address."""
+    from block_scoring_top_amd import pipeline
+    used, real = [], pipeline.attn_slots
+
+    def spy(*a, workspace, stream, **kw):
+        used.append(((stream or torch.cuda.current_stream()).cuda_stream, workspace.data_ptr()))
+        return real(*a, workspace=workspace, stream=stream, **kw)
+
+    monkeypatch.setattr(pipeline, "attn_slots", spy)
+    return used
+
+
+def test_attend_on_two_streams_at_once(monkeypatch):
+    """Calls on different streams share nothing that they write, whichever comes first; those on one stream need no more
+    than one workspace."""
+    inp, p = _path()
+    say(f"attend on two streams, rows={inp.num_rows}")
+    R = inp.num_rows
+    cache, _, _ = _cache("kv4", "bf16", inp.num_pages, 2, 128, 11)
+    qs = [_queries(R, 16, 128, "bf16", 12 + i)[0].clone() for i in range(2)]
+    want = []
+    for q in qs:
+        o = torch.empty_like(q)
+        bst.attn_slots(q, cache, p.slots, o, count=p.out_count, workspace=bst.attn_workspace("cuda"))
+        want.append(o)
+    used = _spy_on_workspaces(monkeypatch)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[torch.empty_like(q) for _ in range(20)] for q in qs]
+    torch.cuda.synchronize()
+    for k in range(20):
+        for i in range(2):
+            p.attend(qs[i], cache, outs[i][k], stream=streams[i])
+    torch.cuda.synchronize()
+    assert len({s for s, _ in used}) == 2 and len(set(used)) == 2 and len({w for _, w in used}) == 2
+    for i in range(2):
+        for o in outs[i]:
+            assert torch.equal(o, want[i])
+
+
+def test_captured_attends_share_no_workspace(monkeypatch):
+    """Two graphs captured from one path, replayed at once on two streams and beside eager calls."""
+    inp, p = _path()
+    say(f"captured attends, rows={inp.num_rows}")
+    R = inp.num_rows
+    cache, _, _ = _cache("kv4", "bf16", inp.num_pages, 2, 128, 11)
+    qs = [torch.empty((R, 16, 128), dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    outs = [torch.empty_like(q) for q in qs]
+    p.attend(qs[0].normal_(generator=torch.Generator(device="cuda").manual_seed(1)), cache, outs[0])
+    graphs, seen = [], []
+    used = _spy_on_workspaces(monkeypatch)
+    p.attend(qs[0], cache, outs[0])
+    seen.append({w for _, w in used})
+    for i in range(2):
+        used.clear()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            p.attend(qs[i], cache, outs[i])
+            p.attend(qs[i], cache, outs[i])                      # as of two layers: they may share
+        graphs.append(g)
+        seen.append({w for _, w in used})
+    assert not (seen[0] & seen[1] or seen[0] & seen[2] or seen[1] & seen[2])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ws = bst.attn_workspace("cuda")
+    for rep in range(6):
+        want = []
+        for i, q in enumerate(qs):
+            q.copy_(torch.randn(q.shape, generator=torch.Generator(device="cuda").manual_seed(10 * rep + i), device="cuda"))
+            o = torch.empty_like(q)
+            bst.attn_slots(q, cache, p.slots, o, count=p.out_count, workspace=ws)
+            want.append(o)
+            outs[i].fill_(-77.0)
+        torch.cuda.synchronize()
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                for _ in range(4):
+                    g.replay()
+        for _ in range(8):
+            p.attend(qs[2], cache, outs[2])
+        torch.cuda.synchronize()
+        for i in range(3):
+            assert torch.equal(outs[i], want[i]), (rep, i)
