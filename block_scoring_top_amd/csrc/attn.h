@@ -12,6 +12,11 @@ namespace bs {
 
 // How far (in log2) a score may exceed the running maximum before that moves.
 constexpr float kSlack = 8.f;
+// Running maxima past this are exact to no more than 2^-4 (in log2), and more
+// than that lies between a score's product with the scale as the maximum has it
+// and as an fma holds it: weights are then of the rounded products.  Of the
+// others they left fp16's range from scores of 2^26 on, and FP32's from 2^31.
+constexpr float kHugeScore = 0x1p20f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <class F, int... I>
@@ -66,6 +71,13 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 // A maximum to subtract: 0 in place of -inf, so that -inf scores give 0 and
 // not NaN.
 __device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.f : m; }
+
+// x * scale rounded, whatever it is used in.
+__device__ __forceinline__ float rounded_product(float x, float scale) {
+  float y = x * scale;
+  asm("" : "+v"(y));
+  return y;
+}
 
 // The 16-bit values of a pair of packed pairs, transposed: lo holds both low
 // halves, hi both high halves.

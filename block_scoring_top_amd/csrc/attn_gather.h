@@ -243,6 +243,7 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT, WINDOW)) vo
   f32x4_t acc[NT][VD];
   float m[NT];
   Sums l[NT];
+  uint64_t huge = 0;  // of lanes with a maximum past kHugeScore
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     m[nt] = -INFINITY, l[nt] = Sums{0.f, 0.f};
@@ -452,19 +453,26 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT, WINDOW)) vo
       float mx = x[0];
 #pragma unroll
       for (int j = 1; j < 8; ++j) mx = max_nan(mx, x[j]);
-      mx = rows_max(mx) * a.scale_log2;
-      if (ballot(mx > m[nt] + kSlack)) {
+      mx = rounded_product(rows_max(mx), a.scale_log2);
+      float scale = a.scale_log2, base = finite_max(m[nt]);  // of the weights
+      if (ballot(mx - m[nt] > kSlack) | huge) {
         mx = fmaxf(m[nt], mx);
-        const float f = exp2_fast(m[nt] - finite_max(mx));
+        base = finite_max(mx);
+        const float f = exp2_fast(m[nt] - base);
         l[nt] *= f;
 #pragma unroll
         for (int d = 0; d < VD; ++d) acc[nt][d] *= f;
         m[nt] = mx;
+        huge |= ballot(fabsf(base) > kHugeScore);
+        if (huge) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = rounded_product(x[j], scale) - base;
+          scale = 1.f, base = 0.f;
+        }
       }
-      const float mf = finite_max(m[nt]) - T::kRaise;
       float p[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) p[j] = exp2_fast(__builtin_fmaf(x[j], a.scale_log2, -mf));
+      for (int j = 0; j < 8; ++j) p[j] = exp2_fast(__builtin_fmaf(x[j], scale, T::kRaise - base));
       l[nt].x += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
       pfr[nt] = u32x4_t{T::pack(p[0], p[1]), T::pack(p[2], p[3]), T::pack(p[4], p[5]), T::pack(p[6], p[7])};
       l[nt].y = add_rounded<T>(pfr[nt], l[nt].y);

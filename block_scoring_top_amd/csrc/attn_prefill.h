@@ -154,6 +154,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prefill_kernel
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[d][i] = 0.f;
   float m = -INFINITY;    // running maximum (scaled)
+  uint64_t huge = 0;      // of lanes with one past kHugeScore
   Sums l = {0.f, 0.f};    // this half's share of the sums
 
   auto page_pos = [&](int i) { return i < sink_pages ? i : wp0 + (i - sink_pages); };
@@ -286,23 +287,32 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prefill_kernel
     {
       const uint32_t u = __float_as_uint(mx);
       auto x = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-      mx = max_nan(__uint_as_float(x[0]), __uint_as_float(x[1])) * a.scale_log2;
+      mx = rounded_product(max_nan(__uint_as_float(x[0]), __uint_as_float(x[1])), a.scale_log2);
     }
-    if (ballot(mx > m + kSlack)) {
+    float scale = a.scale_log2, base = finite_max(m);  // of the weights
+    if (ballot(mx - m > kSlack) | huge) {
       const float mn = fmaxf(m, mx);
-      const float f = exp2_fast(m - finite_max(mn));
+      base = finite_max(mn);
+      const float f = exp2_fast(m - base);
       l *= f;
 #pragma unroll
       for (int d = 0; d < DT; ++d) acc[d] *= f;
       m = mn;
+      huge |= ballot(fabsf(base) > kHugeScore);
+      if (huge) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[j][i] = rounded_product(s[j][i], scale) - base;
+        scale = 1.f, base = 0.f;
+      }
     }
-    const float mf = finite_max(m) - T::kRaise;
     u32x4_t pf[4];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       float p[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) p[i] = exp2_fast(__builtin_fmaf(s[j][i], a.scale_log2, -mf));
+      for (int i = 0; i < 16; ++i) p[i] = exp2_fast(__builtin_fmaf(s[j][i], scale, T::kRaise - base));
       float x = 0.f;
 #pragma unroll
       for (int i = 0; i < 16; i += 4) x += (p[i] + p[i + 1]) + (p[i + 2] + p[i + 3]);

@@ -332,3 +332,64 @@ def test_captured_attends_share_no_workspace(monkeypatch):
         torch.cuda.synchronize()
         for i in range(3):
             assert torch.equal(outs[i], want[i]), (rep, i)
+
+
+# ---------------------------------------------------------------- very large scores
+
+@pytest.mark.parametrize("d,hq,hkv", [(64, 8, 2), (128, 4, 4), (128, 20, 1), (256, 4, 1)])
+@pytest.mark.parametrize("kind,form,bits", [("bf16", "kv16", b) for b in (3, 20, 24, 27, 31, 40, 90)] +
+                         [("f16", "kv16", b) for b in (3, 18, 23, 25)] + [("bf16", "kv4", b) for b in (3, 24, 31, 100)] +
+                         [("f16", "kv4", b) for b in (3, 17, 23, 26)])
+@pytest.mark.parametrize("rows", [1, 6, 70])
+def test_very_large_scores(kind, form, bits, d, hq, hkv, rows):
+    """Scores of small whole numbers times 2^bits, exact in FP32: a row's result is the mean of the values of its best
+    keys, the others' weights being 0 (below exp(-8) for 3 bits: within the bound of the sum over 300 keys)."""
+    say(f"scores of 2^{bits} {kind} {form} d={d} hq={hq} rows={rows}")
+    rng = np.random.default_rng(bits + d)
+    ctx = [300]
+    pt, ptr, pos, pages = _batch(ctx, [rows], 8)
+    c = rng.integers(-6, 3, (pages * 64, hkv))
+    at = pt[0, np.arange(300) // 64] * 64 + np.arange(300) % 64
+    c[at[[5, 37, 100, 229]]] = 3                                 # the best: equal, in different steps of the kernels
+    c[at[10:30]] = -6
+    c = np.where(c == 3, 6, np.where(np.abs(c) == 5, 4, c)).astype(np.float64)    # numbers of the 4-bit form
+    v = rng.choice([-6, -4, -3, -2, -1.5, -1, -.5, .5, 1, 1.5, 2, 3, 4, 6], (pages * 64, hkv, d))
+    k = np.zeros((pages * 64, hkv, d))
+    k[:, :, 7] = c
+    half = bits // 2
+    q = np.zeros((rows, hq, d))
+    q[:, :, 7] = 2.0 ** (bits - half)
+    if form == "kv16":
+        pool = torch.from_numpy(np.stack([k * 2.0 ** half, v], 1)).to(TYPES[kind]).cuda()
+        cache = bst.KV16Cache(pool[:, 0], pool[:, 1])
+    else:
+        mag = np.array([0, .5, 1, 1.5, 2, 3, 4, 6])
+        codes = lambda x: (np.abs(np.abs(x)[..., None] - mag).argmin(-1) + 8 * (x < 0)).astype(np.uint8)  # noqa: E731
+        pack = lambda x: x[..., 0::2] | x[..., 1::2] << 4  # noqa: E731
+        s = np.full((pages * 64, hkv, 2, d // 32), 127, np.uint8)
+        s[:, :, 0] += np.uint8(half)
+        cache = bst.KV4Cache(torch.from_numpy(np.stack([pack(codes(k)), pack(codes(v))], 2)).cuda(), torch.from_numpy(s).cuda())
+    qd = torch.from_numpy(q).to(TYPES[kind]).cuda()
+    assert np.array_equal(_f64(qd), q)
+    u = 2.0 ** -8 if kind == "bf16" else 2.0 ** -11
+    out, lse = torch.empty_like(qd), torch.empty((rows, hq), dtype=torch.float32, device="cuda")
+    args = [torch.from_numpy(x).cuda() for x in (pt, ptr, pos)]
+    for wide in (False, True):
+        if wide:
+            args[0] = torch.nn.functional.pad(args[0], (0, 30000), value=-1)
+        for ws in (bst.attn_workspace("cuda"), None):
+            out.fill_(-77.0), lse.fill_(-77.0)
+            bst.attn_window(qd, cache, *args, rows, 1 << 40, 0, out, scale=1.0, lse=lse, workspace=ws)
+            torch.cuda.synchronize()
+            for r in {0, rows // 2, rows - 1}:
+                seen = at[:int(pos[r]) + 1]
+                for h in range(hq):
+                    g = h // (hq // hkv)
+                    x = c[seen, g] * 2.0 ** bits
+                    w = np.exp(x - x.max())
+                    want = w @ v[seen, g] / w.sum()
+                    wl = x.max() + np.log(w.sum())
+                    tol = (w @ np.abs(v[seen, g]) / w.sum()) * (u + 2.0 ** -10) + 2 * u * np.abs(want)
+                    got = _f64(out[r, h])
+                    assert (np.abs(got - want) <= tol).all(), (r, h, got[:4], want[:4])
+                    assert abs(float(lse[r, h]) - wl) <= abs(wl) * 2.0 ** -20 + 2.0 ** -12, (r, h, float(lse[r, h]), wl)
