@@ -9,7 +9,7 @@ import torch
 import block_scoring_top_amd as bst
 from attn_ref import attend_row, check_rows, dequantise, quantise
 from gpu_util import say
-from test_gpu_attention import TYPES, _batch, _cache, _f64, _queries, _window_want
+from test_gpu_attention import TYPES, _batch, _cache, _f64, _gen, _queries, _window_want
 
 pytestmark = pytest.mark.gpu
 
@@ -393,3 +393,163 @@ def test_very_large_scores(kind, form, bits, d, hq, hkv, rows):
                     got = _f64(out[r, h])
                     assert (np.abs(got - want) <= tol).all(), (r, h, got[:4], want[:4])
                     assert abs(float(lse[r, h]) - wl) <= abs(wl) * 2.0 ** -20 + 2.0 ** -12, (r, h, float(lse[r, h]), wl)
+
+
+# ---------------------------------------------------------------- the 4-bit cache over its whole range
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+def test_every_scale_and_code_reads_back(kind):
+    """Every code with every scale byte, those that kv4_store does not write (0 .. 6, 253, 254) among them, in each type,
+    rounded once."""
+    say(f"kv4_load of every scale {kind}")
+    scales = np.arange(256).astype(np.uint8)
+    n = len(scales)
+    codes = np.zeros((n, 1, 2, 32), np.uint8)
+    codes[..., :16] = np.arange(8)[[0, 1, 2, 3, 4, 5, 6, 7] * 2] * 2 % 16 | (np.arange(16) << 4) & 0xF0
+    codes[..., 16:] = np.arange(16) | (15 - np.arange(16)) << 4
+    sc = np.full((n, 1, 2, 2), 127, np.uint8)
+    sc[:] = scales[:, None, None, None]
+    cache = bst.KV4Cache(torch.from_numpy(codes).cuda(), torch.from_numpy(sc).cuda())
+    k, v = (torch.empty((n, 1, 64), dtype=TYPES[kind], device="cuda") for _ in range(2))
+    bst.kv4_load(cache, torch.arange(n, dtype=torch.int32, device="cuda"), k, v)
+    want = torch.from_numpy(dequantise(codes, sc)).to(TYPES[kind])
+    for i, got in enumerate((k, v)):
+        np.testing.assert_array_equal(_f64(got), _f64(want[:, :, i]))
+
+
+@pytest.mark.parametrize("rows", [1, 6, 150])
+@pytest.mark.parametrize("d,hq,hkv", [(64, 4, 2), (128, 8, 1), (256, 4, 1)])
+@pytest.mark.parametrize("window", [40, 1 << 30])
+def test_fp16_over_large_and_small_scales(rows, d, hq, hkv, window):
+    """4-bit values past fp16's range are infinities to fp16 queries (in V: K stays in it), those below it are rounded; where
+    a row does not see them they do not reach it."""
+    say(f"fp16 over large and small scales rows={rows} d={d} window={window}")
+    pt, ptr, pos, pages = _batch([200], [rows], 8)
+    cache, K, V = _cache("kv4", "f16", pages, hkv, d, 41)
+    rng = np.random.default_rng(5)
+    scales = cache.scales.cpu().numpy()
+    scales[:, :, 1] = rng.integers(127 - 26, 127 + 12, scales[:, :, 1].shape)    # 2^-26 .. 2^11
+    scales[:, :, 0, 0] -= 8                                                       # small keys in one group
+    for p in (199, 198, 130, 90, 20):
+        s = int(pt[0, p // 64]) * 64 + p % 64
+        scales[s, :, 1] = rng.integers(127 + 13, 127 + 18, scales[s, :, 1].shape)   # from 2^13: 6 * 2^14 is past the range
+    cache = bst.KV4Cache(cache.codes, torch.from_numpy(scales).cuda())
+    kv = torch.from_numpy(dequantise(cache.codes.cpu().numpy(), scales)).to(torch.float16).double().numpy()
+    K, V = kv[:, :, 0], kv[:, :, 1]
+    q, out, lse = _queries(rows, hq, d, "f16", 2)
+    res, n = _window_want(_f64(q), K, V, pt, ptr, pos, pages, rows, window, 4, 0.09)
+    assert any(np.isinf(r[0]).any() for r in res)
+    args = [torch.from_numpy(x).cuda() for x in (pt, ptr, pos)]
+    for wide in (False, True):                                   # a wide page table: the prefill kernel, its pages split
+        if wide:
+            args[0] = torch.nn.functional.pad(args[0], (0, 30000), value=-1)
+        for ws in (bst.attn_workspace("cuda"), None):
+            out.fill_(-77.0), lse.fill_(-77.0)
+            bst.attn_window(q, cache, *args, rows, window, 4, out[:rows, :hq], scale=0.09, lse=lse[:rows], workspace=ws)
+            torch.cuda.synchronize()
+            check_rows(_f64(out[:rows, :hq]), _f64(lse[:rows]), res, "f16", n, np.abs(V[np.isfinite(V)]).max())
+
+
+# ---------------------------------------------------------------- the largest launches
+
+def _one_key_cache(kind, form):
+    """Two pages of one head of 64 whose values both forms hold exactly."""
+    k = torch.randint(-6, 7, (128, 1, 64), generator=_gen(1), device="cuda")
+    v = torch.randint(-3, 4, (128, 1, 64), generator=_gen(2), device="cuda")
+    pool = torch.stack([k, v], 1).to(TYPES[kind])
+    if form == "kv16":
+        return bst.KV16Cache(pool[:, 0], pool[:, 1]), pool[:, 1]
+    cache = bst.KV4Cache.empty(2, 1, 64, "cuda")
+    bst.kv4_store(pool[:, 0].contiguous(), pool[:, 1].contiguous(), torch.arange(128, dtype=torch.int32, device="cuda"), cache)
+    return cache, pool[:, 1]
+
+
+@pytest.mark.parametrize("form", ["kv4", "kv16"])
+def test_two_million_rows_of_one_key(form):
+    """The most row tiles that a call takes (2^21), by lists and by windows: each row is the value of its one key."""
+    n = 1 << 21
+    say(f"2^21 rows {form}")
+    cache, v = _one_key_cache("bf16", form)
+    q = torch.randn((n, 1, 64), generator=_gen(3), device="cuda").bfloat16()
+    at = torch.randint(-1, 128, (n,), generator=_gen(4), device="cuda", dtype=torch.int32)
+    want = torch.where((at >= 0)[:, None, None], v[at.clamp(min=0).long()], 0)
+    out = torch.full_like(q, -77.0)
+    bst.attn_slots(q, cache, at.view(-1, 1), out, workspace=bst.attn_workspace("cuda"))
+    assert torch.equal(out, want)
+    out.fill_(-77.0)
+    table = torch.tensor([[1, 0]], dtype=torch.int32, device="cuda").repeat(n, 1)
+    ptr = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    want = torch.where((at >= 0)[:, None, None], v[(at.clamp(min=0).long() + 64) % 128], 0)
+    bst.attn_window(q, cache, table, ptr, at, 1, 1, 0, out, workspace=bst.attn_workspace("cuda"))
+    assert torch.equal(out, want)
+    with pytest.raises(bst.BlockScoreError):
+        q2 = torch.empty((n + 1, 1, 64), dtype=torch.bfloat16, device="cuda")
+        bst.attn_slots(q2, cache, torch.zeros((n + 1, 1), dtype=torch.int32, device="cuda"), torch.empty_like(q2))
+
+
+@pytest.mark.parametrize("form", ["kv4", "kv16"])
+def test_a_million_requests_in_the_prefill_kernel(form):
+    """2^20 requests of up to 300 rows (two tiles each, the most that the prefill kernel takes), three of which have any."""
+    n = 1 << 20
+    say(f"2^20 requests {form}")
+    cache, v = _one_key_cache("bf16", form)
+    counts = torch.zeros(n, dtype=torch.int64, device="cuda")
+    counts[0], counts[n // 2 + 3], counts[n - 1] = 300, 257, 1
+    ptr = torch.nn.functional.pad(counts.cumsum(0), (1, 0)).int()
+    rows = int(counts.sum())
+    q = torch.randn((rows, 1, 64), generator=_gen(3), device="cuda").bfloat16()
+    at = torch.randint(-1, 128, (rows,), generator=_gen(4), device="cuda", dtype=torch.int32)
+    table = torch.tensor([[1, 0]], dtype=torch.int32, device="cuda").repeat(n, 1)
+    want = torch.where((at >= 0)[:, None, None], v[(at.clamp(min=0).long() + 64) % 128], 0)
+    out = torch.full_like(q, -77.0)
+    bst.attn_window(q, cache, table, ptr, at, 300, 1, 0, out, workspace=bst.attn_workspace("cuda"))
+    assert torch.equal(out, want)
+
+
+def test_store_and_load_of_more_pieces_than_a_launch_takes():
+    """16,500 rows x 8,192 heads of 64: 2^31 pieces of 8 channels and some, in two launches each."""
+    T, hkv, d = 16500, 8192, 64
+    say("kv4 of more than 2^31 pieces")
+    x = torch.empty((T, hkv, d), dtype=torch.float16, device="cuda").normal_(generator=_gen(1))
+    pages = -(-T // 64)
+    cache = bst.KV4Cache(torch.empty((pages * 64, hkv, 2, 32), dtype=torch.uint8, device="cuda"),
+                         torch.empty((pages * 64, hkv, 2, 2), dtype=torch.uint8, device="cuda"))
+    slots = (T - 1 - torch.arange(T, device="cuda")).int()
+    bst.kv4_store(x, x, slots, cache)
+    some = [0, 1, 16382, 16383, 16384, 16385, T - 1]
+    for i in some:
+        c, s = quantise(_f64(x[i]))
+        for which in range(2):
+            np.testing.assert_array_equal(cache.codes[T - 1 - i, :, which].cpu().numpy(), c)
+            np.testing.assert_array_equal(cache.scales[T - 1 - i, :, which].cpu().numpy(), s)
+    y = torch.zeros_like(x)
+    bst.kv4_load(cache, slots, y, x)                             # K into y, V over the input
+    assert torch.equal(x, y)
+    for i in some:
+        np.testing.assert_array_equal(_f64(y[i]), dequantise(cache.codes[T - 1 - i, :, 0].cpu().numpy(),
+                                                             cache.scales[T - 1 - i, :, 0].cpu().numpy()))
+    del x, y, cache
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("form", ["kv4", "kv16"])
+def test_a_list_of_almost_2_to_the_31_entries(form):
+    """Counts within a step of 2^31: the entries are -1 but for some at the front, in the middle and at the end."""
+    say(f"a list of 2^31 - 1 entries {form}")
+    n = 2**31 - 1
+    cache, K, V = _cache(form, "bf16", 4, 1, 128, 3)
+    at = np.r_[np.arange(40), 2**30 + np.arange(70), n - 33 + np.arange(33)]
+    slots = np.random.default_rng(2).integers(0, 256, len(at)).astype(np.int32)
+    lists = torch.full((1, n), -1, dtype=torch.int32, device="cuda")
+    lists[0, torch.from_numpy(at).cuda()] = torch.from_numpy(slots).cuda()
+    q, out, lse = _queries(1, 4, 128, "bf16", 4)
+    ws = bst.attn_workspace("cuda")
+    for count in (n, n - 1, n - 32, None):
+        s = slots if count is None else slots[at < count]
+        want = attend_row(_f64(q[0]), K[s], V[s], 128 ** -0.5)
+        c = None if count is None else torch.tensor([count], dtype=torch.int32, device="cuda")
+        bst.attn_slots(q, cache, lists, out[:1, :4], count=c, lse=lse[:1], workspace=ws)
+        torch.cuda.synchronize()
+        check_rows(_f64(out[:1, :4]), _f64(lse[:1]), [want], "bf16", [len(s)], np.abs(V).max())
+    del lists
+    torch.cuda.empty_cache()
