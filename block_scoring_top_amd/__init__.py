@@ -461,6 +461,13 @@ def _ld(t: torch.Tensor) -> int:
     return int(t.stride(0)) if t.shape[0] > 1 else int(t.shape[1] * t.shape[2])
 
 
+def _size(n) -> int:
+    """A size for an int32 argument (which would wrap a larger one)."""
+    if n > 2**31 - 1:
+        raise ValueError(f"a size of {n} is more than 2^31 - 1")
+    return int(n)
+
+
 def _kv4_store_args(k, v, slots, cache):
     """Checked argument tuple of a ``kv4_store`` call (all but the stream)."""
     dev = cache.device
@@ -471,7 +478,7 @@ def _kv4_store_args(k, v, slots, cache):
     if slots.numel() != k.shape[0]:
         raise ValueError("slots must hold num_tok entries")
     return (_rows_ptr(k, tuple(_DTYPES), "k", dev), _rows_ptr(v, tuple(_DTYPES), "v", dev), _DTYPES[k.dtype], _ld(k),
-            _ld(v), _ptr(slots, _I32, "slots", dev), int(k.shape[0]), cache.kv_heads, cache.head_dim,
+            _ld(v), _ptr(slots, _I32, "slots", dev), _size(k.shape[0]), cache.kv_heads, cache.head_dim,
             _ptr(cache.codes, _U8, "codes", dev), _ptr(cache.scales, _U8, "scales", dev), cache.num_pages)
 
 
@@ -490,7 +497,7 @@ def _kv4_load_args(cache, slots, k, v):
     if slots.numel() != k.shape[0]:
         raise ValueError("slots must hold one entry per row of k")
     return (_ptr(cache.codes, _U8, "codes", dev), _ptr(cache.scales, _U8, "scales", dev), cache.num_pages,
-            _ptr(slots, _I32, "slots", dev), int(k.shape[0]), cache.kv_heads, cache.head_dim,
+            _ptr(slots, _I32, "slots", dev), _size(k.shape[0]), cache.kv_heads, cache.head_dim,
             _rows_ptr(k, tuple(_DTYPES), "k", dev), _rows_ptr(v, tuple(_DTYPES), "v", dev), _DTYPES[k.dtype], _ld(k),
             _ld(v))
 
@@ -517,7 +524,7 @@ def _attn_common(q, cache, out, scale, lse, workspace):
         raise ValueError("lse must be [num_rows, q_heads]")
     half = (torch.bfloat16, torch.float16)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    head = (_rows_ptr(q, half, "q", dev), _DTYPES[q.dtype], _ld(q), int(q.shape[0]), int(q.shape[1]), cache.kv_heads,
+    head = (_rows_ptr(q, half, "q", dev), _DTYPES[q.dtype], _ld(q), _size(q.shape[0]), int(q.shape[1]), cache.kv_heads,
             cache.head_dim, *cache._args(q.dtype, dev))
     tail = (float(scale) if scale is not None else 1.0 / math.sqrt(cache.head_dim), _rows_ptr(out, half, "out", dev),
             _ld(out), _ptr(lse, _F32, "lse", dev), _ptr(workspace, _U8, "workspace", dev), ws_bytes)
@@ -532,7 +539,7 @@ def _attn_slots_args(q, cache, slots, out, count=None, scale=None, lse=None, wor
         raise ValueError("slots must be [num_rows, ld_slots]")
     if count is not None and count.numel() != q.shape[0]:
         raise ValueError("count must hold num_rows entries")
-    return (*head, _ptr(slots, _I32, "slots", dev), int(slots.shape[1]), _ptr(count, _I32, "count", dev), *tail)
+    return (*head, _ptr(slots, _I32, "slots", dev), _size(slots.shape[1]), _ptr(count, _I32, "count", dev), *tail)
 
 
 def attn_slots(q, cache, slots, out, count=None, scale=None, lse=None, workspace=None, stream=None):
@@ -559,8 +566,8 @@ def _attn_window_args(q, cache, page_table, req_row_ptr, row_pos, max_rows, wind
         raise ValueError("page_table must be [num_req, pt_stride]")
     if row_pos.numel() != q.shape[0]:
         raise ValueError("row_pos must hold num_rows entries")
-    return (*head, _ptr(page_table, _I32, "page_table", dev), int(page_table.shape[1]),
-            _ptr(req_row_ptr, _I32, "req_row_ptr", dev), B, _ptr(row_pos, _I32, "row_pos", dev), *map(_int32, (
+    return (*head, _ptr(page_table, _I32, "page_table", dev), _size(page_table.shape[1]),
+            _ptr(req_row_ptr, _I32, "req_row_ptr", dev), _size(B), _ptr(row_pos, _I32, "row_pos", dev), *map(_int32, (
                 max_rows, window, sinks)), *tail)
 
 

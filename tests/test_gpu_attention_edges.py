@@ -553,3 +553,21 @@ def test_a_list_of_almost_2_to_the_31_entries(form):
         check_rows(_f64(out[:1, :4]), _f64(lse[:1]), [want], "bf16", [len(s)], np.abs(V).max())
     del lists
     torch.cuda.empty_cache()
+
+
+def test_lists_wider_than_32_bits_are_refused():
+    """2^32 + 3 entries a row are not taken for 3."""
+    say("lists of 2^32 + 3 entries")
+    cache, _ = _one_key_cache("bf16", "kv4")
+    q = torch.zeros((1, 1, 64), dtype=torch.bfloat16, device="cuda")
+    lists = torch.empty((1, 2**32 + 3), dtype=torch.int32, device="cuda")
+    lists[0, :3] = -1
+    with pytest.raises(ValueError, match="2\\^31"):
+        bst.attn_slots(q, cache, lists, torch.empty_like(q))
+    with pytest.raises(ValueError, match="2\\^31"):
+        bst.prepare_attn_slots(q, cache, lists, torch.empty_like(q))
+    one = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="2\\^31"):
+        bst.attn_window(q, cache, lists, one, one[:1], 1, 1, 0, torch.empty_like(q))
+    del lists
+    torch.cuda.empty_cache()
