@@ -154,7 +154,6 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prefill_kernel
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[d][i] = 0.f;
   float m = -INFINITY;    // running maximum (scaled)
-  uint64_t huge = 0;      // of lanes with one past kHugeScore
   Sums l = {0.f, 0.f};    // this half's share of the sums
 
   auto page_pos = [&](int i) { return i < sink_pages ? i : wp0 + (i - sink_pages); };
@@ -289,23 +288,21 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prefill_kernel
       auto x = __builtin_amdgcn_permlane32_swap(u, u, false, false);
       mx = rounded_product(max_nan(__uint_as_float(x[0]), __uint_as_float(x[1])), a.scale_log2);
     }
-    float scale = a.scale_log2, base = finite_max(m);  // of the weights
-    if (ballot(mx - m > kSlack) | huge) {
+    if (ballot(mx - m > kSlack)) {
       const float mn = fmaxf(m, mx);
-      base = finite_max(mn);
-      const float f = exp2_fast(m - base);
+      const float f = exp2_fast(m - finite_max(mn));
       l *= f;
 #pragma unroll
       for (int d = 0; d < DT; ++d) acc[d] *= f;
       m = mn;
-      huge |= ballot(fabsf(base) > kHugeScore);
-      if (huge) {
+    }
+    float scale = a.scale_log2, base = finite_max(m);  // of the weights
+    if constexpr (decltype(careful_c)::value) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) s[j][i] = rounded_product(s[j][i], scale) - base;
-        scale = 1.f, base = 0.f;
-      }
+        for (int i = 0; i < 16; ++i) s[j][i] = rounded_product(s[j][i], scale) - base;
+      scale = 1.f, base = 0.f;
     }
     u32x4_t pf[4];
 #pragma unroll
@@ -401,7 +398,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prefill_kernel
   // A masked weight is 0, and 0 times an infinity or a NaN of V is NaN in rows
   // that do not see it.  Such values show in the result: if a wave's is not
   // finite, the workgroup starts over with masked pages done carefully.  (Care
-  // from the start made a masked page cost 2.8 times an unmasked one.)
+  // from the start made a masked page cost 2.8 times an unmasked one.)  So it
+  // does, with weights of rounded products on all pages, where maxima are huge.
   {
     float top = l.x;
 #pragma unroll
@@ -409,7 +407,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prefill_kernel
 #pragma unroll
       for (int k = 0; k < 16; k += 2) top = max_nan(max_nan(top, fabsf(acc[d][k])), fabsf(acc[d][k + 1]));
     __shared__ uint32_t not_finite[NW];
-    const bool bad = ballot(!(top < INFINITY)) != 0;
+    const bool bad = ballot(!(top < INFINITY) || fabsf(finite_max(m)) > kHugeScore) != 0;
     if (lane == 0) not_finite[wave] = bad;
     __syncthreads();
     uint32_t any = 0;

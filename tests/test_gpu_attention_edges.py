@@ -341,10 +341,11 @@ def test_captured_attends_share_no_workspace(monkeypatch):
                          [("f16", "kv16", b) for b in (3, 18, 23, 25)] + [("bf16", "kv4", b) for b in (3, 24, 31, 100)] +
                          [("f16", "kv4", b) for b in (3, 17, 23, 26)])
 @pytest.mark.parametrize("rows", [1, 6, 70])
-def test_very_large_scores(kind, form, bits, d, hq, hkv, rows):
-    """Scores of small whole numbers times 2^bits, exact in FP32: a row's result is the mean of the values of its best
-    keys, the others' weights being 0 (below exp(-8) for 3 bits: within the bound of the sum over 300 keys)."""
-    say(f"scores of 2^{bits} {kind} {form} d={d} hq={hq} rows={rows}")
+@pytest.mark.parametrize("scale", [1.0, 0.7, -1.7])
+def test_very_large_scores(kind, form, bits, d, hq, hkv, rows, scale):
+    """Products of small whole numbers times 2^bits, exact in FP32: keys with the best of them share a row's result. The
+    scales make their products with log2(e) be rounded up, down and not at all."""
+    say(f"scores of 2^{bits} {kind} {form} d={d} hq={hq} rows={rows} scale={scale}")
     rng = np.random.default_rng(bits + d)
     ctx = [300]
     pt, ptr, pos, pages = _batch(ctx, [rows], 8)
@@ -358,7 +359,8 @@ def test_very_large_scores(kind, form, bits, d, hq, hkv, rows):
     k[:, :, 7] = c
     half = bits // 2
     q = np.zeros((rows, hq, d))
-    q[:, :, 7] = 2.0 ** (bits - half)
+    q[:, :, 7] = np.copysign(2.0 ** (bits - half), scale)
+    scale = float(np.float32(scale))
     if form == "kv16":
         pool = torch.from_numpy(np.stack([k * 2.0 ** half, v], 1)).to(TYPES[kind]).cuda()
         cache = bst.KV16Cache(pool[:, 0], pool[:, 1])
@@ -379,13 +381,13 @@ def test_very_large_scores(kind, form, bits, d, hq, hkv, rows):
             args[0] = torch.nn.functional.pad(args[0], (0, 30000), value=-1)
         for ws in (bst.attn_workspace("cuda"), None):
             out.fill_(-77.0), lse.fill_(-77.0)
-            bst.attn_window(qd, cache, *args, rows, 1 << 40, 0, out, scale=1.0, lse=lse, workspace=ws)
+            bst.attn_window(qd, cache, *args, rows, 1 << 40, 0, out, scale=scale, lse=lse, workspace=ws)
             torch.cuda.synchronize()
             for r in {0, rows // 2, rows - 1}:
                 seen = at[:int(pos[r]) + 1]
                 for h in range(hq):
                     g = h // (hq // hkv)
-                    x = c[seen, g] * 2.0 ** bits
+                    x = c[seen, g] * 2.0 ** bits * abs(scale)
                     w = np.exp(x - x.max())
                     want = w @ v[seen, g] / w.sum()
                     wl = x.max() + np.log(w.sum())
