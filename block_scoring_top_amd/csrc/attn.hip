@@ -36,8 +36,9 @@ constexpr int64_t kPartialBytes = (int64_t)BS_ATTN_WORKSPACE_BYTES - kCounterByt
 //     be padding.  64 requests, window 4,000: 1 row, 16-bit 46 and 59; 6 rows,
 //     4-bit 40 and 60;
 //   * the 4-bit cache at D = 256, where one wave a SIMD is all that the other's
-//     registers allow: 8,192 rows, window 4,000 848 and 961, 500 211 and 206; 64 x 6
-//     rows 74 and 265.
+//     registers allow.  16 query / 2 kv heads, window 4,000: 8,192 rows from position 0
+//     820 and 925, at the end of a 64K context 1,026 and 1,015 (window 500: 207 and
+//     186); 64 x 6 rows 78 and 271.
 bool gathers(const AttnCall& c, int64_t tiles, int64_t keys, int64_t pairs, int64_t num_req) {
   const bool kv4 = c.form == BS_KV_4;
   if (pairs <= 16 || (kv4 && c.d == 256)) return true;
@@ -172,8 +173,9 @@ int run_prefill(const AttnCall& c, const int32_t* page_table, int32_t pt_stride,
   a.max_rows = max_rows, a.window = window, a.sinks = sinks;
   // Without a window a request's later rows see more keys, and workgroups that
   // start last should not be the longest: 8,192 rows from position 0, 16 query / 2
-  // kv heads of 128, 16-bit 310 us so, 406 in order; 4,096 rows of 256 237 and 323.
-  // Under a window all are about as long, and in order is up to 6% quicker.
+  // kv heads of 128, 16-bit 312 us so, 401 in order; 4,096 rows of 256 237 and 323,
+  // of 128 126 and 125.  Under a window all are about as long, and in order is up
+  // to 6% quicker.
   a.latest_first = window >= (int64_t)pt_stride * kPage;
   set_scale(c, a.scale_log2, a.flip);
   a.out = c.out, a.ld_out = c.ld_out, a.lse = c.lse;

@@ -32,11 +32,12 @@
 // workspace and the last workgroup of a group to arrive joins them in split
 // order (so the result does not depend on the arrival order).
 //
-// Measured: 64 x 6 rows of 2,051 slots, 16 query / 2 kv heads of 128, 4-bit
-// cache: 43 us, 225 MB fetched at 5.1 TB/s (a large copy: 4.8), the vector units
-// busy for 54% of it.  16 rows of 2,048 slots, 4 kv heads: 10.1 us; one row: 7.9
-// us.  777 rows of 2,051 slots over a 25 MB 16-bit pool, 3 kv heads of 64: 111 us,
-// 1.2 GB gathered, of which the L2s let 731 MB through at 6.4 TB/s.
+// Measured (calls back to back, the cache in the Infinity Cache where it fits):
+// 64 x 6 rows of 2,051 slots, 16 query / 2 kv heads of 128, 4-bit cache: 43 us, 225
+// MB fetched at 5.1 TB/s (a large copy from HBM: 4.8), the vector units busy for
+// 54% of it.  16 rows of 2,048 slots, 4 kv heads: 10.3 us; one row: 7.9 us.  777
+// rows of 2,051 slots over a 25 MB 16-bit pool, 3 kv heads of 64: 111 to 116 us,
+// 1.2 GB gathered, of which the L2s let 732 MB through at 6.4 TB/s.
 #pragma once
 
 #include "attn.h"

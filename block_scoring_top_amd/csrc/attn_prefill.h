@@ -28,10 +28,11 @@
 // Consecutive row blocks of one kv head run on one XCD, whose L2 then holds
 // their window.
 //
-// Measured: 8,192 rows, window 4,096, 16 query / 2 kv heads of 128, bf16: 279 to
-// 300 us, 920 to 985 TFLOP/s (an 8,192-cubed library product: 1,258), matrix cores
-// busy for 49% of the cycles and vector units for 35%, at a clock that falls to
-// 2.0 GHz.  5 ragged requests over the 4-bit cache in fp16, 28.7 GFLOP: 51 us.
+// Measured (calls back to back; under the profiler in brackets): 8,192 rows, window 4,096, 16 query / 2 kv
+// heads of 128, bf16: 278 to 289 us (301 to 335), 950 to 988 TFLOP/s (an
+// 8,192-cubed library product: 1,258), matrix cores busy for 49% of the cycles
+// and vector units for 35%, at a clock that falls to 2.0 GHz.  5 ragged requests
+// over the 4-bit cache in fp16, 28.7 GFLOP: 51 us (59).
 #pragma once
 
 #include "attn.h"

@@ -476,7 +476,8 @@ int kv4_load(const uint8_t* codes, const uint8_t* scales, int64_t num_pages, con
  * Values of a 4-bit cache are converted to the queries' type: exact in bf16;
  * in fp16 rounded where that type's range ends.
  * A slot listed twice counts twice.  A row without a slot gives zeros and lse
- * -inf.  Scores, running maximum, sums and outputs are held in FP32; the
+ * -inf.  Scores, running maximum, sums and outputs are held in FP32 (2^8 times
+ * the sum of a row's weighted values, relative to its largest, has to fit it); the
  * weights are rounded to the queries' type for their product with V, and the
  * output once (in fp16 a weight below 2^-32 of the largest may count as 0).  An
  * infinity in V is passed on with the weight that its key has; a weight that is
@@ -506,6 +507,8 @@ int kv4_load(const uint8_t* codes, const uint8_t* scales, int64_t num_pages, con
  * does not see do not reach it.
  *   max_rows   host-side bound on the rows of any request (sizes the grid): 1
  *              for decode, the draft length for verify, the chunk for prefill.
+ *              Prompt chunks and single-token rows are served by one call, but
+ *              much quicker by one each (the grid is of max_rows for every request).
  *   window     >= 0, sinks >= 0 (window >= the context: plain causal attention).
  *
  * Both return BS_OK (also when there are no rows), BS_ERR_NULL, BS_ERR_ARG
