@@ -443,8 +443,8 @@ enum bs_kv_form {
  *             8, >= kv_heads * head_dim), 16-byte aligned: rows may lie inside
  *             a fused projection's output.
  *   head_dim  64, 128 or 256.
- * Device precondition: the slots of one call are distinct (a slot named twice
- * holds groups of either row).
+ * Device precondition: the slots of one call are distinct (what a slot named
+ * twice holds is unspecified: codes and scales may be of different rows).
  *
  * kv4_load - reads rows back: row i of k and v receives the values of slot
  * slots[i] in `dtype` (exact in bf16 and fp32; rounded to fp16 where that
