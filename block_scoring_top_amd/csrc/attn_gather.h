@@ -255,10 +255,10 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT, WINDOW)) vo
   auto key_pos = [&](int i) { return i < ns ? i : start + (i - ns); };
   // The slot of this lane's key (lane mod 32) of chunk c; -1: none.
   auto load_slot = [&](int c) -> int {
-    const int i = c * kGaKeys + (lane & 31);
-    if (c >= c1 || i >= n) return -1;
+    const uint32_t i = (uint32_t)c * kGaKeys + (lane & 31);  // unsigned: up to two steps past a list of almost 2^31
+    if (c >= c1 || i >= (uint32_t)n) return -1;
     if constexpr (WINDOW) {
-      const int p = key_pos(i);
+      const int p = key_pos((int)i);
       const int page = ptab[p >> 6];
       return page < 0 || page > (0x7FFFFFFF >> 6) ? -1 : page * kPage + (p & (kPage - 1));
     } else {
@@ -556,7 +556,7 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT, WINDOW)) vo
   int c = c0 + wave;
   auto count = [&] {
     if constexpr (!WINDOW)
-      if (a.count != nullptr) n = max(min(n, a.count[row0]), 0), c1 = min(c1, (n + kGaKeys - 1) / kGaKeys);
+      if (a.count != nullptr) n = max(min(n, a.count[row0]), 0), c1 = min(c1, (int)(((uint32_t)n + kGaKeys - 1) / kGaKeys));
   };
   if constexpr (Stage::kUsed) {
     if (c < c1) {
@@ -597,9 +597,9 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT, WINDOW)) vo
     // slots one chunk earlier still.
     int sl0 = load_slot(c), sl = load_slot(c + kGaWaves);
     count();
-    const int i = c * kGaKeys + (lane & 31);
-    sl0 = i < n ? sl0 : -1;
-    sl = i + kGaWaves * kGaKeys < n ? sl : -1;
+    const uint32_t i = (uint32_t)c * kGaKeys + (lane & 31);
+    sl0 = i < (uint32_t)n ? sl0 : -1;
+    sl = i + kGaWaves * kGaKeys < (uint32_t)n ? sl : -1;
     if (c < c1) {
       Raw r0, r1;
       uint32_t k0, k1;
