@@ -16,7 +16,12 @@ Steps (same names as the C ABI):
 What consumes the chosen slots:
   kv4_store / kv4_load (a 4-bit KV cache, written and read back) and
   attn_slots / attn_window (attention over a selection's slots, and over a
-  sliding window plus the first tokens; 16-bit pools or the 4-bit cache)
+  sliding window plus the first tokens; 16-bit pools, the 4-bit cache or the
+  8-bit one that kv8_store / kv8_load write and read)
+The index keys in 4 bits: idx4_store / idx4_compress_store / idx4_load, scored
+  by idx4_score in place of the first step.
+The tables, positions and slots that these calls take, kept on the GPU:
+  pages_extend / pages_release.
 """
 from __future__ import annotations
 
@@ -89,6 +94,24 @@ def lib():
         L.kv4_store.restype = C.c_int
         L.kv4_load.argtypes = [P, P, i64, P, i32, i32, i32, P, P, i32, i64, i64, P]
         L.kv4_load.restype = C.c_int
+        L.kv8_store.argtypes = L.kv4_store.argtypes
+        L.kv8_store.restype = C.c_int
+        L.kv8_load.argtypes = L.kv4_load.argtypes
+        L.kv8_load.restype = C.c_int
+        L.idx4_store.argtypes = [P, i32, i64, P, i32, P, P, i64, P]
+        L.idx4_store.restype = C.c_int
+        L.idx4_load.argtypes = [P, P, i64, P, i32, P, i32, i64, P]
+        L.idx4_load.restype = C.c_int
+        L.idx4_compress_store.argtypes = [P, i32, P, P, P, i32, i32, i32, i32, i32, i32, C.c_double, P, P, P, i32,
+                                          P, P, i64, P]
+        L.idx4_compress_store.restype = C.c_int
+        L.idx4_score.argtypes = [P, P, P, i64, P, i32, P, i32, P, i32, i32, i32, P, i64, P, P]
+        L.idx4_score.restype = C.c_int
+        pages_args = [P, P, P, i32, P, i32, P, i32, P, P, P, P]
+        L.pages_extend.argtypes = [*pages_args, P, P, P, i32, P]
+        L.pages_extend.restype = C.c_int
+        L.pages_release.argtypes = [*pages_args, P]
+        L.pages_release.restype = C.c_int
         attn_args = [P, i32, i64, i32, i32, i32, i32, P, P, i32, i64, i64]
         L.attn_slots.argtypes = [*attn_args, P, i32, P, C.c_float, P, i64, P, P, C.c_size_t, P]
         L.attn_slots.restype = C.c_int
@@ -149,7 +172,7 @@ def _score_args(q, kcache, num_pages, page_table, req_row_ptr, row_pos, c, max_v
     if row_len is not None and row_len.numel() != num_rows:
         raise ValueError("row_len must hold num_rows entries")
     per_page = PAGE_TOKENS // int(c) if int(c) in (1, 4) else 1
-    if kcache.numel() < int(num_pages) * per_page * DIM:
+    if kcache is not None and kcache.numel() < int(num_pages) * per_page * DIM:
         raise ValueError("kcache holds fewer than num_pages pages")
     return (_ptr(q, _BF16, "q", dev), _ptr(kcache, _BF16, "kcache", dev), int(num_pages),
             _ptr(page_table, _I32, "page_table", dev), int(page_table.shape[1]),
@@ -352,9 +375,9 @@ def idx_select_translate_planned(scores, max_len, k, req_row_ptr, row_pos, c, pa
     _check(lib().idx_select_translate_planned(*args, _stream(stream, scores.device)), "idx_select_translate_planned")
 
 
-def _compress_args(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary_dim, sections, theta, ring,
-                   ring_pos, page_table, kcache, num_pages):
-    """Checked argument tuple of an ``idx_compress_store`` call (all but the stream)."""
+def _compress_head(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary_dim, sections, theta, ring, ring_pos,
+                   page_table):
+    """The checked arguments that both compressing calls begin with."""
     dev = k_raw.device
     T = int(k_raw.shape[0])
     B = int(req_tok_ptr.shape[0]) - 1
@@ -366,8 +389,6 @@ def _compress_args(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary_dim
         raise ValueError("mrope_pos must be [num_tok, 3]")
     if ring_pos is not None and ring_pos.shape != (B, 3):
         raise ValueError("ring_pos must be [num_req, 3]")
-    if kcache.dim() != 2 or kcache.shape[1] != 128 or kcache.shape[0] < 16 * int(num_pages):
-        raise ValueError("kcache must be [>= num_pages * 16, 128]")
     sec = [int(v) for v in sections]
     if len(sec) != 3:
         raise ValueError("sections must hold 3 entries (t, h, w)")
@@ -375,7 +396,16 @@ def _compress_args(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary_dim
             _ptr(tok_start, _I32, "tok_start", dev), _ptr(mrope_pos, _I32, "mrope_pos", dev), B, int(max_tok),
             int(rotary_dim), sec[0], sec[1], sec[2], float(theta), _ptr(ring, _BF16, "ring", dev),
             _ptr(ring_pos, _I32, "ring_pos", dev), _ptr(page_table, _I32, "page_table", dev),
-            int(page_table.shape[1]), _ptr(kcache, _BF16, "kcache", dev), int(num_pages))
+            int(page_table.shape[1]))
+
+
+def _compress_args(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary_dim, sections, theta, ring,
+                   ring_pos, page_table, kcache, num_pages):
+    """Checked argument tuple of an ``idx_compress_store`` call (all but the stream)."""
+    if kcache.dim() != 2 or kcache.shape[1] != 128 or kcache.shape[0] < 16 * int(num_pages):
+        raise ValueError("kcache must be [>= num_pages * 16, 128]")
+    return (*_compress_head(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary_dim, sections, theta, ring,
+                            ring_pos, page_table), _ptr(kcache, _BF16, "kcache", k_raw.device), int(num_pages))
 
 
 def idx_compress_store(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary_dim, sections, theta, ring,
@@ -389,6 +419,7 @@ def idx_compress_store(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # bs_dtype
 _U8 = (torch.uint8,)
+_CODES8 = (torch.uint8, torch.float8_e4m3fn)
 
 
 class KV4Cache:
@@ -417,6 +448,34 @@ class KV4Cache:
 
     def _args(self, dtype, dev):
         return _ptr(self.codes, _U8, "codes", dev), _ptr(self.scales, _U8, "scales", dev), self.form, 0, self.num_pages
+
+
+class KV8Cache:
+    """An 8-bit KV cache (layout: ``kv8_store`` in blockscore.h): ``codes``
+    uint8 (or float8_e4m3fn) [slots, kv_heads, 2, head_dim] and ``scales``
+    float32 [slots / 64, kv_heads, 2], contiguous, ``slots`` a multiple of 64."""
+
+    form = 8  # BS_KV_8
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
+        if codes.dim() != 4 or codes.shape[2] != 2 or codes.shape[0] % PAGE_TOKENS:
+            raise ValueError("codes must be [num_pages * 64, kv_heads, 2, head_dim]")
+        self.codes, self.scales = codes, scales
+        self.kv_heads, self.head_dim = int(codes.shape[1]), int(codes.shape[3])
+        self.num_pages = int(codes.shape[0]) // PAGE_TOKENS
+        if scales.shape != (self.num_pages, self.kv_heads, 2):
+            raise ValueError("scales must be [num_pages, kv_heads, 2]")
+        self.device = codes.device
+
+    @classmethod
+    def empty(cls, num_pages: int, kv_heads: int, head_dim: int, device) -> "KV8Cache":
+        """Storage for ``num_pages`` pages (every slot reads back as zeros)."""
+        n = int(num_pages)
+        return cls(torch.zeros((n * PAGE_TOKENS, kv_heads, 2, head_dim), dtype=torch.uint8, device=device),
+                   torch.full((n, kv_heads, 2), 2.0 ** -120, dtype=torch.float32, device=device))
+
+    def _args(self, dtype, dev):
+        return _ptr(self.codes, _CODES8, "codes", dev), _ptr(self.scales, _F32, "scales", dev), self.form, 0, self.num_pages
 
 
 class KV16Cache:
@@ -468,43 +527,223 @@ def _size(n) -> int:
     return int(n)
 
 
-def _kv4_store_args(k, v, slots, cache):
-    """Checked argument tuple of a ``kv4_store`` call (all but the stream)."""
+def _kv_store_args(k, v, slots, cache, kind):
+    """Checked argument tuple of a ``kv4_store`` or ``kv8_store`` call (all but the stream)."""
     dev = cache.device
-    if not isinstance(cache, KV4Cache):
-        raise TypeError("cache must be a KV4Cache")
+    if not isinstance(cache, kind):
+        raise TypeError(f"cache must be a {kind.__name__}")
     if k.dim() != 3 or k.shape != v.shape or k.shape[1:] != (cache.kv_heads, cache.head_dim) or k.dtype != v.dtype:
         raise ValueError("k and v must both be [num_tok, kv_heads, head_dim] of one dtype")
     if slots.numel() != k.shape[0]:
         raise ValueError("slots must hold num_tok entries")
+    codes, scales, _, _, num_pages = cache._args(None, dev)
     return (_rows_ptr(k, tuple(_DTYPES), "k", dev), _rows_ptr(v, tuple(_DTYPES), "v", dev), _DTYPES[k.dtype], _ld(k),
-            _ld(v), _ptr(slots, _I32, "slots", dev), _size(k.shape[0]), cache.kv_heads, cache.head_dim,
-            _ptr(cache.codes, _U8, "codes", dev), _ptr(cache.scales, _U8, "scales", dev), cache.num_pages)
+            _ld(v), _ptr(slots, _I32, "slots", dev), _size(k.shape[0]), cache.kv_heads, cache.head_dim, codes, scales,
+            num_pages)
 
 
 def kv4_store(k, v, slots, cache: KV4Cache, stream=None):
     """Quantise new K/V rows into the 4-bit cache.  See ``kv4_store`` in blockscore.h."""
-    PreparedCall("kv4_store", _kv4_store_args(k, v, slots, cache), cache.device, once=True)(stream)
+    PreparedCall("kv4_store", _kv_store_args(k, v, slots, cache, KV4Cache), cache.device, once=True)(stream)
 
 
-def _kv4_load_args(cache, slots, k, v):
-    """Checked argument tuple of a ``kv4_load`` call (all but the stream)."""
+def kv8_store(k, v, slots, cache: KV8Cache, stream=None):
+    """Quantise new K/V rows into the 8-bit cache.  See ``kv8_store`` in blockscore.h."""
+    PreparedCall("kv8_store", _kv_store_args(k, v, slots, cache, KV8Cache), cache.device, once=True)(stream)
+
+
+def _kv_load_args(cache, slots, k, v, kind):
+    """Checked argument tuple of a ``kv4_load`` or ``kv8_load`` call (all but the stream)."""
     dev = cache.device
-    if not isinstance(cache, KV4Cache):
-        raise TypeError("cache must be a KV4Cache")
+    if not isinstance(cache, kind):
+        raise TypeError(f"cache must be a {kind.__name__}")
     if k.dim() != 3 or k.shape != v.shape or k.shape[1:] != (cache.kv_heads, cache.head_dim) or k.dtype != v.dtype:
         raise ValueError("k and v must both be [num_slots, kv_heads, head_dim] of one dtype")
     if slots.numel() != k.shape[0]:
         raise ValueError("slots must hold one entry per row of k")
-    return (_ptr(cache.codes, _U8, "codes", dev), _ptr(cache.scales, _U8, "scales", dev), cache.num_pages,
-            _ptr(slots, _I32, "slots", dev), _size(k.shape[0]), cache.kv_heads, cache.head_dim,
-            _rows_ptr(k, tuple(_DTYPES), "k", dev), _rows_ptr(v, tuple(_DTYPES), "v", dev), _DTYPES[k.dtype], _ld(k),
-            _ld(v))
+    codes, scales, _, _, num_pages = cache._args(None, dev)
+    return (codes, scales, num_pages, _ptr(slots, _I32, "slots", dev), _size(k.shape[0]), cache.kv_heads,
+            cache.head_dim, _rows_ptr(k, tuple(_DTYPES), "k", dev), _rows_ptr(v, tuple(_DTYPES), "v", dev),
+            _DTYPES[k.dtype], _ld(k), _ld(v))
 
 
 def kv4_load(cache: KV4Cache, slots, k, v, stream=None):
     """Read rows of the 4-bit cache back.  See ``kv4_load`` in blockscore.h."""
-    PreparedCall("kv4_load", _kv4_load_args(cache, slots, k, v), cache.device, once=True)(stream)
+    PreparedCall("kv4_load", _kv_load_args(cache, slots, k, v, KV4Cache), cache.device, once=True)(stream)
+
+
+def kv8_load(cache: KV8Cache, slots, k, v, stream=None):
+    """Read rows of the 8-bit cache back.  See ``kv8_load`` in blockscore.h."""
+    PreparedCall("kv8_load", _kv_load_args(cache, slots, k, v, KV8Cache), cache.device, once=True)(stream)
+
+
+class Idx4Cache:
+    """Index keys in 4 bits (layout: ``idx4_store`` in blockscore.h): ``codes``
+    uint8 [keys, 64] and ``scales`` uint8 [keys, 4], contiguous, ``keys`` a
+    multiple of 64 / c."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, c: int):
+        if int(c) not in (1, 4):
+            raise ValueError("c must be 1 or 4")
+        if codes.dim() != 2 or codes.shape[1] != DIM // 2 or codes.shape[0] % (PAGE_TOKENS // int(c)):
+            raise ValueError("codes must be [num_pages * (64 / c), 64]")
+        if scales.shape != (codes.shape[0], DIM // 32):
+            raise ValueError("scales must be [num_pages * (64 / c), 4]")
+        self.codes, self.scales, self.c = codes, scales, int(c)
+        self.num_keys = int(codes.shape[0])
+        self.num_pages = self.num_keys // (PAGE_TOKENS // self.c)
+        self.device = codes.device
+
+    @classmethod
+    def empty(cls, num_pages: int, c: int, device) -> "Idx4Cache":
+        """Storage for ``num_pages`` pages (every key reads back as zeros)."""
+        n = int(num_pages) * (PAGE_TOKENS // int(c))
+        return cls(torch.zeros((n, DIM // 2), dtype=torch.uint8, device=device),
+                   torch.full((n, DIM // 32), 127, dtype=torch.uint8, device=device), c)
+
+    def _ptrs(self, dev):
+        return _ptr(self.codes, _U8, "codes", dev), _ptr(self.scales, _U8, "scales", dev)
+
+
+def _keys_ptr(t: torch.Tensor, name: str, rows: int, dev):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != DIM:
+        raise ValueError(f"{name} must be [rows, 128], one row per slot")
+    return _rows_ptr(t.unsqueeze(1), tuple(_DTYPES), name, dev), _DTYPES[t.dtype], _ld(t.unsqueeze(1))
+
+
+def _idx4_cache(cache):
+    if not isinstance(cache, Idx4Cache):
+        raise TypeError("cache must be an Idx4Cache")
+    return cache.device
+
+
+def _idx4_store_args(keys, slots, cache):
+    """Checked argument tuple of an ``idx4_store`` call (all but the stream)."""
+    dev = _idx4_cache(cache)
+    n = _size(slots.numel())
+    return (*_keys_ptr(keys, "keys", n, dev), _ptr(slots, _I32, "slots", dev), n, *cache._ptrs(dev),
+            _size(cache.num_keys))
+
+
+def idx4_store(keys, slots, cache: Idx4Cache, stream=None):
+    """Quantise index keys into the 4-bit cache.  See ``idx4_store`` in blockscore.h."""
+    PreparedCall("idx4_store", _idx4_store_args(keys, slots, cache), cache.device, once=True)(stream)
+
+
+def _idx4_load_args(cache, slots, keys):
+    """Checked argument tuple of an ``idx4_load`` call (all but the stream)."""
+    dev = _idx4_cache(cache)
+    n = _size(slots.numel())
+    return (*cache._ptrs(dev), _size(cache.num_keys), _ptr(slots, _I32, "slots", dev), n,
+            *_keys_ptr(keys, "keys", n, dev))
+
+
+def idx4_load(cache: Idx4Cache, slots, keys, stream=None):
+    """Read 4-bit index keys back.  See ``idx4_load`` in blockscore.h."""
+    PreparedCall("idx4_load", _idx4_load_args(cache, slots, keys), cache.device, once=True)(stream)
+
+
+def _idx4_compress_args(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary_dim, sections, theta, ring, ring_pos,
+                        page_table, cache):
+    """Checked argument tuple of an ``idx4_compress_store`` call (all but the stream)."""
+    dev = _idx4_cache(cache)
+    if cache.c != 4:
+        raise ValueError("compressed keys go to a cache of c = 4")
+    return (*_compress_head(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary_dim, sections, theta, ring,
+                            ring_pos, page_table), *cache._ptrs(k_raw.device), cache.num_pages)
+
+
+def idx4_compress_store(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary_dim, sections, theta, ring, ring_pos,
+                        page_table, cache: Idx4Cache, stream=None):
+    """Compress new raw index keys into the 4-bit c = 4 keys (and update the
+    rings).  See ``idx4_compress_store`` in blockscore.h."""
+    PreparedCall("idx4_compress_store", _idx4_compress_args(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok,
+                                                            rotary_dim, sections, theta, ring, ring_pos, page_table,
+                                                            cache), k_raw.device, once=True)(stream)
+
+
+def _idx4_score_args(q, cache, page_table, req_row_ptr, row_pos, max_vis, scores, row_len=None):
+    """Checked argument tuple of an ``idx4_score`` call (all but the stream)."""
+    _idx4_cache(cache)
+    a = _score_args(q, None, cache.num_pages, page_table, req_row_ptr, row_pos, cache.c, max_vis, scores, row_len)
+    return (a[0], *cache._ptrs(q.device), *a[2:])
+
+
+def idx4_score(q, cache: Idx4Cache, page_table, req_row_ptr, row_pos, max_vis, scores, row_len=None, stream=None):
+    """Scores over 4-bit index keys, any number of rows a request.  See ``idx4_score`` in blockscore.h."""
+    PreparedCall("idx4_score", _idx4_score_args(q, cache, page_table, req_row_ptr, row_pos, max_vis, scores, row_len),
+                 q.device, once=True)(stream)
+
+
+class PagePool:
+    """The free pages of a cache: ``ring`` int32 [size], their ids, and
+    ``state`` int32 [4], head, count, what the last ``pages_extend`` lacked, 0
+    (``pages_extend`` in blockscore.h)."""
+
+    def __init__(self, ring: torch.Tensor, state: torch.Tensor):
+        if ring.dim() != 1 or state.shape != (4,):
+            raise ValueError("ring must be [size] and state [4]")
+        self.ring, self.state = ring, state
+
+    @classmethod
+    def full(cls, num_pages: int, device) -> "PagePool":
+        """All of ``num_pages`` pages, free."""
+        n = _size(num_pages)
+        return cls(torch.arange(n, dtype=torch.int32, device=device),
+                   torch.tensor([0, n, 0, 0], dtype=torch.int32, device=device))
+
+
+def _pages_args(pool, kv_len, held, change, name, page_table, kv_len_out, held_out, pool_out):
+    if not isinstance(pool, PagePool) or not (pool_out is None or isinstance(pool_out, PagePool)):
+        raise TypeError("pool and pool_out must be PagePools")
+    dev = pool.ring.device
+    B = kv_len.numel()
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be [num_req, pt_stride]")
+    outs = [x if y is None else y for x, y in ((kv_len, kv_len_out), (held, held_out), (pool, pool_out))]
+    if any(x.numel() != B for x in (held, change, *outs[:2])):
+        raise ValueError(f"held, {name}, kv_len_out and held_out must hold num_req entries")
+    if outs[2].ring.data_ptr() != pool.ring.data_ptr():
+        raise ValueError("pool_out must be of the same ring")
+    return (_ptr(kv_len, _I32, "kv_len", dev), _ptr(held, _I32, "held", dev), _ptr(change, _I32, name, dev), _size(B),
+            _ptr(page_table, _I32, "page_table", dev), _size(page_table.shape[1]), _ptr(pool.ring, _I32, "ring", dev),
+            _size(pool.ring.numel()), _ptr(pool.state, _I32, "state", dev), _ptr(outs[0], _I32, "kv_len_out", dev),
+            _ptr(outs[1], _I32, "held_out", dev), _ptr(outs[2].state, _I32, "state", dev))
+
+
+def _pages_extend_args(pool, kv_len, held, new_len, page_table, req_row_ptr, row_pos, slots, kv_len_out=None,
+                       held_out=None, pool_out=None):
+    """Checked argument tuple of a ``pages_extend`` call (all but the stream)."""
+    a = _pages_args(pool, kv_len, held, new_len, "new_len", page_table, kv_len_out, held_out, pool_out)
+    dev = pool.ring.device
+    if req_row_ptr.numel() != kv_len.numel() + 1 or slots.numel() != row_pos.numel():
+        raise ValueError("req_row_ptr must hold num_req + 1 entries, row_pos and slots num_rows each")
+    return (*a, _ptr(req_row_ptr, _I32, "req_row_ptr", dev), _ptr(row_pos, _I32, "row_pos", dev),
+            _ptr(slots, _I32, "slots", dev), _size(row_pos.numel()))
+
+
+def pages_extend(pool: PagePool, kv_len, held, new_len, page_table, req_row_ptr, row_pos, slots, kv_len_out=None,
+                 held_out=None, pool_out=None, stream=None):
+    """Append new tokens to a batch: their pages, positions and slots.  The
+    state is updated in place unless told otherwise (``pool_out``: a PagePool of
+    the same ring).  See ``pages_extend`` in blockscore.h."""
+    PreparedCall("pages_extend", _pages_extend_args(pool, kv_len, held, new_len, page_table, req_row_ptr, row_pos,
+                                                    slots, kv_len_out, held_out, pool_out), pool.ring.device,
+                 once=True)(stream)
+
+
+def _pages_release_args(pool, kv_len, held, keep_len, page_table, kv_len_out=None, held_out=None, pool_out=None):
+    """Checked argument tuple of a ``pages_release`` call (all but the stream)."""
+    return _pages_args(pool, kv_len, held, keep_len, "keep_len", page_table, kv_len_out, held_out, pool_out)
+
+
+def pages_release(pool: PagePool, kv_len, held, keep_len, page_table, kv_len_out=None, held_out=None, pool_out=None,
+                  stream=None):
+    """Cut requests back and return their pages.  See ``pages_release`` in blockscore.h."""
+    PreparedCall("pages_release", _pages_release_args(pool, kv_len, held, keep_len, page_table, kv_len_out, held_out,
+                                                      pool_out), pool.ring.device, once=True)(stream)
 
 
 def attn_workspace(device) -> torch.Tensor:
@@ -685,7 +924,10 @@ __all__ = [
     "topk_planned_workspace", "topk_plan_rows", "idx_select_translate_planned", "prepare_plan",
     "prepare_select_translate_planned", "KV4Cache", "KV16Cache", "kv4_store", "kv4_load", "attn_workspace",
     "ATTN_WORKSPACE_BYTES", "attn_slots", "attn_window", "prepare_kv4_store", "prepare_kv4_load",
-    "prepare_attn_slots", "prepare_attn_window",
+    "prepare_attn_slots", "prepare_attn_window", "KV8Cache", "kv8_store", "kv8_load", "prepare_kv8_store",
+    "prepare_kv8_load", "Idx4Cache", "idx4_store", "idx4_load", "idx4_compress_store", "idx4_score",
+    "prepare_idx4_store", "prepare_idx4_load", "prepare_idx4_compress_store", "prepare_idx4_score", "PagePool",
+    "pages_extend", "pages_release", "prepare_pages_extend", "prepare_pages_release",
 ]
 
 
@@ -699,12 +941,62 @@ def prepare_compress_store(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, ro
 
 def prepare_kv4_store(k, v, slots, cache: KV4Cache) -> PreparedCall:
     """``kv4_store`` with fixed arguments."""
-    return PreparedCall("kv4_store", _kv4_store_args(k, v, slots, cache), cache.device)
+    return PreparedCall("kv4_store", _kv_store_args(k, v, slots, cache, KV4Cache), cache.device)
 
 
 def prepare_kv4_load(cache: KV4Cache, slots, k, v) -> PreparedCall:
     """``kv4_load`` with fixed arguments."""
-    return PreparedCall("kv4_load", _kv4_load_args(cache, slots, k, v), cache.device)
+    return PreparedCall("kv4_load", _kv_load_args(cache, slots, k, v, KV4Cache), cache.device)
+
+
+def prepare_kv8_store(k, v, slots, cache: KV8Cache) -> PreparedCall:
+    """``kv8_store`` with fixed arguments."""
+    return PreparedCall("kv8_store", _kv_store_args(k, v, slots, cache, KV8Cache), cache.device)
+
+
+def prepare_kv8_load(cache: KV8Cache, slots, k, v) -> PreparedCall:
+    """``kv8_load`` with fixed arguments."""
+    return PreparedCall("kv8_load", _kv_load_args(cache, slots, k, v, KV8Cache), cache.device)
+
+
+def prepare_idx4_store(keys, slots, cache: Idx4Cache) -> PreparedCall:
+    """``idx4_store`` with fixed arguments."""
+    return PreparedCall("idx4_store", _idx4_store_args(keys, slots, cache), cache.device)
+
+
+def prepare_idx4_load(cache: Idx4Cache, slots, keys) -> PreparedCall:
+    """``idx4_load`` with fixed arguments."""
+    return PreparedCall("idx4_load", _idx4_load_args(cache, slots, keys), cache.device)
+
+
+def prepare_idx4_compress_store(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary_dim, sections, theta, ring,
+                                ring_pos, page_table, cache: Idx4Cache) -> PreparedCall:
+    """``idx4_compress_store`` with fixed arguments."""
+    return PreparedCall("idx4_compress_store", _idx4_compress_args(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok,
+                                                                   rotary_dim, sections, theta, ring, ring_pos,
+                                                                   page_table, cache), k_raw.device)
+
+
+def prepare_idx4_score(q, cache: Idx4Cache, page_table, req_row_ptr, row_pos, max_vis, scores,
+                       row_len=None) -> PreparedCall:
+    """``idx4_score`` with fixed arguments."""
+    return PreparedCall("idx4_score", _idx4_score_args(q, cache, page_table, req_row_ptr, row_pos, max_vis, scores,
+                                                       row_len), q.device)
+
+
+def prepare_pages_extend(pool: PagePool, kv_len, held, new_len, page_table, req_row_ptr, row_pos, slots,
+                         kv_len_out=None, held_out=None, pool_out=None) -> PreparedCall:
+    """``pages_extend`` with fixed arguments."""
+    return PreparedCall("pages_extend", _pages_extend_args(pool, kv_len, held, new_len, page_table, req_row_ptr,
+                                                           row_pos, slots, kv_len_out, held_out, pool_out),
+                        pool.ring.device)
+
+
+def prepare_pages_release(pool: PagePool, kv_len, held, keep_len, page_table, kv_len_out=None, held_out=None,
+                          pool_out=None) -> PreparedCall:
+    """``pages_release`` with fixed arguments."""
+    return PreparedCall("pages_release", _pages_release_args(pool, kv_len, held, keep_len, page_table, kv_len_out,
+                                                             held_out, pool_out), pool.ring.device)
 
 
 def prepare_attn_slots(q, cache, slots, out, count=None, scale=None, lse=None, workspace=None) -> PreparedCall:

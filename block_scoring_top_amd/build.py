@@ -12,9 +12,8 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libblockscore.so")
 SOURCES = ["api.hip", "score_decode.hip", "score_prefill.hip", "topk.hip", "expand.hip", "compress.hip", "kv4.hip",
-           "attn.hip", "attn_gather_bf16_kv4.hip", "attn_gather_bf16_kv16.hip", "attn_gather_f16_kv4.hip",
-           "attn_gather_f16_kv16.hip", "attn_prefill_bf16_kv4.hip", "attn_prefill_bf16_kv16.hip",
-           "attn_prefill_f16_kv4.hip", "attn_prefill_f16_kv16.hip"]
+           "kv8.hip", "idx4.hip", "score4.hip", "pages.hip", "attn.hip",
+           *(f"attn_{k}_{t}_{f}.hip" for k in ("gather", "prefill") for t in ("bf16", "f16") for f in ("kv4", "kv8", "kv16"))]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -219,20 +219,35 @@ BS_EXPORT int idx_select_translate_noalloc(const float* scores, int64_t ld_score
                                              out_count, ld_out, static_cast<hipStream_t>(stream));
 }
 
-BS_EXPORT int idx_compress_store(const uint16_t* k_raw, int32_t num_tok, const int32_t* req_tok_ptr,
-                                 const int32_t* tok_start, const int32_t* mrope_pos, int32_t num_req,
-                                 int32_t max_tok, int32_t rotary_dim, int32_t sec_t, int32_t sec_h, int32_t sec_w,
-                                 double theta, uint16_t* ring, int32_t* ring_pos, const int32_t* page_table,
-                                 int32_t pt_stride, uint16_t* kcache, int64_t num_pages, void* stream) {
+namespace {
+
+inline int check_compress_args(const uint16_t* k_raw, int32_t num_tok, const int32_t* req_tok_ptr,
+                               const int32_t* tok_start, const int32_t* mrope_pos, int32_t num_req, int32_t max_tok,
+                               int32_t rotary_dim, int32_t sec_t, int32_t sec_h, int32_t sec_w, double theta,
+                               const uint16_t* ring, const int32_t* ring_pos, const int32_t* page_table,
+                               int32_t pt_stride, const void* cache, int64_t num_pages) {
   if (num_req < 0 || num_tok < 0 || max_tok < 0 || num_pages < 0 || num_req > 65535) return BS_ERR_ARG;
   if (max_tok > num_tok) return BS_ERR_ARG;
   if (rotary_dim < 0 || rotary_dim > BS_DIM || (rotary_dim & 1)) return BS_ERR_ARG;
   if (sec_t < 0 || sec_h < 0 || sec_w < 0 || sec_t + sec_h + sec_w != rotary_dim / 2) return BS_ERR_ARG;
   if (!(theta > 0.0) || !std::isfinite(theta)) return BS_ERR_ARG;
   if (num_req == 0 || num_tok == 0 || max_tok == 0) return BS_OK;
-  if (!k_raw || !req_tok_ptr || !tok_start || !ring || !page_table || !kcache) return BS_ERR_NULL;
+  if (!k_raw || !req_tok_ptr || !tok_start || !ring || !page_table || !cache) return BS_ERR_NULL;
   if (mrope_pos && !ring_pos) return BS_ERR_NULL;
   if (pt_stride < 1 || num_pages < 1) return BS_ERR_ARG;
+  return BS_OK;
+}
+
+}  // namespace
+
+BS_EXPORT int idx_compress_store(const uint16_t* k_raw, int32_t num_tok, const int32_t* req_tok_ptr,
+                                 const int32_t* tok_start, const int32_t* mrope_pos, int32_t num_req,
+                                 int32_t max_tok, int32_t rotary_dim, int32_t sec_t, int32_t sec_h, int32_t sec_w,
+                                 double theta, uint16_t* ring, int32_t* ring_pos, const int32_t* page_table,
+                                 int32_t pt_stride, uint16_t* kcache, int64_t num_pages, void* stream) {
+  const int st = check_compress_args(k_raw, num_tok, req_tok_ptr, tok_start, mrope_pos, num_req, max_tok, rotary_dim,
+                                     sec_t, sec_h, sec_w, theta, ring, ring_pos, page_table, pt_stride, kcache, num_pages);
+  if (st != BS_OK || num_req == 0 || num_tok == 0 || max_tok == 0) return st;
   return bs::launch_compress(k_raw, num_tok, req_tok_ptr, tok_start, mrope_pos, num_req, max_tok, rotary_dim,
                              sec_t, sec_h, theta, ring, ring_pos, page_table, pt_stride, kcache, num_pages,
                              static_cast<hipStream_t>(stream));
@@ -267,7 +282,7 @@ inline int check_attn_args(const void* q, int32_t dtype, int64_t ld_q, int32_t n
   if (num_rows < 0 || num_pages < 0 || num_pages > kMaxPages || kv_heads < 1 || q_heads < 1 || !head_dim_ok(head_dim))
     return BS_ERR_ARG;
   if (dtype != BS_BF16 && dtype != BS_F16) return BS_ERR_ARG;
-  if (cache_form != BS_KV_16 && cache_form != BS_KV_4) return BS_ERR_ARG;
+  if (cache_form != BS_KV_16 && cache_form != BS_KV_4 && cache_form != BS_KV_8) return BS_ERR_ARG;
   // The kernels multiply by scale * log2(e), which has to be finite too.
   if (q_heads % kv_heads != 0 || !(std::fabs(scale) <= 0x1p127f)) return BS_ERR_ARG;
   const int64_t qw = (int64_t)q_heads * head_dim, kvw = (int64_t)kv_heads * head_dim;
@@ -302,6 +317,123 @@ BS_EXPORT int kv4_load(const uint8_t* codes, const uint8_t* scales, int64_t num_
   if (st != BS_OK || num_slots == 0) return st;
   return bs::launch_kv4_load(codes, scales, slots_of_pages(num_pages), slots, num_slots, kv_heads, head_dim, k, v,
                              dtype, ld_k, ld_v, static_cast<hipStream_t>(stream));
+}
+
+BS_EXPORT int kv8_store(const void* k, const void* v, int32_t dtype, int64_t ld_k, int64_t ld_v, const int32_t* slots,
+                        int32_t num_tok, int32_t kv_heads, int32_t head_dim, uint8_t* codes, float* scales,
+                        int64_t num_pages, void* stream) {
+  const int st = check_kv4_args(k, v, dtype, ld_k, ld_v, slots, num_tok, kv_heads, head_dim, codes,
+                                reinterpret_cast<const uint8_t*>(scales), num_pages);
+  if (st != BS_OK || num_tok == 0) return st;
+  return bs::launch_kv8_store(k, v, dtype, ld_k, ld_v, slots, num_tok, kv_heads, head_dim, codes, scales,
+                              slots_of_pages(num_pages), static_cast<hipStream_t>(stream));
+}
+
+BS_EXPORT int kv8_load(const uint8_t* codes, const float* scales, int64_t num_pages, const int32_t* slots,
+                       int32_t num_slots, int32_t kv_heads, int32_t head_dim, void* k, void* v, int32_t dtype,
+                       int64_t ld_k, int64_t ld_v, void* stream) {
+  const int st = check_kv4_args(k, v, dtype, ld_k, ld_v, slots, num_slots, kv_heads, head_dim, codes,
+                                reinterpret_cast<const uint8_t*>(scales), num_pages);
+  if (st != BS_OK || num_slots == 0) return st;
+  return bs::launch_kv8_load(codes, scales, slots_of_pages(num_pages), slots, num_slots, kv_heads, head_dim, k, v,
+                             dtype, ld_k, ld_v, static_cast<hipStream_t>(stream));
+}
+
+namespace {
+
+inline int check_idx4_args(const void* keys, int32_t dtype, int64_t ld, const int32_t* slots, int32_t rows,
+                           const uint8_t* codes, const uint8_t* scales, int64_t cache_keys) {
+  if (rows < 0 || cache_keys < 0 || cache_keys > 0x7FFFFFFF) return BS_ERR_ARG;
+  if (dtype != BS_BF16 && dtype != BS_F16 && dtype != BS_F32) return BS_ERR_ARG;
+  if (!row_stride_ok(ld, BS_DIM)) return BS_ERR_ARG;
+  if (rows == 0) return BS_OK;
+  if (!keys || !slots || !codes || !scales) return BS_ERR_NULL;
+  if (cache_keys < 1 || !aligned16(keys) || !aligned16(codes) || !aligned16(scales)) return BS_ERR_ARG;
+  return BS_OK;
+}
+
+inline int check_pages_args(const int32_t* kv_len, const int32_t* held, const int32_t* change, int32_t num_req,
+                            const int32_t* page_table, int32_t pt_stride, const int32_t* ring, int32_t ring_size,
+                            const int32_t* pool, const int32_t* kv_len_out, const int32_t* held_out,
+                            const int32_t* pool_out) {
+  if (num_req < 0 || pt_stride < 1 || ring_size < 1 || ring_size > kMaxPages) return BS_ERR_ARG;
+  if (!ring || !pool || !pool_out) return BS_ERR_NULL;
+  if (num_req > 0 && (!kv_len || !held || !change || !page_table || !kv_len_out || !held_out)) return BS_ERR_NULL;
+  return BS_OK;
+}
+
+}  // namespace
+
+BS_EXPORT int idx4_store(const void* keys, int32_t dtype, int64_t ld, const int32_t* slots, int32_t num_keys,
+                         uint8_t* codes, uint8_t* scales, int64_t cache_keys, void* stream) {
+  const int st = check_idx4_args(keys, dtype, ld, slots, num_keys, codes, scales, cache_keys);
+  if (st != BS_OK || num_keys == 0) return st;
+  return bs::launch_idx4_store(keys, dtype, ld, slots, num_keys, codes, scales, (int32_t)cache_keys,
+                               static_cast<hipStream_t>(stream));
+}
+
+BS_EXPORT int idx4_load(const uint8_t* codes, const uint8_t* scales, int64_t cache_keys, const int32_t* slots,
+                        int32_t num_slots, void* keys, int32_t dtype, int64_t ld, void* stream) {
+  const int st = check_idx4_args(keys, dtype, ld, slots, num_slots, codes, scales, cache_keys);
+  if (st != BS_OK || num_slots == 0) return st;
+  return bs::launch_idx4_load(codes, scales, (int32_t)cache_keys, slots, num_slots, keys, dtype, ld,
+                              static_cast<hipStream_t>(stream));
+}
+
+BS_EXPORT int idx4_compress_store(const uint16_t* k_raw, int32_t num_tok, const int32_t* req_tok_ptr,
+                                  const int32_t* tok_start, const int32_t* mrope_pos, int32_t num_req,
+                                  int32_t max_tok, int32_t rotary_dim, int32_t sec_t, int32_t sec_h, int32_t sec_w,
+                                  double theta, uint16_t* ring, int32_t* ring_pos, const int32_t* page_table,
+                                  int32_t pt_stride, uint8_t* codes, uint8_t* scales, int64_t num_pages,
+                                  void* stream) {
+  const int st = check_compress_args(k_raw, num_tok, req_tok_ptr, tok_start, mrope_pos, num_req, max_tok, rotary_dim,
+                                     sec_t, sec_h, sec_w, theta, ring, ring_pos, page_table, pt_stride, codes, num_pages);
+  if (st != BS_OK || num_req == 0 || num_tok == 0 || max_tok == 0) return st;
+  if (!scales) return BS_ERR_NULL;
+  if (!aligned16(codes) || !aligned16(scales)) return BS_ERR_ARG;
+  return bs::launch_compress4(k_raw, num_tok, req_tok_ptr, tok_start, mrope_pos, num_req, max_tok, rotary_dim,
+                              sec_t, sec_h, theta, ring, ring_pos, page_table, pt_stride, codes, scales, num_pages,
+                              static_cast<hipStream_t>(stream));
+}
+
+BS_EXPORT int idx4_score(const uint16_t* q, const uint8_t* codes, const uint8_t* scales, int64_t num_pages,
+                         const int32_t* page_table, int32_t pt_stride, const int32_t* req_row_ptr, int32_t num_req,
+                         const int32_t* row_pos, int32_t num_rows, int32_t c, int32_t max_vis, float* scores,
+                         int64_t ld_scores, int32_t* row_len, void* stream) {
+  const int st = check_score_args(q, reinterpret_cast<const uint16_t*>(codes), num_pages, page_table, pt_stride,
+                                  req_row_ptr, num_req, row_pos, num_rows, c, max_vis, scores, ld_scores);
+  if (st != BS_OK || num_rows == 0 || num_req == 0) return st;
+  if (!scales) return BS_ERR_NULL;
+  if (num_req > 65535 || (int64_t)max_vis > (int64_t)65535 * 4096 || num_pages > kMaxPages) return BS_ERR_ARG;
+  if (!aligned16(q) || !aligned16(codes) || !aligned16(scales)) return BS_ERR_ARG;
+  return bs::launch_idx4_score(q, codes, scales, num_pages, page_table, pt_stride, req_row_ptr, num_req, row_pos,
+                               num_rows, c, max_vis, scores, ld_scores, row_len, static_cast<hipStream_t>(stream));
+}
+
+BS_EXPORT int pages_extend(const int32_t* kv_len, const int32_t* held, const int32_t* new_len, int32_t num_req,
+                           int32_t* page_table, int32_t pt_stride, int32_t* ring, int32_t ring_size,
+                           const int32_t* pool, int32_t* kv_len_out, int32_t* held_out, int32_t* pool_out,
+                           int32_t* req_row_ptr, int32_t* row_pos, int32_t* slots, int32_t num_rows, void* stream) {
+  const int st = check_pages_args(kv_len, held, new_len, num_req, page_table, pt_stride, ring, ring_size, pool,
+                                  kv_len_out, held_out, pool_out);
+  if (st != BS_OK) return st;
+  if (num_rows < 0) return BS_ERR_ARG;
+  if (!req_row_ptr || (num_rows > 0 && (!row_pos || !slots))) return BS_ERR_NULL;
+  return bs::launch_pages({kv_len, held, new_len, num_req, page_table, pt_stride, ring, ring_size, pool, kv_len_out,
+                           held_out, pool_out, req_row_ptr, row_pos, slots, num_rows},
+                          false, static_cast<hipStream_t>(stream));
+}
+
+BS_EXPORT int pages_release(const int32_t* kv_len, const int32_t* held, const int32_t* keep_len, int32_t num_req,
+                            int32_t* page_table, int32_t pt_stride, int32_t* ring, int32_t ring_size,
+                            const int32_t* pool, int32_t* kv_len_out, int32_t* held_out, int32_t* pool_out,
+                            void* stream) {
+  const int st = check_pages_args(kv_len, held, keep_len, num_req, page_table, pt_stride, ring, ring_size, pool,
+                                  kv_len_out, held_out, pool_out);
+  if (st != BS_OK) return st;
+  return bs::launch_pages({kv_len, held, keep_len, num_req, page_table, pt_stride, ring, ring_size, pool, kv_len_out,
+                           held_out, pool_out, nullptr, nullptr, nullptr, 0},
+                          true, static_cast<hipStream_t>(stream));
 }
 
 BS_EXPORT int attn_slots(const void* q, int32_t dtype, int64_t ld_q, int32_t num_rows, int32_t q_heads,

@@ -6,9 +6,13 @@
 #include <utility>
 
 #include "kernels.h"
-#include "kv4.h"
+#include "kv8.h"
 
 namespace bs {
+
+// The cache's form, as the kernels are instantiated: 16-bit pools, the 4-bit
+// cache, the 8-bit one.
+enum : int { kForm16 = 0, kForm4 = 1, kForm8 = 2 };
 
 // How far (in log2) a score may exceed the running maximum before that moves.
 constexpr float kSlack = 8.f;

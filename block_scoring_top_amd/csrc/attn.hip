@@ -9,15 +9,16 @@
 
 namespace bs {
 
-extern template int launch_attn_prefill<Bf16, true>(const PrefillArgs&, int, int, uint32_t, hipStream_t);
-extern template int launch_attn_prefill<Bf16, false>(const PrefillArgs&, int, int, uint32_t, hipStream_t);
-extern template int launch_attn_prefill<F16, true>(const PrefillArgs&, int, int, uint32_t, hipStream_t);
-extern template int launch_attn_prefill<F16, false>(const PrefillArgs&, int, int, uint32_t, hipStream_t);
-
-extern template int launch_attn_gather<Bf16, true>(const GatherArgs&, int, int, bool, hipStream_t);
-extern template int launch_attn_gather<Bf16, false>(const GatherArgs&, int, int, bool, hipStream_t);
-extern template int launch_attn_gather<F16, true>(const GatherArgs&, int, int, bool, hipStream_t);
-extern template int launch_attn_gather<F16, false>(const GatherArgs&, int, int, bool, hipStream_t);
+#define BS_FORM(T, FORM)                                                                                       \
+  extern template int launch_attn_prefill<T, FORM>(const PrefillArgs&, int, int, uint32_t, hipStream_t);       \
+  extern template int launch_attn_gather<T, FORM>(const GatherArgs&, int, int, bool, hipStream_t);
+BS_FORM(Bf16, kForm16)
+BS_FORM(Bf16, kForm4)
+BS_FORM(Bf16, kForm8)
+BS_FORM(F16, kForm16)
+BS_FORM(F16, kForm4)
+BS_FORM(F16, kForm8)
+#undef BS_FORM
 
 namespace {
 
@@ -40,7 +41,7 @@ constexpr int64_t kPartialBytes = (int64_t)BS_ATTN_WORKSPACE_BYTES - kCounterByt
 //     820 and 925, at the end of a 64K context 1,026 and 1,015 (window 500: 207 and
 //     186); 64 x 6 rows 78 and 271.
 bool gathers(const AttnCall& c, int64_t tiles, int64_t keys, int64_t pairs, int64_t num_req) {
-  const bool kv4 = c.form == BS_KV_4;
+  const bool kv4 = c.form != BS_KV_16;
   if (pairs <= 16 || (kv4 && c.d == 256)) return true;
   const double most = kv4 ? (c.d == 64 ? 550e3 : 700e3) : c.d == 64 ? 500e3 : c.d == 128 ? 60e3 : 80e3;
   const int64_t ratio = kv4 || c.d == 64 ? 2 : 0;
@@ -65,6 +66,16 @@ constexpr double kJoinPages = 2.5, kPartsPerPage = 42, kPartPages = 1. / 6;
 constexpr int64_t kEightWaves = 512;
 // Row tiles times head blocks of a launch: 2^30 lanes.
 constexpr int64_t kMaxGroups = (int64_t)1 << 21;
+
+template <class F>
+int by_type_and_form(const AttnCall& c, F f) {
+  auto form = [&](auto t) {
+    if (c.form == BS_KV_4) return f(t, std::integral_constant<int, kForm4>());
+    if (c.form == BS_KV_8) return f(t, std::integral_constant<int, kForm8>());
+    return f(t, std::integral_constant<int, kForm16>());
+  };
+  return c.dtype == BS_BF16 ? form(Bf16()) : form(F16());
+}
 
 // The running maximum is of unscaled scores times the scale, which then must
 // not be negative (q changes sign instead) nor 0 (a masked -inf times 0): the
@@ -106,9 +117,9 @@ void split_heads(GatherArgs& a, int nt) {
 // workgroups and 256 keys a part allow, 11%: 1 row of 256 slots 5.5 and 8.0 us, 30
 // requests x 2 rows x 8 heads of D = 256 over 4,096 keys 24 and 42.
 int gather_splits(const AttnCall& c, int nt, int cols, int64_t groups, int64_t keys, int64_t most) {
-  const bool kv4 = c.form == BS_KV_4;
+  const bool kv4 = c.form != BS_KV_16;
   const double chunk = 0.6 + 0.7 * nt * c.d / 128 + (kv4 || c.d == 64 ? 0. : c.d == 256 ? 3. : 1.1);
-  const double read = groups * keys * c.d * (kv4 ? 17. / 16 : 4.) / 4.5e6;
+  const double read = groups * keys * c.d * (c.form == BS_KV_4 ? 17. / 16 : kv4 ? 2. : 4.) / 4.5e6;
   const double part = cols * (c.d + 4) * 4e-6 * groups, rounds = cols * c.d / 16384.;
   int64_t best = 1;
   double least = 0;
@@ -138,11 +149,9 @@ int run_gather(GatherArgs& a, const AttnCall& c, int nt, bool window, int64_t ti
   // Rows of a request read many of the same keys: 64 x 6 verify rows of 2,051
   // slots (4-bit) 42.0 us with eight neighbours on an XCD, 44.8 without.
   a.xcd_rows = tiles >= 64;
-  if (c.dtype == BS_BF16)
-    return c.form == BS_KV_4 ? launch_attn_gather<Bf16, true>(a, c.d, nt, window, stream)
-                             : launch_attn_gather<Bf16, false>(a, c.d, nt, window, stream);
-  return c.form == BS_KV_4 ? launch_attn_gather<F16, true>(a, c.d, nt, window, stream)
-                           : launch_attn_gather<F16, false>(a, c.d, nt, window, stream);
+  return by_type_and_form(c, [&](auto t, auto form) {
+    return launch_attn_gather<decltype(t), decltype(form)::value>(a, c.d, nt, window, stream);
+  });
 }
 
 int run_prefill(const AttnCall& c, const int32_t* page_table, int32_t pt_stride, const int32_t* req_row_ptr,
@@ -192,11 +201,9 @@ int run_prefill(const AttnCall& c, const int32_t* page_table, int32_t pt_stride,
   if (blocks > kMaxGroups) return BS_ERR_ARG;
   a.groups = (uint32_t)blocks;
   const uint32_t grid = (a.groups * a.nsplit + 63) / 64 * 64;
-  if (c.dtype == BS_BF16)
-    return c.form == BS_KV_4 ? launch_attn_prefill<Bf16, true>(a, c.d, waves, grid, stream)
-                             : launch_attn_prefill<Bf16, false>(a, c.d, waves, grid, stream);
-  return c.form == BS_KV_4 ? launch_attn_prefill<F16, true>(a, c.d, waves, grid, stream)
-                           : launch_attn_prefill<F16, false>(a, c.d, waves, grid, stream);
+  return by_type_and_form(c, [&](auto t, auto form) {
+    return launch_attn_prefill<decltype(t), decltype(form)::value>(a, c.d, waves, grid, stream);
+  });
 }
 
 }  // namespace

@@ -50,7 +50,7 @@ constexpr int kGaKeys = 32;  // keys per wave and step
 struct GatherArgs {
   const void* q;
   int64_t ld_q;
-  const uint8_t *a, *b;  // 4-bit: codes, scales; 16-bit: K and V pools
+  const uint8_t *a, *b;  // 4-bit and 8-bit: codes, scales; 16-bit: K and V pools
   int64_t ld_kv;         // 16-bit pools: elements from one slot to the next
   int32_t num_slots, num_rows, hq, hkv;
   int32_t gb, hblocks;   // heads per block and blocks of one kv head's query heads
@@ -73,10 +73,11 @@ struct GatherArgs {
   bool xcd_rows;
 };
 
-template <bool FP4, int D>
+template <int FORM, int D>
 struct GatherRaw {
-  static constexpr int kKDwords = FP4 ? D / 32 : D / 8;                 // a quarter of a key's row
-  static constexpr int kVDwords = FP4 ? (D < 128 ? 1 : D / 128) : D / 32;  // D/16 channels of a key
+  static constexpr int kKDwords = FORM == kForm4 ? D / 32 : FORM == kForm8 ? D / 16 : D / 8;  // a quarter of a key's row
+  // D/16 channels of a key
+  static constexpr int kVDwords = FORM == kForm4 ? (D < 128 ? 1 : D / 128) : FORM == kForm8 ? D / 64 : D / 32;
   uint32_t k[2][kKDwords];
   uint32_t v[8][kVDwords];
 };
@@ -110,17 +111,19 @@ __device__ __forceinline__ void load_dwords(uint32_t (&dst)[N], const uint8_t* p
 // pools are staged at D = 64 only: larger chunks would leave LDS for too few
 // waves.
 //
-// A buffer holds the rows of the 32 keys (4-bit: K and V codes, which lie
-// together, then the scales; 16-bit: K, then V), their 16-byte pieces XOR-ed
+// A buffer holds the rows of the 32 keys (4-bit and 8-bit: K and V codes, which
+// lie together, then the scales; 16-bit: K, then V), their 16-byte pieces XOR-ed
 // with a function of the key that spreads the operands' reads over the banks.
-template <bool FP4, int D>
+template <int FORM, int D>
 struct Staging {
-  static constexpr bool kUsed = FP4 || D == 64;
-  static constexpr int kRow = FP4 ? D : 2 * D, kArrays = FP4 ? 1 : 2;
+  static constexpr bool kUsed = FORM != kForm16 || D == 64;
+  static constexpr int kRow = FORM == kForm4 ? D : 2 * D, kArrays = FORM == kForm16 ? 2 : 1;
   static constexpr int kLanes = kRow / 16, kKeysPerCopy = 64 / kLanes, kCopies = kGaKeys / kKeysPerCopy;
-  static constexpr int kScales = kArrays * kGaKeys * kRow, kBytes = kScales + (FP4 ? kGaKeys * D / 16 : 0);
-  static constexpr int kInFlight = kArrays * kCopies + (FP4 ? 1 : 0);  // copy instructions a chunk
+  static constexpr int kScaleBytes = FORM == kForm4 ? D / 16 : FORM == kForm8 ? 8 : 0;  // of a key
+  static constexpr int kScales = kArrays * kGaKeys * kRow, kBytes = kScales + kGaKeys * kScaleBytes;
+  static constexpr int kInFlight = kArrays * kCopies + (FORM != kForm16 ? 1 : 0);  // copy instructions a chunk
   static __device__ __forceinline__ int swizzle(int key) {
+    if (FORM == kForm8 && kRow >= 256) return key & 15;
     return kRow == 64 ? key >> 2 & 3 : kRow == 128 ? (key >> 1 & 3) | (key & 4) : key & 7;
   }
   static __device__ __forceinline__ const uint8_t* at(const uint8_t* buf, int key, int byte) {
@@ -147,14 +150,15 @@ __device__ __forceinline__ void wait_copies() {
 // 64 KiB in flight): 64 decode rows of 2,051 slots, D = 256, 16-bit pool 60 us,
 // 131 with two.  Four where two registers decide between three and four: 1,024
 // rows of 2,051 slots, 4-bit, D = 128: 71 us, 75 with three.
-constexpr int gather_waves(bool fp4, int d, int nt, bool window) {
-  return nt * d == 256 && !fp4 ? 1 : fp4 && nt * d == 128 && !window ? 4 : 2;
+constexpr int gather_waves(int form, int d, int nt, bool window) {
+  return nt * d == 256 && form != kForm4 ? 1 : form == kForm4 && nt * d == 128 && !window ? 4 : 2;
 }
 
-template <class T, bool FP4, int D, int NT, bool WINDOW>
-__global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT, WINDOW)) void attn_gather_kernel(const GatherArgs a) {
-  typedef GatherRaw<FP4, D> Raw;
-  typedef Staging<FP4, D> Stage;
+template <class T, int FORM, int D, int NT, bool WINDOW>
+__global__ __launch_bounds__(64 * kGaWaves, gather_waves(FORM, D, NT, WINDOW)) void attn_gather_kernel(const GatherArgs a) {
+  constexpr bool FP4 = FORM == kForm4, FP8 = FORM == kForm8;
+  typedef GatherRaw<FORM, D> Raw;
+  typedef Staging<FORM, D> Stage;
   constexpr int KS = D / 32;       // 32-channel steps of the score product
   constexpr int VD = D / 16;       // channels of the output per lane and accumulator row
   constexpr int COLS = 16 * NT;    // (row, head) pairs of a tile
@@ -222,6 +226,7 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT, WINDOW)) vo
   // the wave (their order is free): those that its 16-byte loads of a key hold,
   // which four quarters make 64 contiguous bytes.
   auto channel = [&](int ks) {
+    if constexpr (FP8) return 64 * (ks / 2) + 16 * qd + 8 * (ks % 2);
     return !FP4 ? 32 * ks + 8 * qd : D == 64 ? 16 * qd + 8 * ks : 128 * (ks / 4) + 32 * qd + 8 * (ks % 4);
   };
   // This lane's query vectors (column 16*nt + n16 of the tile).
@@ -270,7 +275,7 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT, WINDOW)) vo
   auto put_offsets = [&](int sl, uint32_t& mask) {
     const bool ok = sl >= 0 && sl < a.num_slots;
     mask = (uint32_t)ballot(ok);
-    const uint32_t rec = FP4 ? (uint32_t)a.hkv * D : (uint32_t)a.ld_kv * 2;
+    const uint32_t rec = FP4 ? (uint32_t)a.hkv * D : FP8 ? (uint32_t)a.hkv * 2 * D : (uint32_t)a.ld_kv * 2;
     wave_fence();
     if (lane < kGaKeys) sh.st.at[wave][lane] = (uint64_t)(uint32_t)(ok ? sl : 0) * rec;
     wave_fence();
@@ -314,6 +319,11 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT, WINDOW)) vo
   };
   auto copy_rows = [&](int sl, int buf, uint32_t& mask) {
     put_offsets(sl, mask);
+    uint32_t page_of = 0;
+    if constexpr (FP8) {
+      const uint32_t x = __shfl(sl, lane >> 1);
+      page_of = x < (uint32_t)a.num_slots ? x : 0;
+    }
     const uint64_t* ls = sh.st.at[wave];
     const uint32_t dst = lds_buf + buf * Stage::kBytes;
     // The buffer's last operands have been read, and so have the slot numbers.
@@ -323,8 +333,10 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT, WINDOW)) vo
       const int key = i * Stage::kKeysPerCopy + lane / Stage::kLanes;
       const uint64_t at = ls[key] + kvh * Stage::kRow + ((lane % Stage::kLanes) ^ Stage::swizzle(key)) * 16;
       copy_to_lds16(a.a + at, dst + i * 1024);
-      if constexpr (!FP4) copy_to_lds16(a.b + at, dst + kGaKeys * Stage::kRow + i * 1024);
+      if constexpr (FORM == kForm16) copy_to_lds16(a.b + at, dst + kGaKeys * Stage::kRow + i * 1024);
     }
+    if constexpr (FP8)  // the scales of each key's page: a lane's is K's or V's
+      copy_to_lds4(a.b + ((uint64_t)(page_of >> 6) * a.hkv + kvh) * 8 + (lane & 1) * 4, dst + Stage::kScales);
     if constexpr (FP4) {
       const uint8_t* sc = a.b + kvh * (D / 16);
       if constexpr (D == 64) {
@@ -350,10 +362,11 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT, WINDOW)) vo
         for (int i = 0; i < Raw::kKDwords; i += 4) load_4dwords(&r.k[j][i], Stage::at(rows, key, 16 * i + qd * 16));
       }
     }
-    const uint8_t* v = FP4 ? rows : rows + kGaKeys * Stage::kRow;
+    const uint8_t* v = FORM != kForm16 ? rows : rows + kGaKeys * Stage::kRow;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint8_t* p = Stage::at(v, (j >> 2) * 16 + 4 * qd + (j & 3), FP4 ? D / 2 + n16 * (D / 32) : n16 * (D / 8));
+      const uint8_t* p = Stage::at(v, (j >> 2) * 16 + 4 * qd + (j & 3),
+                                   FP4 ? D / 2 + n16 * (D / 32) : FP8 ? D + n16 * (D / 16) : n16 * (D / 8));
       if constexpr (FP4 && D == 64)
         r.v[j][0] = *reinterpret_cast<const uint16_t*>(p);
       else
@@ -380,6 +393,13 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT, WINDOW)) vo
       for (int j = 0; j < 8; ++j)
         vscale[j] = kv4_scale(sc[((j >> 2) * 16 + 4 * qd + (j & 3)) * (D / 16) + D / 32 + n16 * D / 512]);
     }
+    if constexpr (FP8) {
+      const float* sc = reinterpret_cast<const float*>(sh.st.buf[wave][buf] + Stage::kScales);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) kscale[j][0] = sc[2 * (16 * j + n16)];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) vscale[j] = sc[2 * ((j >> 2) * 16 + 4 * qd + (j & 3)) + 1];
+    }
     // Keys without a slot: their K is read from slot 0 and masked below,
     // their V must be zeros (0 * NaN is not 0).
     // Bit j: is there a key of v[j]?  (Opaque, or its eight tests move in front
@@ -396,7 +416,7 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT, WINDOW)) vo
         const bool ok = (there >> j) & 1u;
 #pragma unroll
         for (int i = 0; i < Raw::kVDwords; ++i) r.v[j][i] = ok ? r.v[j][i] : 0u;
-        if constexpr (FP4) vscale[j] = ok ? vscale[j] : 1.f;
+        if constexpr (FP4 || FP8) vscale[j] = ok ? vscale[j] : 1.f;
       }
     }
 
@@ -413,6 +433,11 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT, WINDOW)) vo
           const uint32_t w = r.k[j][ks];
           kf = u32x4_t{T::template from_fp4<0>(w, sc), T::template from_fp4<1>(w, sc), T::template from_fp4<2>(w, sc),
                        T::template from_fp4<3>(w, sc)};
+        } else if constexpr (FP8) {
+          const float sc = kscale[j][0];
+          const uint32_t w0 = r.k[j][2 * ks], w1 = r.k[j][2 * ks + 1];
+          kf = u32x4_t{T::template from_fp8<0>(w0, sc), T::template from_fp8<1>(w0, sc), T::template from_fp8<0>(w1, sc),
+                       T::template from_fp8<1>(w1, sc)};
         } else {
           kf = u32x4_t{r.k[j][4 * ks], r.k[j][4 * ks + 1], r.k[j][4 * ks + 2], r.k[j][4 * ks + 3]};
         }
@@ -488,6 +513,10 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT, WINDOW)) vo
         for (int j = 0; j < 8; ++j) {
           if constexpr (FP4) {
             bad |= vscale[j] > T::kTopScale;
+          } else if constexpr (FP8) {
+            bad |= vscale[j] > T::kTopScale8;
+#pragma unroll
+            for (int i = 0; i < Raw::kVDwords; ++i) bad |= kv8_nan_codes(r.v[j][i]);
           } else {
 #pragma unroll
             for (int i = 0; i < Raw::kVDwords; ++i) bad |= nonfinite_pair<T>(r.v[j][i]);
@@ -503,6 +532,8 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT, WINDOW)) vo
       for (int j = 0; j < 8; ++j) {
         if constexpr (FP4)
           two[j] = T::template from_fp4<pi % 4>(r.v[j][pi / 4], vscale[j]);
+        else if constexpr (FP8)
+          two[j] = T::template from_fp8<pi % 2>(r.v[j][pi / 2], vscale[j]);
         else
           two[j] = r.v[j][pi];
       }
@@ -689,11 +720,11 @@ __global__ __launch_bounds__(64 * kGaWaves, gather_waves(FP4, D, NT, WINDOW)) vo
 }
 
 // nt: column tiles of a workgroup, 1 or (head_dim up to 128: registers) 2.
-template <class T, bool FP4>
+template <class T, int FORM>
 int launch_attn_gather(const GatherArgs& a, int d, int nt, bool window, hipStream_t stream) {
   const dim3 grid(a.xcd_rows ? (a.tiles + 63) / 64 * 64 : a.tiles, a.hkv * a.hblocks, a.nsplit);
   auto go = [&](auto dim, auto tiles, auto win) {
-    hipLaunchKernelGGL((attn_gather_kernel<T, FP4, decltype(dim)::value, decltype(tiles)::value, decltype(win)::value>),
+    hipLaunchKernelGGL((attn_gather_kernel<T, FORM, decltype(dim)::value, decltype(tiles)::value, decltype(win)::value>),
                        grid, dim3(64 * kGaWaves), 0, stream, a);
   };
   auto by_window = [&](auto dim, auto tiles) {

@@ -3,6 +3,6 @@
 
 namespace bs {
 
-template int launch_attn_gather<F16, false>(const GatherArgs&, int, int, bool, hipStream_t);
+template int launch_attn_gather<F16, kForm16>(const GatherArgs&, int, int, bool, hipStream_t);
 
 }  // namespace bs

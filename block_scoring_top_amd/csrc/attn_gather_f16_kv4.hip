@@ -3,6 +3,6 @@
 
 namespace bs {
 
-template int launch_attn_gather<F16, true>(const GatherArgs&, int, int, bool, hipStream_t);
+template int launch_attn_gather<F16, kForm4>(const GatherArgs&, int, int, bool, hipStream_t);
 
 }  // namespace bs

@@ -7,8 +7,8 @@
 // (the heads of a group packed beside the rows, so that a tile spans few
 // positions) and walks the pages of its keys; a page is a tile of 64 keys:
 //   * K and V pages are copied from HBM straight into LDS (16-bit pools), or
-//     loaded into registers, converted and written there (4-bit cache), one
-//     page ahead, two buffers, one barrier a page;
+//     loaded into registers, converted and written there (codes), one page
+//     ahead, two buffers, one barrier a page;
 //   * S^T = K q^T with v_mfma_f32_32x32x16: a lane holds one query vector and
 //     16 of every 32 keys, so the row maximum and sum need one exchange
 //     between the wave's halves;
@@ -92,8 +92,9 @@ __device__ __forceinline__ u32x2_t lds_read_tr(const uint8_t* p) {
                                          (__attribute__((address_space(3))) i16x4_t*)(uintptr_t)(uint32_t)(uintptr_t)p));
 }
 
-template <class T, bool FP4, int D, int NW>
+template <class T, int FORM, int D, int NW>
 __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prefill_kernel(const PrefillArgs a) {
+  constexpr bool FP4 = FORM == kForm4, FP8 = FORM == kForm8, CODES = FP4 || FP8;
   constexpr int ROW = D * 2;                // bytes of a key in LDS
   constexpr int NS = D / 8;                 // its 16-byte slices
   constexpr int KSWZ = NS < 16 ? NS - 1 : 15, VSWZ = NS < 16 ? NS - 1 : 15;
@@ -167,10 +168,10 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prefill_kernel
     return i;
   };
 
-  // 4-bit: what a thread holds of the next page: 32 channels (16 bytes of
-  // codes and their scale) of K or V, UNITS times.
-  constexpr int PIECES = kPage * D / 16, UNITS = FP4 ? (PIECES + THREADS - 1) / THREADS : 1;
-  static_assert(FP4 || kPage * NS % THREADS == 0, "the copies fill whole waves");
+  // 4-bit (8-bit): what a thread holds of the next page: 32 (16) channels, 16
+  // bytes of codes, and their scale, of K or V, UNITS times.
+  constexpr int PARTS = FP8 ? D / 8 : D / 16, PIECES = kPage * PARTS, UNITS = CODES ? (PIECES + THREADS - 1) / THREADS : 1;
+  static_assert(CODES || kPage * NS % THREADS == 0, "the copies fill whole waves");
   u32x4_t codes[UNITS];
   uint32_t scale[UNITS];
   auto issue = [&](int page, int buf) {
@@ -184,6 +185,17 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prefill_kernel
         if (PIECES % THREADS != 0 && x >= PIECES) continue;
         codes[u] = *reinterpret_cast<const u32x4_t*>(c0 + (uint64_t)key * rec + part * 16);
         scale[u] = s0[(uint64_t)key * (rec / 16) + part];
+      }
+    } else if constexpr (FP8) {
+      const uint64_t rec = (uint64_t)a.hkv * 2 * D;
+      const uint8_t* c0 = a.a + (uint64_t)page * kPage * rec + kvh * 2 * D;
+      const uint32_t* s0 = reinterpret_cast<const uint32_t*>(a.b) + ((uint64_t)page * a.hkv + kvh) * 2;
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) {
+        const int x = u * THREADS + tid, key = x / PARTS, part = x % PARTS;
+        if (PIECES % THREADS != 0 && x >= PIECES) continue;
+        codes[u] = *reinterpret_cast<const u32x4_t*>(c0 + (uint64_t)key * rec + part * 16);
+        scale[u] = s0[part >= PARTS / 2];
       }
     } else {
       const uint32_t rec = (uint32_t)(a.ld_kv * 2), bytes = rec * (kPage - 1) + D * 2;
@@ -217,6 +229,22 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prefill_kernel
           *reinterpret_cast<u32x4_t*>(row + ((s + i) ^ f) * 16) =
               u32x4_t{T::template from_fp4<0>(w, sc), T::template from_fp4<1>(w, sc), T::template from_fp4<2>(w, sc),
                       T::template from_fp4<3>(w, sc)};
+        }
+      }
+    } else if constexpr (FP8) {
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) {
+        const int x = u * THREADS + tid, key = x / PARTS, part = x % PARTS;
+        if (PIECES % THREADS != 0 && x >= PIECES) continue;
+        const int which = part >= PARTS / 2, s = (part % (PARTS / 2)) * 2, f = which ? (2 * key) & VSWZ : key & KSWZ;
+        uint8_t* row = &kv[buf][which][key * ROW];
+        const float sc = __uint_as_float(scale[u]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t w0 = codes[u][2 * i], w1 = codes[u][2 * i + 1];
+          *reinterpret_cast<u32x4_t*>(row + ((s + i) ^ f) * 16) =
+              u32x4_t{T::template from_fp8<0>(w0, sc), T::template from_fp8<1>(w0, sc), T::template from_fp8<0>(w1, sc),
+                      T::template from_fp8<1>(w1, sc)};
         }
       }
     } else {
@@ -493,12 +521,12 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const PrefillArgs a) {
                   a.lse == nullptr ? nullptr : a.lse + (int64_t)(w.row0 + rr) * a.hq + w.h0 + hh);
 }
 
-template <class T, bool FP4>
+template <class T, int FORM>
 int launch_attn_prefill(const PrefillArgs& a, int d, int waves, uint32_t grid, hipStream_t stream) {
   auto go = [&](auto dim, auto nw) {
     constexpr int NW = decltype(nw)::value;
     constexpr int D = decltype(dim)::value, COLS = 32 * NW;
-    hipLaunchKernelGGL((attn_prefill_kernel<T, FP4, D, NW>), dim3(grid), dim3(64 * NW), 0, stream, a);
+    hipLaunchKernelGGL((attn_prefill_kernel<T, FORM, D, NW>), dim3(grid), dim3(64 * NW), 0, stream, a);
     if (a.nsplit > 1)
       hipLaunchKernelGGL((attn_join_kernel<T, D, COLS>), dim3(a.groups * (COLS * D / 4 / 256)), dim3(256), 0, stream, a);
   };
@@ -512,7 +540,7 @@ int launch_attn_prefill(const PrefillArgs& a, int d, int waves, uint32_t grid, h
     by_waves(std::integral_constant<int, 64>());
   else if (d == 128)
     by_waves(std::integral_constant<int, 128>());
-  else if constexpr (!FP4)  // the registers hold one wave a SIMD; the 4-bit cache is gathered at this size
+  else if constexpr (FORM == kForm16)  // the registers hold one wave a SIMD; codes are gathered at this size
     go(std::integral_constant<int, 256>(), std::integral_constant<int, 4>());
   return hipGetLastError() == hipSuccess ? BS_OK : BS_ERR_LAUNCH;
 }

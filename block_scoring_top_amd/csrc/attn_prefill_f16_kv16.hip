@@ -3,6 +3,6 @@
 
 namespace bs {
 
-template int launch_attn_prefill<F16, false>(const PrefillArgs&, int, int, uint32_t, hipStream_t);
+template int launch_attn_prefill<F16, kForm16>(const PrefillArgs&, int, int, uint32_t, hipStream_t);
 
 }  // namespace bs

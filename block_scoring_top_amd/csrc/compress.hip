@@ -26,7 +26,7 @@
 // consumed any ring entries.
 #include <cmath>
 
-#include "device.h"
+#include "idx4.h"
 #include "kernels.h"
 
 namespace bs {
@@ -54,13 +54,16 @@ __device__ __forceinline__ float wave_max(float v) {
 
 }  // namespace
 
+// FOUR: the keys, rounded to bf16 all the same, are then quantised into the
+// 4-bit cache (kcache: codes) in place of being stored as they are.
+template <bool FOUR>
 __global__ __launch_bounds__(64) void compress_kernel(
     const uint16_t* __restrict__ k_raw, int32_t num_tok, const int32_t* __restrict__ req_tok_ptr,
     const int32_t* __restrict__ tok_start, const int32_t* __restrict__ mrope_pos, int32_t max_tok,
     int32_t rot, int32_t sec0, int32_t sec01, double base,
     uint16_t* ring, int32_t* ring_pos,
     const int32_t* __restrict__ page_table, int32_t pt_stride,
-    uint16_t* __restrict__ kcache, int64_t num_pages) {
+    uint16_t* __restrict__ kcache, uint8_t* __restrict__ scales, int64_t num_pages) {
   __shared__ __align__(16) uint16_t raw[4][kDim];
   __shared__ float ys[kDim];
   __shared__ __align__(16) uint16_t outs[kDim];
@@ -167,8 +170,19 @@ __global__ __launch_bounds__(64) void compress_kernel(
     __syncthreads();
 
     if (page >= 0 && page < num_pages) {
-      uint16_t* dst = kcache + ((int64_t)page * (kPage / 4) + (j & (kPage / 4 - 1))) * kDim;
-      reinterpret_cast<uint32_t*>(dst)[lane] = reinterpret_cast<const uint32_t*>(outs)[lane];
+      const int64_t slot = (int64_t)page * (kPage / 4) + (j & (kPage / 4 - 1));
+      if constexpr (FOUR) {
+        if (lane < kDim / 8) {
+          Chunk<Bf16> x;
+          x.load(outs + lane * 8);
+          bool bad;
+          const uint32_t ex = group_exponent(quad_max(x.top()), bad);
+          reinterpret_cast<uint32_t*>(kcache)[slot * (kIdxCodes / 4) + lane] = bad ? 0u : x.codes(kv4_scale(ex));
+          if ((lane & 3) == 0) scales[slot * kIdxScales + lane / 4] = (uint8_t)(bad ? kExpNan : ex);
+        }
+      } else {
+        reinterpret_cast<uint32_t*>(kcache + slot * kDim)[lane] = reinterpret_cast<const uint32_t*>(outs)[lane];
+      }
     }
   }
 
@@ -182,18 +196,41 @@ __global__ __launch_bounds__(64) void compress_kernel(
   }
 }
 
+namespace {
+
+template <bool FOUR>
+int launch(const uint16_t* k_raw, int32_t num_tok, const int32_t* req_tok_ptr, const int32_t* tok_start,
+           const int32_t* mrope_pos, int32_t num_req, int32_t max_tok, int32_t rotary_dim, int32_t sec_t, int32_t sec_h,
+           double theta, uint16_t* ring, int32_t* ring_pos, const int32_t* page_table, int32_t pt_stride,
+           uint16_t* kcache, uint8_t* scales, int64_t num_pages, hipStream_t stream) {
+  const int items = max(1, (max_tok + 3) / 4);
+  // theta^(-2/rot), the ratio of successive pair frequencies
+  const double base = rotary_dim > 0 ? std::pow(theta, -2.0 / (double)rotary_dim) : 1.0;
+  hipLaunchKernelGGL(compress_kernel<FOUR>, dim3(items, num_req), dim3(64), 0, stream, k_raw, num_tok, req_tok_ptr,
+                     tok_start, mrope_pos, max_tok, rotary_dim, sec_t, sec_t + sec_h, base, ring, ring_pos,
+                     page_table, pt_stride, kcache, scales, num_pages);
+  return hipGetLastError() == hipSuccess ? BS_OK : BS_ERR_LAUNCH;
+}
+
+}  // namespace
+
 int launch_compress(const uint16_t* k_raw, int32_t num_tok, const int32_t* req_tok_ptr, const int32_t* tok_start,
                     const int32_t* mrope_pos, int32_t num_req, int32_t max_tok, int32_t rotary_dim,
                     int32_t sec_t, int32_t sec_h, double theta, uint16_t* ring, int32_t* ring_pos,
                     const int32_t* page_table, int32_t pt_stride, uint16_t* kcache, int64_t num_pages,
                     hipStream_t stream) {
-  const int items = max(1, (max_tok + 3) / 4);
-  // theta^(-2/rot), the ratio of successive pair frequencies
-  const double base = rotary_dim > 0 ? std::pow(theta, -2.0 / (double)rotary_dim) : 1.0;
-  hipLaunchKernelGGL(compress_kernel, dim3(items, num_req), dim3(64), 0, stream, k_raw, num_tok, req_tok_ptr,
-                     tok_start, mrope_pos, max_tok, rotary_dim, sec_t, sec_t + sec_h, base, ring, ring_pos,
-                     page_table, pt_stride, kcache, num_pages);
-  return hipGetLastError() == hipSuccess ? BS_OK : BS_ERR_LAUNCH;
+  return launch<false>(k_raw, num_tok, req_tok_ptr, tok_start, mrope_pos, num_req, max_tok, rotary_dim, sec_t, sec_h,
+                       theta, ring, ring_pos, page_table, pt_stride, kcache, nullptr, num_pages, stream);
+}
+
+int launch_compress4(const uint16_t* k_raw, int32_t num_tok, const int32_t* req_tok_ptr, const int32_t* tok_start,
+                     const int32_t* mrope_pos, int32_t num_req, int32_t max_tok, int32_t rotary_dim,
+                     int32_t sec_t, int32_t sec_h, double theta, uint16_t* ring, int32_t* ring_pos,
+                     const int32_t* page_table, int32_t pt_stride, uint8_t* codes, uint8_t* scales, int64_t num_pages,
+                     hipStream_t stream) {
+  return launch<true>(k_raw, num_tok, req_tok_ptr, tok_start, mrope_pos, num_req, max_tok, rotary_dim, sec_t, sec_h,
+                      theta, ring, ring_pos, page_table, pt_stride, reinterpret_cast<uint16_t*>(codes), scales, num_pages,
+                      stream);
 }
 
 }  // namespace bs

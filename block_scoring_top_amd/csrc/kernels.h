@@ -70,6 +70,46 @@ int launch_compress(const uint16_t* k_raw, int32_t num_tok, const int32_t* req_t
                     int32_t sec_t, int32_t sec_h, double theta, uint16_t* ring, int32_t* ring_pos,
                     const int32_t* page_table, int32_t pt_stride, uint16_t* kcache, int64_t num_pages,
                     hipStream_t stream);
+// The same into the 4-bit index keys.
+int launch_compress4(const uint16_t* k_raw, int32_t num_tok, const int32_t* req_tok_ptr, const int32_t* tok_start,
+                     const int32_t* mrope_pos, int32_t num_req, int32_t max_tok, int32_t rotary_dim,
+                     int32_t sec_t, int32_t sec_h, double theta, uint16_t* ring, int32_t* ring_pos,
+                     const int32_t* page_table, int32_t pt_stride, uint8_t* codes, uint8_t* scales, int64_t num_pages,
+                     hipStream_t stream);
+
+// The page tables of a batch; arguments validated by the caller.  change: new
+// tokens (extend) or tokens to keep (release).
+struct PagesCall {
+  const int32_t *kv_len, *held, *change;
+  int32_t num_req;
+  int32_t* page_table;
+  int32_t pt_stride;
+  int32_t* ring;
+  int32_t ring_size;
+  const int32_t* pool;
+  int32_t *kv_len_out, *held_out, *pool_out;
+  int32_t *req_row_ptr, *row_pos, *slots;  // extend
+  int32_t num_rows;
+};
+int launch_pages(const PagesCall& a, bool release, hipStream_t stream);
+
+// The 8-bit KV cache; arguments validated by the caller.
+int launch_kv8_store(const void* k, const void* v, int32_t dtype, int64_t ld_k, int64_t ld_v, const int32_t* slots,
+                     int32_t num_tok, int32_t hkv, int32_t d, uint8_t* codes, float* scales, int32_t num_slots,
+                     hipStream_t stream);
+int launch_kv8_load(const uint8_t* codes, const float* scales, int32_t num_slots, const int32_t* slots,
+                    int32_t num_slot_ids, int32_t hkv, int32_t d, void* k, void* v, int32_t dtype, int64_t ld_k,
+                    int64_t ld_v, hipStream_t stream);
+
+// The 4-bit index keys; arguments validated by the caller.
+int launch_idx4_store(const void* keys, int32_t dtype, int64_t ld, const int32_t* slots, int32_t num_keys,
+                      uint8_t* codes, uint8_t* scales, int32_t num_slots, hipStream_t stream);
+int launch_idx4_load(const uint8_t* codes, const uint8_t* scales, int32_t num_slots, const int32_t* slots,
+                     int32_t num_slot_ids, void* out, int32_t dtype, int64_t ld, hipStream_t stream);
+int launch_idx4_score(const uint16_t* q, const uint8_t* codes, const uint8_t* scales, int64_t num_pages,
+                      const int32_t* page_table, int32_t pt_stride, const int32_t* req_row_ptr, int32_t num_req,
+                      const int32_t* row_pos, int32_t num_rows, int32_t c, int32_t max_vis, float* scores, int64_t ld,
+                      int32_t* row_len, hipStream_t stream);
 
 // The 4-bit KV cache; arguments validated by the caller.
 int launch_kv4_store(const void* k, const void* v, int32_t dtype, int64_t ld_k, int64_t ld_v, const int32_t* slots,

@@ -21,67 +21,6 @@
 
 namespace bs {
 
-namespace {
-
-__device__ __forceinline__ uint32_t quad_max(uint32_t x) {
-  x = max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, kDppQuadXor1, 0xF, 0xF, true));
-  return max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, kDppQuadXor2, 0xF, 0xF, true));
-}
-
-// 8 channels as loaded: 4 pairs of 16-bit values, or 8 floats.
-template <class T>
-struct Chunk {
-  u32x4_t v;
-  __device__ __forceinline__ void load(const void* p) { v = *reinterpret_cast<const u32x4_t*>(p); }
-  __device__ __forceinline__ uint32_t top() const {
-    return max(max(T::abs_bits(v.x), T::abs_bits(v.y)), max(T::abs_bits(v.z), T::abs_bits(v.w)));
-  }
-  __device__ __forceinline__ uint32_t codes(float s) const {
-    uint32_t c = T::template to_fp4<0>(0u, v.x, s);
-    c = T::template to_fp4<1>(c, v.y, s);
-    c = T::template to_fp4<2>(c, v.z, s);
-    return T::template to_fp4<3>(c, v.w, s);
-  }
-  __device__ __forceinline__ void values(uint32_t c, float s) {
-    v = u32x4_t{T::template from_fp4<0>(c, s), T::template from_fp4<1>(c, s), T::template from_fp4<2>(c, s),
-                T::template from_fp4<3>(c, s)};
-  }
-  __device__ __forceinline__ void store(void* p) const { __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(p)); }
-};
-
-template <>
-struct Chunk<F32> {
-  float v[8];
-  __device__ __forceinline__ void load(const void* p) {
-    const f32x4_t a = reinterpret_cast<const f32x4_t*>(p)[0], b = reinterpret_cast<const f32x4_t*>(p)[1];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
-  }
-  __device__ __forceinline__ uint32_t top() const {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    return m;
-  }
-  __device__ __forceinline__ uint32_t codes(float s) const {
-    uint32_t c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v[0], v[1], s, 0);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2], v[3], s, 1);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4], v[5], s, 2);
-    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6], v[7], s, 3);
-  }
-  __device__ __forceinline__ void values(uint32_t c, float s) {
-    const f32x2_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 1);
-    const f32x2_t d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 2), e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 3);
-    v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y, v[4] = d.x, v[5] = d.y, v[6] = e.x, v[7] = e.y;
-  }
-  __device__ __forceinline__ void store(void* p) const {
-    __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4_t*>(p));
-    __builtin_nontemporal_store(f32x4_t{v[4], v[5], v[6], v[7]}, reinterpret_cast<f32x4_t*>(p) + 1);
-  }
-};
-
-}  // namespace
-
 // Lane `id` of a call: 8 channels of a row; a row's lanes go through its
 // heads, K then V of each, so that a wave writes whole lines of codes.
 template <int D>

@@ -15,7 +15,12 @@
  * What consumes the chosen slots: attn_slots (attention over each row's
  * slots) and attn_window (a sliding window and a few first tokens, for the
  * layers without an indexer), over 16-bit K/V pools or a 4-bit cache that
- * kv4_store writes and kv4_load reads back.
+ * kv4_store writes and kv4_load reads back, or an 8-bit one (kv8_store,
+ * kv8_load).
+ *
+ * The index keys may be held in 4 bits: idx4_store and idx4_compress_store
+ * write them, idx4_score is step 1 over them.  The tables, positions and slots
+ * that all calls take can be kept on the GPU: pages_extend, pages_release.
  *
  * Sources (pages on the subject):
  *   [QSA]   "Qwen3.8-Flash-Next Day-0 in SGLang" (theainews.cc), section on Qwen
@@ -417,7 +422,8 @@ enum bs_dtype { BS_BF16 = 0, BS_F16 = 1, BS_F32 = 2 };
 enum bs_kv_form {
   BS_KV_16 = 0, /* cache0, cache1: K and V pools of the queries' 16-bit type, [num_pages * 64] slots of
                    [kv_heads][head_dim], ld_cache elements from a slot to the next (kv_heads * head_dim .. 2^24) */
-  BS_KV_4 = 1   /* cache0, cache1: codes and scales as kv4_store writes them; ld_cache is not used */
+  BS_KV_4 = 1,  /* cache0, cache1: codes and scales as kv4_store writes them; ld_cache is not used */
+  BS_KV_8 = 8   /* the same of kv8_store */
 };
 
 /*
@@ -464,6 +470,147 @@ int kv4_load(const uint8_t* codes, const uint8_t* scales, int64_t num_pages, con
              void* stream);
 
 /*
+ * The 8-bit KV cache.  Per (slot, kv head):
+ *   codes  [num_pages * 64][kv_heads][2][head_dim] uint8: K, then V; E4M3 (sign,
+ *          4 exponent bits of bias 7, 3 mantissa bits; 0x7F and 0xFF: NaN).
+ * Per (page of 64 slots, kv head):
+ *   scales [num_pages][kv_heads][2] FP32: K's, then V's; powers of two from
+ *          2^-120 to 2^119.
+ * A channel's value is code * scale.
+ *
+ * kv8_store - quantises K and V rows as they are written.  Row t of k and v goes
+ * to slot slots[t]; rows whose slot is negative or >= 64 * num_pages are
+ * skipped (padding).  Per (page, kv head, K or V) that the call writes to, with m
+ * the largest finite magnitude that it writes there: e = the least with m <= 448 *
+ * 2^e, clamped to -120 .. 119.
+ *   - A call that writes a page's first slot begins the page anew: its scale
+ *     becomes 2^e.  What its slots that the call does not write then hold is
+ *     unspecified.
+ *   - Any other call leaves a scale of 2^e or more as it is.  If it is less, it
+ *     becomes 2^e, and the codes of the page's other slots (of that head, K or V)
+ *     are rounded to it: nearest, ties to even.
+ * A row's codes are x / scale rounded to the nearest E4M3 value, ties to even,
+ * at most 448.  An infinity or a NaN becomes a NaN of its own channel alone.
+ * Scales of a cache that has not been written are 2^-120 (and codes 0), so that a
+ * page may be begun anywhere.
+ *   k, v, dtype, ld_k, ld_v, head_dim: as kv4_store.
+ * Device preconditions: the slots of one call are distinct, and those of one
+ * page lie within 64 consecutive rows (in any order, with other rows between), as
+ * pages_extend lists them; otherwise what the page holds is unspecified.  Tokens
+ * of a page come in order of their slots, but for its first slot in any.
+ *
+ * kv8_load - reads rows back: row i of k and v receives the values of slot
+ * slots[i] in `dtype` (exact in bf16 and fp32; rounded to fp16 where that
+ * type's range ends), zeros where the slot is negative or >= 64 * num_pages.
+ * Slots may repeat.
+ *
+ * Both return what kv4_store returns, for the same reasons.
+ */
+int kv8_store(const void* k, const void* v, int32_t dtype, int64_t ld_k, int64_t ld_v, const int32_t* slots,
+              int32_t num_tok, int32_t kv_heads, int32_t head_dim, uint8_t* codes, float* scales,
+              int64_t num_pages, void* stream);
+int kv8_load(const uint8_t* codes, const float* scales, int64_t num_pages, const int32_t* slots, int32_t num_slots,
+             int32_t kv_heads, int32_t head_dim, void* k, void* v, int32_t dtype, int64_t ld_k, int64_t ld_v,
+             void* stream);
+
+/*
+ * The 4-bit index keys: kcache's slots, in 68 bytes in place of 256.
+ *   codes  [num_pages * (64/c)][64] uint8: E2M1 codes, channel 2i in the low
+ *          nibble of byte i, 2i + 1 in the high one.
+ *   scales [num_pages * (64/c)][4] uint8: byte b of a group of 32 channels
+ *          stands for 2^(b - 127), 255 for NaN.
+ * Groups are quantised as kv4_store's: e = floor(log2(max |x|)) - 2, clamped to
+ * -120 .. 125; the nearest E2M1 value, ties to the even code, 6 for anything
+ * larger; NaN for a group that holds an infinity or a NaN.
+ *
+ * idx4_store - quantises keys as they are written: row t of keys (128 channels of
+ * `dtype`, ld elements from a row to the next, a multiple of 8, 16-byte aligned)
+ * goes to key slot slots[t]; rows whose slot is negative or >= cache_keys are
+ * skipped.  For c = 1 key slots are token slots.  Device precondition: the slots
+ * of one call are distinct.
+ *
+ * idx4_load - reads keys back: row i receives key slots[i] in `dtype` (exact in
+ * bf16 and fp32; rounded to fp16 where that type's range ends), zeros where the
+ * slot is negative or >= cache_keys.
+ *
+ * idx4_compress_store - idx_compress_store into the 4-bit keys (c = 4): the key,
+ * rounded to bf16 as that call stores it, is quantised.  Same arguments with codes
+ * and scales in place of kcache.
+ *
+ * idx4_score - idx_score_decode and idx_score_prefill over the 4-bit keys, any
+ * number of rows a request: the same arguments, layouts, outputs, preconditions
+ * and errors with codes and scales in place of kcache.  Each query head is
+ * quantised as a key is, by the call; with q4 and k4 the values that queries and
+ * keys then have,
+ *   scores[r*ld_scores + j] = (1/sqrt(128)) * sum_{h=0..3} max(0, <q4[r][h][:], k4_b[j][:]>)
+ * with sums in FP32.  Products with a group that is NaN count as 0.
+ *
+ * All return BS_OK (also when there are no rows), BS_ERR_NULL, BS_ERR_ARG (dtype,
+ * negative counts, cache_keys outside 1 .. 2^31 - 1, a stride below 128 or no
+ * multiple of 8, a pointer (idx4_score: q, codes, scales) that is not 16-byte
+ * aligned, and what idx_compress_store and idx_score_decode refuse) or
+ * BS_ERR_LAUNCH.
+ */
+int idx4_store(const void* keys, int32_t dtype, int64_t ld, const int32_t* slots, int32_t num_keys, uint8_t* codes,
+               uint8_t* scales, int64_t cache_keys, void* stream);
+int idx4_load(const uint8_t* codes, const uint8_t* scales, int64_t cache_keys, const int32_t* slots,
+              int32_t num_slots, void* keys, int32_t dtype, int64_t ld, void* stream);
+int idx4_compress_store(const uint16_t* k_raw, int32_t num_tok, const int32_t* req_tok_ptr,
+                        const int32_t* tok_start, const int32_t* mrope_pos, int32_t num_req, int32_t max_tok,
+                        int32_t rotary_dim, int32_t sec_t, int32_t sec_h, int32_t sec_w, double theta,
+                        uint16_t* ring, int32_t* ring_pos, const int32_t* page_table, int32_t pt_stride,
+                        uint8_t* codes, uint8_t* scales, int64_t num_pages, void* stream);
+int idx4_score(const uint16_t* q, const uint8_t* codes, const uint8_t* scales, int64_t num_pages,
+               const int32_t* page_table, int32_t pt_stride, const int32_t* req_row_ptr, int32_t num_req,
+               const int32_t* row_pos, int32_t num_rows, int32_t c, int32_t max_vis,
+               float* scores, int64_t ld_scores, int32_t* row_len, void* stream);
+
+/*
+ * The page tables of a batch, kept on the GPU.
+ *   kv_len     [num_req] int32: tokens that a request has (from 0).
+ *   held       [num_req] int32: pages that it has, its table's first entries.  At
+ *              least ceil(kv_len / 64); more after a kv_len was set back.
+ *   page_table [num_req][pt_stride] int32, written in place.
+ *   ring       [ring_size] int32: the ids of free pages, as a ring: `count` of
+ *              them from index `head` on, wrapping at ring_size.  ring_size is at
+ *              least the number of pages there are.
+ *   pool       [4] int32: head, count, pages that the last extend lacked, 0.
+ * kv_len_out, held_out and pool_out receive the state after the call and may be
+ * kv_len, held and pool themselves; pool_out[3] must be 0 before the call, and
+ * is 0 after it.
+ *
+ * pages_extend - appends new_len[b] tokens to request b (below 0 counts as 0; no
+ * more than its table holds, 64 * pt_stride in all, and in the order of the
+ * requests no more than num_rows in all).  Pages that a request lacks for its
+ * tokens are taken from the ring, requests in order.
+ *   req_row_ptr [num_req + 1], row_pos [num_rows]: as the other calls take
+ *               them, the new tokens being the rows.
+ *   slots       [num_rows]: each new token's slot, table entry * 64 + position
+ *               mod 64, for the calls that store.
+ * Rows behind the last new token get row_pos and slot -1 (a captured call is of a
+ * fixed num_rows).  When the ring has too few pages, the last requests' tokens
+ * have no page: slot -1 and their table entries as they were; held_out counts the
+ * pages there are, and pool_out[2] is how many are lacking.
+ *
+ * pages_release - cuts request b back to keep_len[b] tokens (0: all of it is
+ * given back; below 0 or more than kv_len: none) and puts the pages past
+ * ceil(keep / 64) at the ring's end, requests in order, their table entries
+ * becoming -1.
+ *
+ * Calls on the same state must not overlap in time.  Both return BS_OK,
+ * BS_ERR_NULL, BS_ERR_ARG (negative counts, pt_stride < 1, ring_size outside 1
+ * .. 2^25 - 1) or BS_ERR_LAUNCH.  With num_req 0 the rows are padding and the
+ * pool's state is passed on.
+ */
+int pages_extend(const int32_t* kv_len, const int32_t* held, const int32_t* new_len, int32_t num_req,
+                 int32_t* page_table, int32_t pt_stride, int32_t* ring, int32_t ring_size, const int32_t* pool,
+                 int32_t* kv_len_out, int32_t* held_out, int32_t* pool_out, int32_t* req_row_ptr, int32_t* row_pos,
+                 int32_t* slots, int32_t num_rows, void* stream);
+int pages_release(const int32_t* kv_len, const int32_t* held, const int32_t* keep_len, int32_t num_req,
+                  int32_t* page_table, int32_t pt_stride, int32_t* ring, int32_t ring_size, const int32_t* pool,
+                  int32_t* kv_len_out, int32_t* held_out, int32_t* pool_out, void* stream);
+
+/*
  * attn_slots - grouped-query attention of each query row over its own list of
  * KV slots [QSA: sparse GQA reads the selected entries of the K/V cache; MASK:
  * the only mask is slot >= 0], the slots as idx_select_translate emits them.
@@ -473,7 +620,7 @@ int kv4_load(const uint8_t* codes, const uint8_t* scales, int64_t num_pages, con
  * [0, 64 * num_pages):
  *   x_i = scale * <q[r][h], K[slot_i][g]>,
  *   out[r][h] = sum_i exp(x_i - lse) V[slot_i][g],  lse[r][h] = log sum_i exp(x_i).
- * Values of a 4-bit cache are converted to the queries' type: exact in bf16;
+ * Values of a 4-bit or 8-bit cache are converted to the queries' type: exact in bf16;
  * in fp16 rounded where that type's range ends.
  * A slot listed twice counts twice.  A row without a slot gives zeros and lse
  * -inf.  Scores, running maximum, sums and outputs are held in FP32 (2^8 times
