@@ -108,7 +108,7 @@ def lib():
         L.idx4_score.argtypes = [P, P, P, i64, P, i32, P, i32, P, i32, i32, i32, P, i64, P, P]
         L.idx4_score.restype = C.c_int
         pages_args = [P, P, P, i32, P, i32, P, i32, P, P, P, P]
-        L.pages_extend.argtypes = [*pages_args, P, P, P, i32, P]
+        L.pages_extend.argtypes = [*pages_args, P, P, P, P, i32, P]
         L.pages_extend.restype = C.c_int
         L.pages_release.argtypes = [*pages_args, P]
         L.pages_release.restype = C.c_int
@@ -713,25 +713,27 @@ def _pages_args(pool, kv_len, held, change, name, page_table, kv_len_out, held_o
             _ptr(outs[1], _I32, "held_out", dev), _ptr(outs[2].state, _I32, "state", dev))
 
 
-def _pages_extend_args(pool, kv_len, held, new_len, page_table, req_row_ptr, row_pos, slots, kv_len_out=None,
-                       held_out=None, pool_out=None):
+def _pages_extend_args(pool, kv_len, held, new_len, page_table, req_row_ptr, row_pos, slots, tok_start=None,
+                       kv_len_out=None, held_out=None, pool_out=None):
     """Checked argument tuple of a ``pages_extend`` call (all but the stream)."""
     a = _pages_args(pool, kv_len, held, new_len, "new_len", page_table, kv_len_out, held_out, pool_out)
     dev = pool.ring.device
     if req_row_ptr.numel() != kv_len.numel() + 1 or slots.numel() != row_pos.numel():
         raise ValueError("req_row_ptr must hold num_req + 1 entries, row_pos and slots num_rows each")
-    return (*a, _ptr(req_row_ptr, _I32, "req_row_ptr", dev), _ptr(row_pos, _I32, "row_pos", dev),
+    if tok_start is not None and tok_start.numel() != kv_len.numel():
+        raise ValueError("tok_start must hold num_req entries")
+    return (*a, _ptr(req_row_ptr, _I32, "req_row_ptr", dev), _ptr(tok_start, _I32, "tok_start", dev), _ptr(row_pos, _I32, "row_pos", dev),
             _ptr(slots, _I32, "slots", dev), _size(row_pos.numel()))
 
 
-def pages_extend(pool: PagePool, kv_len, held, new_len, page_table, req_row_ptr, row_pos, slots, kv_len_out=None,
-                 held_out=None, pool_out=None, stream=None):
+def pages_extend(pool: PagePool, kv_len, held, new_len, page_table, req_row_ptr, row_pos, slots, tok_start=None,
+                 kv_len_out=None, held_out=None, pool_out=None, stream=None):
     """Append new tokens to a batch: their pages, positions and slots.  The
     state is updated in place unless told otherwise (``pool_out``: a PagePool of
     the same ring).  See ``pages_extend`` in blockscore.h."""
     PreparedCall("pages_extend", _pages_extend_args(pool, kv_len, held, new_len, page_table, req_row_ptr, row_pos,
-                                                    slots, kv_len_out, held_out, pool_out), pool.ring.device,
-                 once=True)(stream)
+                                                    slots, tok_start, kv_len_out, held_out, pool_out),
+                 pool.ring.device, once=True)(stream)
 
 
 def _pages_release_args(pool, kv_len, held, keep_len, page_table, kv_len_out=None, held_out=None, pool_out=None):
@@ -985,11 +987,11 @@ def prepare_idx4_score(q, cache: Idx4Cache, page_table, req_row_ptr, row_pos, ma
 
 
 def prepare_pages_extend(pool: PagePool, kv_len, held, new_len, page_table, req_row_ptr, row_pos, slots,
-                         kv_len_out=None, held_out=None, pool_out=None) -> PreparedCall:
+                         tok_start=None, kv_len_out=None, held_out=None, pool_out=None) -> PreparedCall:
     """``pages_extend`` with fixed arguments."""
     return PreparedCall("pages_extend", _pages_extend_args(pool, kv_len, held, new_len, page_table, req_row_ptr,
-                                                           row_pos, slots, kv_len_out, held_out, pool_out),
-                        pool.ring.device)
+                                                           row_pos, slots, tok_start, kv_len_out, held_out,
+                                                           pool_out), pool.ring.device)
 
 
 def prepare_pages_release(pool: PagePool, kv_len, held, keep_len, page_table, kv_len_out=None, held_out=None,

@@ -413,14 +413,15 @@ BS_EXPORT int idx4_score(const uint16_t* q, const uint8_t* codes, const uint8_t*
 BS_EXPORT int pages_extend(const int32_t* kv_len, const int32_t* held, const int32_t* new_len, int32_t num_req,
                            int32_t* page_table, int32_t pt_stride, int32_t* ring, int32_t ring_size,
                            const int32_t* pool, int32_t* kv_len_out, int32_t* held_out, int32_t* pool_out,
-                           int32_t* req_row_ptr, int32_t* row_pos, int32_t* slots, int32_t num_rows, void* stream) {
+                           int32_t* req_row_ptr, int32_t* tok_start, int32_t* row_pos, int32_t* slots,
+                           int32_t num_rows, void* stream) {
   const int st = check_pages_args(kv_len, held, new_len, num_req, page_table, pt_stride, ring, ring_size, pool,
                                   kv_len_out, held_out, pool_out);
   if (st != BS_OK) return st;
   if (num_rows < 0) return BS_ERR_ARG;
   if (!req_row_ptr || (num_rows > 0 && (!row_pos || !slots))) return BS_ERR_NULL;
   return bs::launch_pages({kv_len, held, new_len, num_req, page_table, pt_stride, ring, ring_size, pool, kv_len_out,
-                           held_out, pool_out, req_row_ptr, row_pos, slots, num_rows},
+                           held_out, pool_out, req_row_ptr, tok_start, row_pos, slots, num_rows},
                           false, static_cast<hipStream_t>(stream));
 }
 
@@ -432,7 +433,7 @@ BS_EXPORT int pages_release(const int32_t* kv_len, const int32_t* held, const in
                                   kv_len_out, held_out, pool_out);
   if (st != BS_OK) return st;
   return bs::launch_pages({kv_len, held, keep_len, num_req, page_table, pt_stride, ring, ring_size, pool, kv_len_out,
-                           held_out, pool_out, nullptr, nullptr, nullptr, 0},
+                           held_out, pool_out, nullptr, nullptr, nullptr, nullptr, 0},
                           true, static_cast<hipStream_t>(stream));
 }
 

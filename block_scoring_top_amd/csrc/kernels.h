@@ -88,7 +88,7 @@ struct PagesCall {
   int32_t ring_size;
   const int32_t* pool;
   int32_t *kv_len_out, *held_out, *pool_out;
-  int32_t *req_row_ptr, *row_pos, *slots;  // extend
+  int32_t *req_row_ptr, *tok_start, *row_pos, *slots;  // extend; tok_start may be null
   int32_t num_rows;
 };
 int launch_pages(const PagesCall& a, bool release, hipStream_t stream);

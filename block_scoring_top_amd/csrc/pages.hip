@@ -99,6 +99,7 @@ __global__ __launch_bounds__(kThreads) void pages_kernel(const PagesCall a) {
       sh.len[i] = min((uint32_t)max(a.kv_len[b0 + i], 0), cap);
       sh.held[i] = min(max(a.held[b0 + i], 0), a.pt_stride);
       sh.change[i] = a.change[b0 + i];
+      if (!RELEASE && blockIdx.x == 0 && a.tok_start != nullptr) a.tok_start[b0 + i] = sh.len[i];
     }
     __syncthreads();
     const uint32_t head = sh.head, count = sh.count;

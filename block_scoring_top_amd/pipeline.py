@@ -1,5 +1,6 @@
 """The whole hot path on one GPU: score -> top-k -> expand/translate, and the
-attention that reads the chosen slots.
+attention that reads the chosen slots; and the state of a batch that they work
+on, its page tables among it.
 
 Allocates the output and workspace tensors once (torch, device memory) and
 then enqueues the three C-ABI calls on the current stream.  No host
@@ -10,9 +11,42 @@ from __future__ import annotations
 import torch
 
 from . import (ATTN_WORKSPACE_BYTES, attn_slots, attn_workspace, idx_expand_translate, idx_score_decode,
-               idx_score_prefill, idx_select_translate, idx_select_translate_planned, prepare_score,
-               prepare_select_translate, topk_plan, topk_plan_rows, topk_planned_workspace, topk_select_rows,
-               topk_workspace)
+               idx4_score, idx_score_prefill, idx_select_translate, idx_select_translate_planned, PagePool, pages_extend,
+               pages_release, prepare_idx4_score, prepare_score, prepare_select_translate, topk_plan, topk_plan_rows,
+               topk_planned_workspace, topk_select_rows, topk_workspace)
+
+
+class PagedBatch:
+    """Requests whose tokens live in the pages of one pool: the tables and
+    lengths, kept on the GPU, and the rows of the step in hand.
+
+    Row b of ``page_table`` (and ``kv_len``, ``held``) is request b.  After
+    ``extend``, ``req_row_ptr`` and ``row_pos`` are what the scorers, the
+    selection and ``attn_window`` take, and ``slots`` what ``kv4_store``,
+    ``kv8_store`` and ``idx4_store`` (c = 1) take; ``tok_start`` and
+    ``req_row_ptr`` are what the key compression takes.  Nothing here waits for the
+    GPU; calls on one batch belong on one stream."""
+
+    def __init__(self, num_req: int, max_tokens: int, num_pages: int, num_rows: int, device):
+        n = dict(dtype=torch.int32, device=device)
+        self.pool = PagePool.full(num_pages, device)
+        self.page_table = torch.full((num_req, max(1, -(-max_tokens // 64))), -1, **n)
+        self.kv_len = torch.zeros(num_req, **n)
+        self.held = torch.zeros(num_req, **n)
+        self.tok_start = torch.zeros(num_req, **n)
+        self.req_row_ptr = torch.zeros(num_req + 1, **n)
+        self.row_pos = torch.full((num_rows,), -1, **n)
+        self.slots = torch.full((num_rows,), -1, **n)
+
+    def extend(self, new_len, stream=None):
+        """Appends ``new_len`` [num_req] tokens: rows, positions, slots, pages."""
+        pages_extend(self.pool, self.kv_len, self.held, new_len, self.page_table, self.req_row_ptr, self.row_pos,
+                     self.slots, tok_start=self.tok_start, stream=stream)
+
+    def release(self, keep_len, stream=None):
+        """Cuts requests back to ``keep_len`` [num_req] tokens (0: finished;
+        below 0: left alone)."""
+        pages_release(self.pool, self.kv_len, self.held, keep_len, self.page_table, stream=stream)
 
 
 class IndexerPath:
@@ -20,12 +54,15 @@ class IndexerPath:
 
     ``inp`` is any object with the device-input fields (c, k, q, kcache,
     num_pages, page_table, req_row_ptr, row_pos, max_vis), e.g.
-    ``synth.device.DeviceInputs``.  ``scorer`` is "decode" or "prefill".
+    ``synth.device.DeviceInputs``.  ``scorer`` is "decode" or "prefill", or
+    "idx4" for 4-bit keys: ``kcache`` is then an ``Idx4Cache``.
     """
 
     def __init__(self, inp, scorer: str = "decode"):
-        if scorer not in ("decode", "prefill"):
-            raise ValueError("scorer must be 'decode' or 'prefill'")
+        if scorer not in ("decode", "prefill", "idx4"):
+            raise ValueError("scorer must be 'decode', 'prefill' or 'idx4'")
+        if scorer == "idx4" and inp.kcache.c != inp.c:
+            raise ValueError("the 4-bit keys are of another c")
         self.inp = inp
         self.scorer = scorer
         dev = inp.q.device
@@ -52,6 +89,8 @@ class IndexerPath:
         i = self.inp
         fn = "idx_score_decode" if self.scorer == "decode" else "idx_score_prefill"
         self._prepared = (
+            prepare_idx4_score(i.q, i.kcache, i.page_table, i.req_row_ptr, i.row_pos, i.max_vis, self.scores,
+                               self.row_len) if self.scorer == "idx4" else
             prepare_score(fn, i.q, i.kcache, i.num_pages, i.page_table, i.req_row_ptr, i.row_pos, i.c, i.max_vis,
                           self.scores, self.row_len),
             prepare_select_translate(self.scores, self.row_len, int(i.max_vis), i.k, i.req_row_ptr, i.row_pos,
@@ -60,6 +99,10 @@ class IndexerPath:
 
     def score(self, stream=None):
         i = self.inp
+        if self.scorer == "idx4":
+            idx4_score(i.q, i.kcache, i.page_table, i.req_row_ptr, i.row_pos, i.max_vis, self.scores, self.row_len,
+                       stream=stream)
+            return
         fn = idx_score_decode if self.scorer == "decode" else idx_score_prefill
         fn(i.q, i.kcache, i.num_pages, i.page_table, i.req_row_ptr, i.row_pos, i.c, i.max_vis,
            self.scores, self.row_len, stream=stream)
@@ -133,7 +176,7 @@ class IndexerPath:
     def attend(self, q, cache, out, scale=None, lse=None, stream=None):
         """Attention of the main query heads ``q`` [num_rows, q_heads,
         head_dim] over the slots of the last ``run``, read from ``cache``
-        (``KV4Cache`` or ``KV16Cache``) into ``out``.
+        (``KV4Cache``, ``KV8Cache`` or ``KV16Cache``) into ``out``.
 
         Calls on different streams may overlap: each stream has a workspace of
         its own (32 MiB, kept with the path), and so has each captured call.

@@ -585,6 +585,8 @@ int idx4_score(const uint16_t* q, const uint8_t* codes, const uint8_t* scales, i
  * tokens are taken from the ring, requests in order.
  *   req_row_ptr [num_req + 1], row_pos [num_rows]: as the other calls take
  *               them, the new tokens being the rows.
+ *   tok_start   [num_req] or NULL: kv_len before the call, the position of each
+ *               request's first new token (idx_compress_store).
  *   slots       [num_rows]: each new token's slot, table entry * 64 + position
  *               mod 64, for the calls that store.
  * Rows behind the last new token get row_pos and slot -1 (a captured call is of a
@@ -592,9 +594,9 @@ int idx4_score(const uint16_t* q, const uint8_t* codes, const uint8_t* scales, i
  * have no page: slot -1 and their table entries as they were; held_out counts the
  * pages there are, and pool_out[2] is how many are lacking.
  *
- * pages_release - cuts request b back to keep_len[b] tokens (0: all of it is
- * given back; below 0 or more than kv_len: none) and puts the pages past
- * ceil(keep / 64) at the ring's end, requests in order, their table entries
+ * pages_release - cuts request b back to keep_len[b] tokens (0: it is finished;
+ * below 0 or more than kv_len: no token goes) and puts its pages past
+ * ceil(tokens / 64) at the ring's end, requests in order, their table entries
  * becoming -1.
  *
  * Calls on the same state must not overlap in time.  Both return BS_OK,
@@ -604,8 +606,8 @@ int idx4_score(const uint16_t* q, const uint8_t* codes, const uint8_t* scales, i
  */
 int pages_extend(const int32_t* kv_len, const int32_t* held, const int32_t* new_len, int32_t num_req,
                  int32_t* page_table, int32_t pt_stride, int32_t* ring, int32_t ring_size, const int32_t* pool,
-                 int32_t* kv_len_out, int32_t* held_out, int32_t* pool_out, int32_t* req_row_ptr, int32_t* row_pos,
-                 int32_t* slots, int32_t num_rows, void* stream);
+                 int32_t* kv_len_out, int32_t* held_out, int32_t* pool_out, int32_t* req_row_ptr, int32_t* tok_start,
+                 int32_t* row_pos, int32_t* slots, int32_t num_rows, void* stream);
 int pages_release(const int32_t* kv_len, const int32_t* held, const int32_t* keep_len, int32_t num_req,
                   int32_t* page_table, int32_t pt_stride, int32_t* ring, int32_t ring_size, const int32_t* pool,
                   int32_t* kv_len_out, int32_t* held_out, int32_t* pool_out, void* stream);
