@@ -11,6 +11,7 @@
 // writes its share of the rows and pages; the lengths, which a caller may have
 // updated in place, are written by the last workgroup to have read them.
 #include <algorithm>
+#include <type_traits>
 
 #include "device.h"
 #include "kernels.h"
@@ -19,8 +20,6 @@ namespace bs {
 
 namespace {
 
-constexpr int kThreads = 1024, kPgWaves = kThreads / 64;
-constexpr int kBatch = 4096;             // requests held in LDS at a time
 constexpr uint32_t kMost = 0x7FFFFFFFu;  // sums saturate here
 
 __device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) { return min(a + b, kMost); }  // of two at most kMost
@@ -37,22 +36,24 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
   return x;
 }
 
+template <int THREADS, int BATCH>
 struct Shared {
-  int32_t len[kBatch], held[kBatch], change[kBatch];
-  uint32_t row_end[kThreads], page_end[kThreads];  // of the chunk's requests
-  uint32_t sums[2][kPgWaves];
+  int32_t len[BATCH], held[BATCH], change[BATCH];
+  uint32_t row_end[THREADS], page_end[THREADS];  // of the chunk's requests
+  uint32_t sums[2][THREADS / 64];
   uint32_t head, count, arrived;
 };
 
 // The same over the workgroup, on top of `carry`; `carry` becomes the total.
-__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t (&sums)[kPgWaves], uint32_t& carry) {
+template <int WAVES>
+__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t (&sums)[WAVES], uint32_t& carry) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   x = wave_scan(x);
   if (lane == 63) sums[wave] = x;
   __syncthreads();
   uint32_t before = carry;
 #pragma unroll
-  for (int w = 0; w < kPgWaves; ++w) {
+  for (int w = 0; w < WAVES; ++w) {
     const uint32_t s = sums[w];
     before = w < wave ? sat_add(before, s) : before;
     carry = sat_add(carry, s);
@@ -80,11 +81,12 @@ __device__ __forceinline__ uint32_t ring_at(uint32_t head, uint32_t i, uint32_t 
 
 }  // namespace
 
-template <bool RELEASE>
-__global__ __launch_bounds__(kThreads) void pages_kernel(const PagesCall a) {
-  __shared__ Shared sh;
+// BATCH requests in LDS at a time, of which THREADS are scanned together.
+template <bool RELEASE, int THREADS, int BATCH>
+__global__ __launch_bounds__(THREADS) void pages_kernel(const PagesCall a) {
+  __shared__ Shared<THREADS, BATCH> sh;
   const int tid = threadIdx.x;
-  const uint32_t share = gridDim.x * kThreads, mine = blockIdx.x * kThreads + tid;
+  const uint32_t share = gridDim.x * THREADS, mine = blockIdx.x * THREADS + tid;
   const uint32_t size = a.ring_size, cap = (uint32_t)min((int64_t)a.pt_stride * kPage, (int64_t)kMost);
   if (tid == 0) {
     sh.head = min(max(a.pool[0], 0), a.ring_size - 1);
@@ -93,9 +95,9 @@ __global__ __launch_bounds__(kThreads) void pages_kernel(const PagesCall a) {
   }
   uint32_t rows = 0, pages = 0;  // of the requests so far
   bool last = gridDim.x == 1;
-  for (int b0 = 0; b0 < a.num_req; b0 += kBatch) {  // one turn, unless one workgroup does everything
-    const int nb = min(kBatch, a.num_req - b0);
-    for (int i = tid; i < nb; i += kThreads) {
+  for (int b0 = 0; b0 < a.num_req; b0 += BATCH) {  // one turn, unless one workgroup does everything
+    const int nb = min(BATCH, a.num_req - b0);
+    for (int i = tid; i < nb; i += THREADS) {
       sh.len[i] = min((uint32_t)max(a.kv_len[b0 + i], 0), cap);
       sh.held[i] = min(max(a.held[b0 + i], 0), a.pt_stride);
       sh.change[i] = a.change[b0 + i];
@@ -106,8 +108,8 @@ __global__ __launch_bounds__(kThreads) void pages_kernel(const PagesCall a) {
     if (gridDim.x > 1 && tid == 0)
       sh.arrived = __hip_atomic_fetch_add(reinterpret_cast<uint32_t*>(a.pool_out + 3), 1u, __ATOMIC_RELAXED,
                                           __HIP_MEMORY_SCOPE_AGENT);
-    for (int c0 = 0; c0 < nb; c0 += kThreads) {
-      const int nc = min(kThreads, nb - c0), i = c0 + tid;
+    for (int c0 = 0; c0 < nb; c0 += THREADS) {
+      const int nc = min(THREADS, nb - c0), i = c0 + tid;
       const bool there = tid < nc;
       const uint32_t len = there ? sh.len[i] : 0, held = there ? sh.held[i] : 0;
       const int change = there ? sh.change[i] : 0;
@@ -176,7 +178,7 @@ __global__ __launch_bounds__(kThreads) void pages_kernel(const PagesCall a) {
     __syncthreads();
     if (gridDim.x > 1) last = sh.arrived == gridDim.x - 1;
     if (last)
-      for (int i = tid; i < nb; i += kThreads) a.kv_len_out[b0 + i] = sh.len[i], a.held_out[b0 + i] = sh.held[i];
+      for (int i = tid; i < nb; i += THREADS) a.kv_len_out[b0 + i] = sh.len[i], a.held_out[b0 + i] = sh.held[i];
     __syncthreads();
   }
   if constexpr (!RELEASE)
@@ -195,17 +197,30 @@ __global__ __launch_bounds__(kThreads) void pages_kernel(const PagesCall a) {
   }
 }
 
-// A workgroup takes up to kItems rows (extend) or page table entries (release:
-// few of them are given back) before there is a second one.
+// There is a workgroup for every kItems rows (extend) or 16 times as many page
+// table entries (release: few of them are given back).  us, both calls of 1,003
+// requests with 56,000 new tokens, kItems 512 / 1,024 / 2,048: 12.2 / 11.0 / 12.7.
+// Up to 256 requests: workgroups of 256, whose barriers and scans are shorter
+// (64 requests x 6 rows: 7.7 us, 8.9 with 1,024; the host takes about as long).
 int launch_pages(const PagesCall& a, bool release, hipStream_t stream) {
-  constexpr int64_t kItems = 4096;
-  const int64_t items = release ? (int64_t)a.num_req * a.pt_stride / 16 : a.num_rows;
-  const bool once = a.num_req > 0 && a.num_req <= kBatch;  // else one workgroup does everything, in turns
-  const uint32_t grid = once ? (uint32_t)std::min<int64_t>(64, std::max<int64_t>(1, items / kItems)) : 1;
+  constexpr int64_t kItems = 1024;
+  auto go = [&](auto rel, auto threads, auto batch) {
+    constexpr int THREADS = decltype(threads)::value, BATCH = decltype(batch)::value;
+    const int64_t items = release ? (int64_t)a.num_req * a.pt_stride / 16 : a.num_rows;
+    const bool once = a.num_req > 0 && a.num_req <= BATCH;  // else one workgroup does everything, in turns
+    const uint32_t grid = once ? (uint32_t)std::min<int64_t>(128, std::max<int64_t>(1, items / kItems)) : 1;
+    hipLaunchKernelGGL((pages_kernel<decltype(rel)::value, THREADS, BATCH>), dim3(grid), dim3(THREADS), 0, stream, a);
+  };
+  auto by_size = [&](auto rel) {
+    if (a.num_req <= 256)
+      go(rel, std::integral_constant<int, 256>(), std::integral_constant<int, 256>());
+    else
+      go(rel, std::integral_constant<int, 1024>(), std::integral_constant<int, 4096>());
+  };
   if (release)
-    hipLaunchKernelGGL(pages_kernel<true>, dim3(grid), dim3(kThreads), 0, stream, a);
+    by_size(std::true_type());
   else
-    hipLaunchKernelGGL(pages_kernel<false>, dim3(grid), dim3(kThreads), 0, stream, a);
+    by_size(std::false_type());
   return hipGetLastError() == hipSuccess ? BS_OK : BS_ERR_LAUNCH;
 }
 
