@@ -66,13 +66,18 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t x) {
 }  // namespace
 
 // S: rows of the call whose runs (rows of one page) a workgroup takes if they
-// begin there, one run after the other.
+// begin there, one run after the other: S rows a group, `groups` from group0 on.
+//
+// In a prompt's rows every fourth group of 16 begins a run.  Consecutive
+// workgroups go to the 8 XCDs in turn, so groups 4 apart are neighbours in the
+// grid: with the groups in order, two XCDs did all the work (8,192 rows x 8
+// heads of 128: 31.5 us).
 template <class T, int D, int S>
 __global__ __launch_bounds__(2 * D) void kv8_store_kernel(const typename T::elem* __restrict__ k,
                                                           const typename T::elem* __restrict__ v, int64_t ld_k,
                                                           int64_t ld_v, const int32_t* __restrict__ slots,
                                                           int32_t num_tok, int32_t hkv, int32_t num_slots,
-                                                          uint8_t* codes, float* scales, uint32_t block0) {
+                                                          uint8_t* codes, float* scales, uint32_t group0, uint32_t groups) {
   constexpr int LANES = D / 8, ROWS = D / LANES, PASSES = kPage / ROWS;  // of a row; rows at a time
   static_assert(ROWS == 8 && PASSES == 8, "D lanes for K, D for V");
   constexpr int HALF_WAVES = D / 64;  // waves that work on K (V)
@@ -82,11 +87,17 @@ __global__ __launch_bounds__(2 * D) void kv8_store_kernel(const typename T::elem
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = blockIdx.y, which = wave / HALF_WAVES;
   const int r0 = tid % D / LANES, j = tid % LANES;
-  const int64_t first = ((int64_t)blockIdx.x + block0) * S;
-  const typename T::elem* src = which ? v : k;
+  uint32_t group = blockIdx.x;
+  if constexpr (S == 16) {
+    const uint32_t quarter = (groups + 3) / 4;
+    group = group % quarter * 4 + group / quarter;
+    if (group >= groups) return;
+  }
+  const int64_t first = ((int64_t)group0 + group) * S;
+  const typename T::elem* src = (which ? v : k) + h * D + j * 8;
   const int64_t ld = which ? ld_v : ld_k;
 
-  // The slots around: page numbers would do, but padding must not match.
+  // The slots around; -1 for those that are none.
   for (int i = tid; i < kSpan - 1 + S + kSpan - 1; i += 2 * D) {
     const int64_t t = first - (kSpan - 1) + i;
     const int32_t s = t >= 0 && t < num_tok ? slots[t] : -1;
@@ -119,80 +130,98 @@ __global__ __launch_bounds__(2 * D) void kv8_store_kernel(const typename T::elem
     const int s = sl[at + lane];
     const bool mine = s >= 0 && s >> 6 == page;
     const uint64_t mask = ballot(mine);
-    // A row may name a slot twice; more rows than the page has slots cannot be.
-    const int n = __popcll(mask);
+    const int n = __popcll(mask), passes = (n + ROWS - 1) / ROWS;
     const bool anew = ballot(mine && (s & 63) == 0) != 0;
-    const uint64_t written = wave_or64(mine ? 1ull << ((s & 63)) : 0);
     if (wave == 0 && mine) {
       const int m = lanes_below(mask);
-      mate_row[m] = at - (kSpan - 1) + lane, mate_slot[m] = s;
+      mate_row[m] = at - (kSpan - 1) + lane, mate_slot[m] = s & 63;
     }
     float* const scale_at = scales + ((int64_t)page * hkv + h) * 2 + which;
     const float was = *scale_at;
     __syncthreads();
 
-    Chunk<T> x[PASSES];
-    uint32_t top = 0;
+    auto run = [&](auto passes_c) {
+      constexpr int P = decltype(passes_c)::value;
+      // Lanes past the last row take it again.
+      Chunk<T> x[P];
+      uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-      const int m = i * ROWS + r0;
-      if (m < n) x[i].load(src + (first + mate_row[m]) * ld + h * D + j * 8);
-    }
+      for (int i = 0; i < P; ++i)
+        if (i < passes) x[i].load(src + (first + mate_row[min(i * ROWS + r0, n - 1)]) * ld);
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-      if (i * ROWS + r0 < n) {
-        const Values<T> y(x[i]);
+      for (int i = 0; i < P; ++i)
+        if (i < passes) top = max(top, x[i].top());
+      // Infinities and NaN are left out of the maximum, in a second look if there are any.
+      bool careful = false;
+      if (ballot(top >= 0x7F800000u)) {
+        careful = true, top = 0;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint32_t u = __float_as_uint(y.v[c]) & 0x7FFFFFFFu;
-          top = max(top, u < 0x7F800000u ? u : 0u);
+        for (int i = 0; i < P; ++i) {
+          if (i >= passes) continue;
+          const Values<T> y(x[i]);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const uint32_t u = __float_as_uint(y.v[c]) & 0x7FFFFFFFu;
+            top = max(top, u < 0x7F800000u ? u : 0u);
+          }
         }
       }
-    }
-    top = wave_max_u32(top);
-    if (lane == 0) tops[which][wave % HALF_WAVES] = top;
-    __syncthreads();
+      top = wave_max_u32(top);
+      if (lane == 0) tops[which][wave % HALF_WAVES] = top;
+      __syncthreads();
 #pragma unroll
-    for (int w = 0; w < HALF_WAVES; ++w) top = max(top, tops[which][w]);
-    int e = kv8_exponent(top);
-    const int old = min(max((int)(__float_as_uint(was) >> 23), kExpMin8), kExpMax8);
-    const bool raised = !anew && e > old;
-    if (!anew) e = max(e, old);
-    const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
+      for (int w = 0; w < HALF_WAVES; ++w) top = max(top, tops[which][w]);
+      int e = kv8_exponent(top);
+      const int old = min(max((int)(__float_as_uint(was) >> 23), kExpMin8), kExpMax8);
+      const bool raised = !anew && e > old;
+      if (!anew) e = max(e, old);
+      const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
+      careful = careful || e == kExpMax8;  // values past 448 scales
 
-    uint8_t* const page_codes = codes + (((int64_t)page * kPage * hkv + h) * 2 + which) * D + j * 8;
-    const int64_t step = (int64_t)hkv * 2 * D;
+      uint8_t* const page_codes = codes + (((int64_t)page * kPage * hkv + h) * 2 + which) * D + j * 8;
+      const int64_t step = (int64_t)hkv * 2 * D;
+      auto write = [&](auto careful_c) {
+        constexpr bool CAREFUL = decltype(careful_c)::value;
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-      const int m = i * ROWS + r0;
-      if (m < n) {
-        const Values<T> y(x[i]);
-        u32x2_t c;
-        c.x = kv8_codes<true>(kv8_codes<false>(0u, y.v[0] * inv, y.v[1] * inv), y.v[2] * inv, y.v[3] * inv);
-        c.y = kv8_codes<true>(kv8_codes<false>(0u, y.v[4] * inv, y.v[5] * inv), y.v[6] * inv, y.v[7] * inv);
-        *reinterpret_cast<u32x2_t*>(page_codes + (mate_slot[m] & 63) * step) = c;
-      }
-    }
-    if (raised) {
-      const float f = __uint_as_float((uint32_t)(127 + old - e > 0 ? 127 + old - e : 0) << 23);  // 2^-127 and less: 0
+        for (int i = 0; i < P; ++i) {
+          const int m = i * ROWS + r0;
+          if (i >= passes) continue;
+          const Values<T> y(x[i]);
+          u32x2_t c;
+          c.x = kv8_codes<true, CAREFUL>(kv8_codes<false, CAREFUL>(0u, y.v[0] * inv, y.v[1] * inv), y.v[2] * inv, y.v[3] * inv);
+          c.y = kv8_codes<true, CAREFUL>(kv8_codes<false, CAREFUL>(0u, y.v[4] * inv, y.v[5] * inv), y.v[6] * inv, y.v[7] * inv);
+          if (m < n) *reinterpret_cast<u32x2_t*>(page_codes + mate_slot[m] * step) = c;
+        }
+      };
+      if (careful)
+        write(std::true_type());
+      else
+        write(std::false_type());
+      if (raised) {
+        const uint64_t written = wave_or64(mine ? 1ull << (s & 63) : 0);
+        const float f = __uint_as_float((uint32_t)max(127 + old - e, 0) << 23);  // 2^-127 and less: 0
+        u32x2_t c[PASSES];
 #pragma unroll
-      for (int i = 0; i < PASSES; ++i) {
-        const int m = i * ROWS + r0;
-        if ((written >> m & 1) == 0) {
-          u32x2_t* p = reinterpret_cast<u32x2_t*>(page_codes + m * step);
-          u32x2_t c = *p;
+        for (int i = 0; i < PASSES; ++i) c[i] = *reinterpret_cast<u32x2_t*>(page_codes + (i * ROWS + r0) * step);
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) {
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
-            const f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[w], false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[w], true);
-            c[w] = kv8_codes<true>(kv8_codes<false>(0u, a.x * f, a.y * f), b.x * f, b.y * f);
+            const f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[i][w], false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[i][w], true);
+            c[i][w] = kv8_codes<true, true>(kv8_codes<false, true>(0u, a.x * f, a.y * f), b.x * f, b.y * f);
           }
-          *p = c;
+          const int m = i * ROWS + r0;
+          if ((written >> m & 1) == 0) *reinterpret_cast<u32x2_t*>(page_codes + m * step) = c[i];
         }
       }
-    }
-    if (anew || raised) {
-      if (tid % D == 0) *scale_at = __uint_as_float((uint32_t)e << 23);
-    }
+      if ((anew || raised) && tid % D == 0) *scale_at = __uint_as_float((uint32_t)e << 23);
+    };
+    // Few rows (decode, verify) by code of their own: what runs once a workgroup
+    // is fetched as it runs.
+    if (passes == 1)
+      run(std::integral_constant<int, 1>());
+    else
+      run(std::integral_constant<int, PASSES>());
     __syncthreads();  // the lists are free again
   }
 }
@@ -260,11 +289,12 @@ int launch_kv8_store(const void* k, const void* v, int32_t dtype, int64_t ld_k, 
     constexpr int D = decltype(dim)::value;
     auto go = [&](auto rows) {
       constexpr int S = decltype(rows)::value;
-      const int64_t blocks = ((int64_t)num_tok + S - 1) / S, most = ((int64_t)1 << 31) / (2 * D);  // of a launch
-      for (int64_t b = 0; b < blocks; b += most) {
-        hipLaunchKernelGGL((kv8_store_kernel<T, D, S>), dim3((uint32_t)std::min(most, blocks - b), hkv), dim3(2 * D), 0,
-                           stream, static_cast<const elem*>(k), static_cast<const elem*>(v), ld_k, ld_v, slots, num_tok,
-                           hkv, num_slots, codes, scales, (uint32_t)b);
+      const int64_t groups = ((int64_t)num_tok + S - 1) / S, most = ((int64_t)1 << 31) / (2 * D);  // of a launch
+      for (int64_t g = 0; g < groups; g += most) {
+        const uint32_t n = (uint32_t)std::min(most, groups - g);
+        hipLaunchKernelGGL((kv8_store_kernel<T, D, S>), dim3(S == 16 ? (n + 3) / 4 * 4 : n, hkv), dim3(2 * D), 0, stream,
+                           static_cast<const elem*>(k), static_cast<const elem*>(v), ld_k, ld_v, slots, num_tok, hkv,
+                           num_slots, codes, scales, (uint32_t)g, n);
         if (hipGetLastError() != hipSuccess) return (int)BS_ERR_LAUNCH;
       }
       return (int)BS_OK;
