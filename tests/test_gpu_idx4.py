@@ -151,7 +151,8 @@ SCORE_CASES = [  # c, contexts, rows
     (1, [1], [1]), (4, [3], [1]), (4, [4], [1]), (1, [64, 65, 130], [1, 1, 1]), (4, [8194], [1]), (4, [700, 64, 3, 260], [4, 1, 3, 2]),
     (1, [500, 70], [4, 3]), (4, [1500, 40, 900], [6, 5, 6]), (1, [333, 90], [8, 6]), (4, [2000, 300], [9, 9]),
     (1, [600], [17]), (4, [3000], [130]), (1, [700, 200, 20], [129, 64, 1]), (4, [9000, 500], [300, 33]), (1, [1100], [1000]),
-    (4, [400] * 20, [0, 1] * 10), (1, [5000] * 64, [1] * 64), (4, [70000] * 16, [2] * 16), (4, [33000] * 32, [6] * 32)]
+    (4, [400] * 20, [0, 1] * 10), (4, [900] * 70, [1] * 63 + [700, 0, 40] + [1] * 4), (1, [300] * 130, [40] * 130),
+    (1, [2100, 90], [30, 2]), (4, [1300] * 9, [0, 0, 33, 0, 64, 1, 31, 32, 90]), (1, [5000] * 64, [1] * 64), (4, [70000] * 16, [2] * 16), (4, [33000] * 32, [6] * 32)]
 
 
 @pytest.mark.parametrize("c,ctx,rows", SCORE_CASES)
