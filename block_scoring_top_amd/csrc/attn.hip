@@ -40,11 +40,19 @@ constexpr int64_t kPartialBytes = (int64_t)BS_ATTN_WORKSPACE_BYTES - kCounterByt
 //     registers allow.  16 query / 2 kv heads, window 4,000: 8,192 rows from position 0
 //     820 and 925, at the end of a 64K context 1,026 and 1,015 (window 500: 207 and
 //     186); 64 x 6 rows 78 and 271.
+// The 8-bit cache: 16 query / 2 kv heads, gathered and not, D = 128: 100 rows, window
+// 1,200 (60,000 tiles times keys) 16 and 19 us, 300, 1,000 (150,000) 21 and 22, 700,
+// 1,000 (350,000) 41 and 27; 36 x 6 rows, window 700 18 and 22, 64 x 6, window 4,000
+// 65 and 60.  D = 64: 1,000 rows, window 1,000 (500,000) 18 and 24.  D = 256, where
+// its codes take the other's registers only for a page at a time: 100 rows, window
+// 1,000 (100,000) 23 and 37, 300, 2,000 (600,000) 74 and 54, 2,000 rows 292 and 159; 64 x
+// 6 rows, window 4,000 140 and 324.
 bool gathers(const AttnCall& c, int64_t tiles, int64_t keys, int64_t pairs, int64_t num_req) {
-  const bool kv4 = c.form != BS_KV_16;
+  const bool kv4 = c.form == BS_KV_4, kv8 = c.form == BS_KV_8;
   if (pairs <= 16 || (kv4 && c.d == 256)) return true;
-  const double most = kv4 ? (c.d == 64 ? 550e3 : 700e3) : c.d == 64 ? 500e3 : c.d == 128 ? 60e3 : 80e3;
-  const int64_t ratio = kv4 || c.d == 64 ? 2 : 0;
+  const double most = kv8 ? (c.d == 64 ? 550e3 : c.d == 128 ? 150e3 : 350e3)
+                      : kv4 ? (c.d == 64 ? 550e3 : 700e3) : c.d == 64 ? 500e3 : c.d == 128 ? 60e3 : 80e3;
+  const int64_t ratio = kv8 ? (c.d == 64 ? 2 : c.d == 128 ? 1 : 4) : kv4 || c.d == 64 ? 2 : 0;
   return (double)tiles * keys <= most || tiles <= ratio * num_req * c.hkv * ((pairs + 127) / 128);
 }
 // Keys are split over up to kFillBlocks workgroups in all.  us, 512 / 768 / 1,024:

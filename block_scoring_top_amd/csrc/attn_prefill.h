@@ -540,7 +540,7 @@ int launch_attn_prefill(const PrefillArgs& a, int d, int waves, uint32_t grid, h
     by_waves(std::integral_constant<int, 64>());
   else if (d == 128)
     by_waves(std::integral_constant<int, 128>());
-  else if constexpr (FORM == kForm16)  // the registers hold one wave a SIMD; codes are gathered at this size
+  else if constexpr (FORM != kForm4)  // the registers hold one wave a SIMD; the 4-bit cache is gathered at this size
     go(std::integral_constant<int, 256>(), std::integral_constant<int, 4>());
   return hipGetLastError() == hipSuccess ? BS_OK : BS_ERR_LAUNCH;
 }
