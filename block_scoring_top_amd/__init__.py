@@ -648,7 +648,7 @@ def idx4_load(cache: Idx4Cache, slots, keys, stream=None):
 def _idx4_compress_args(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary_dim, sections, theta, ring, ring_pos,
                         page_table, cache):
     """Checked argument tuple of an ``idx4_compress_store`` call (all but the stream)."""
-    dev = _idx4_cache(cache)
+    _idx4_cache(cache)
     if cache.c != 4:
         raise ValueError("compressed keys go to a cache of c = 4")
     return (*_compress_head(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary_dim, sections, theta, ring,

@@ -496,8 +496,9 @@ int kv4_load(const uint8_t* codes, const uint8_t* scales, int64_t num_pages, con
  *   k, v, dtype, ld_k, ld_v, head_dim: as kv4_store.
  * Device preconditions: the slots of one call are distinct, and those of one
  * page lie within 64 consecutive rows (in any order, with other rows between), as
- * pages_extend lists them; otherwise what the page holds is unspecified.  Tokens
- * of a page come in order of their slots, but for its first slot in any.
+ * pages_extend lists them; otherwise what the page holds is unspecified.  Since a
+ * page begins anew with its first slot, a call that writes that one comes before
+ * the calls that write the page's others; those may come in any order.
  *
  * kv8_load - reads rows back: row i of k and v receives the values of slot
  * slots[i] in `dtype` (exact in bf16 and fp32; rounded to fp16 where that
@@ -543,13 +544,15 @@ int kv8_load(const uint8_t* codes, const float* scales, int64_t num_pages, const
  * quantised as a key is, by the call; with q4 and k4 the values that queries and
  * keys then have,
  *   scores[r*ld_scores + j] = (1/sqrt(128)) * sum_{h=0..3} max(0, <q4[r][h][:], k4_b[j][:]>)
- * with sums in FP32.  Products with a group that is NaN count as 0.
+ * with sums in FP32.  Products with a group that is NaN count as 0.  Prompt chunks
+ * and single-token rows are served by one call, but quicker by one each (one
+ * kernel serves a call, chosen for its mean rows a request).
  *
  * All return BS_OK (also when there are no rows), BS_ERR_NULL, BS_ERR_ARG (dtype,
- * negative counts, cache_keys outside 1 .. 2^31 - 1, a stride below 128 or no
- * multiple of 8, a pointer (idx4_score: q, codes, scales) that is not 16-byte
- * aligned, and what idx_compress_store and idx_score_decode refuse) or
- * BS_ERR_LAUNCH.
+ * negative counts, cache_keys outside 1 .. 2^31 - 1, num_pages past 2^25 - 1 for
+ * idx4_score, a stride below 128 or no multiple of 8, a pointer (idx4_score: q,
+ * codes, scales) that is not 16-byte aligned, and what idx_compress_store and
+ * idx_score_decode refuse) or BS_ERR_LAUNCH.
  */
 int idx4_store(const void* keys, int32_t dtype, int64_t ld, const int32_t* slots, int32_t num_keys, uint8_t* codes,
                uint8_t* scales, int64_t cache_keys, void* stream);
@@ -590,9 +593,13 @@ int idx4_score(const uint16_t* q, const uint8_t* codes, const uint8_t* scales, i
  *   slots       [num_rows]: each new token's slot, table entry * 64 + position
  *               mod 64, for the calls that store.
  * Rows behind the last new token get row_pos and slot -1 (a captured call is of a
- * fixed num_rows).  When the ring has too few pages, the last requests' tokens
- * have no page: slot -1 and their table entries as they were; held_out counts the
- * pages there are, and pool_out[2] is how many are lacking.
+ * fixed num_rows).  The stores skip them; the scorers and attn_window leave what
+ * they have of them as it was, row_len too (fill it with zeros once); slot lists
+ * of them hold nothing but -1.  When the ring has too few pages, the last
+ * requests' tokens have no page: slot -1 and their table entries as they were;
+ * held_out counts the pages there are, and pool_out[2] is how many are lacking.
+ * Such tokens are in kv_len_out all the same: cut them off with pages_release, or
+ * the pages that a later call finds for them will hold what they held before.
  *
  * pages_release - cuts request b back to keep_len[b] tokens (0: it is finished;
  * below 0 or more than kv_len: no token goes) and puts its pages past
