@@ -544,9 +544,11 @@ int kv8_load(const uint8_t* codes, const float* scales, int64_t num_pages, const
  * quantised as a key is, by the call; with q4 and k4 the values that queries and
  * keys then have,
  *   scores[r*ld_scores + j] = (1/sqrt(128)) * sum_{h=0..3} max(0, <q4[r][h][:], k4_b[j][:]>)
- * with sums in FP32.  Products with a group that is NaN count as 0.  Prompt chunks
- * and single-token rows are served by one call, but quicker by one each (one
- * kernel serves a call, chosen for its mean rows a request).
+ * with sums in FP32 (products of scales below 2^-126 may count as 0; past FP32's
+ * range a score is unspecified, but no NaN).  Products with a group that is NaN
+ * count as 0.  Prompt chunks and single-token rows are served by one call, but
+ * quicker by one each (one kernel serves a call, chosen for its mean rows a
+ * request).
  *
  * All return BS_OK (also when there are no rows), BS_ERR_NULL, BS_ERR_ARG (dtype,
  * negative counts, cache_keys outside 1 .. 2^31 - 1, num_pages past 2^25 - 1 for

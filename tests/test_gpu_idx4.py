@@ -198,6 +198,34 @@ def test_groups_of_nan_count_as_nothing():
             assert (np.abs(got[r, :n] - want) <= bound).all(), r
 
 
+@pytest.mark.parametrize("rows", [3, 70])
+def test_scales_over_their_whole_range(rows):
+    """Keys and queries of 2^-118 to 2^120, whose products leave FP32's range on both sides.  Beside the bound, what may be
+    lost below its least normal number: 2^-126 for each of 4 x 128 products and as many sums, over sqrt(128)."""
+    say(f"idx4 scales rows={rows}")
+    rng = np.random.default_rng(rows)
+    pt, ptr, pos, kc, ks, q, vis = _score_case(1, [700], [rows], 2)
+    K = dequantise(kc, ks) * np.ldexp(1.0, rng.integers(-118, 118, (len(kc), 1)))
+    kc, ks = quantise(K)
+    q = (q.double() * torch.tensor(np.ldexp(1.0, rng.integers(-118, 118, (rows, 1, 1))))).bfloat16()
+    cache = bst.Idx4Cache(torch.from_numpy(kc).cuda(), torch.from_numpy(ks).cuda(), 1)
+    scores = torch.full((rows, vis), -77.0, device="cuda")
+    bst.idx4_score(q.cuda(), cache, _i32(pt), _i32(ptr), _i32(pos), vis, scores)
+    got = scores.cpu().numpy().astype(np.float64)
+    K, Q, finite = dequantise(kc, ks), dequantise(*quantise(_f64(q))), 0
+    for r in range(rows):
+        j = np.arange(pos[r] + 1)
+        k = K[pt[0][j // 64].astype(np.int64) * 64 + j % 64]
+        want, bound = score_row(Q[r], k)
+        mag = (np.abs(Q[r]) @ np.abs(k).T).sum(0)
+        small = mag < 2.0 ** 127                                 # no sum on the way leaves the range
+        finite += small.sum()
+        err = np.abs(np.where(small, got[r, j] - want, 0.0))
+        assert (err <= bound + 4 * 256 * 2.0 ** -126 / np.sqrt(128.0)).all(), (r, err.max())
+        assert not np.isnan(got[r, j]).any() and (got[r, j] >= 0).all()
+    assert finite > 300
+
+
 def test_caches_past_4_gib():
     """Keys whose byte offsets pass 32 bits."""
     say("idx4 past 4 GiB")
