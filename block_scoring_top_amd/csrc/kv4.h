@@ -19,6 +19,7 @@ constexpr int kExpMax = 252;        // 2^125: 6 * 2^125 is finite in bf16 and fp
 constexpr uint32_t kExpNan = 255;   // the group held an infinity or a NaN: every value reads back as NaN
 
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef int16_t i16x2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
@@ -48,6 +49,11 @@ struct Bf16 {
   template <int SEL>
   static __device__ __forceinline__ uint32_t from_fp8(uint32_t codes, float scale) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, SEL != 0));
+  }
+  // And back: nearest, ties to even; for finite values of at most 448 scales.
+  template <int SEL>
+  static __device__ __forceinline__ i16x2_t to_fp8(i16x2_t old, uint32_t two, float scale) {
+    return __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(old, __builtin_bit_cast(vec2, two), scale, SEL != 0);
   }
   // Bit pattern of |x| in 32 bits, for both halves of a pair.
   static __device__ __forceinline__ uint32_t abs_bits(uint32_t two) {
@@ -83,6 +89,11 @@ struct F16 {
   template <int SEL>
   static __device__ __forceinline__ uint32_t from_fp8(uint32_t codes, float scale) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes, scale, SEL != 0));
+  }
+  // And back: nearest, ties to even; for finite values of at most 448 scales.
+  template <int SEL>
+  static __device__ __forceinline__ i16x2_t to_fp8(i16x2_t old, uint32_t two, float scale) {
+    return __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(old, __builtin_bit_cast(vec2, two), scale, SEL != 0);
   }
   static __device__ __forceinline__ uint32_t abs_bits(uint32_t two) {
     const vec2 h = __builtin_bit_cast(vec2, two);

@@ -27,13 +27,11 @@ __device__ __forceinline__ int kv8_exponent(uint32_t top) {
   return min(max(e, kExpMin8), kExpMax8);
 }
 
-// Two values over their scale as codes, in the low or high half of `old`:
-// nearest, ties to even.  CAREFUL: at most 448, and NaN for infinities and NaN;
-// without it the values are finite and at most 448.
-template <bool HIGH, bool CAREFUL>
-__device__ __forceinline__ uint32_t kv8_codes(uint32_t old, float x, float y) {
+// Two values, already over their scale, as codes in the low or high half of `old`:
+// nearest, ties to even, at most 448, and NaN for infinities and NaN.
+template <bool HIGH>
+__device__ __forceinline__ uint32_t kv8_pack(uint32_t old, float x, float y) {
   auto fit = [](float v) {
-    if (!CAREFUL) return v;
     const float t = __builtin_amdgcn_fmed3f(v, -kTop8, kTop8);
     return fabsf(v) < INFINITY ? t : __builtin_nanf("");
   };

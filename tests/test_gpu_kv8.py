@@ -133,6 +133,49 @@ def test_store_and_load_match_the_definition(T, hkv, d, kind, layout, fused):
         assert (out[:, 2 * hkv:] == 7.0).all()
 
 
+@pytest.mark.parametrize("T,hkv,d,kind", [(70, 2, 64, "bf16"), (150, 1, 128, "f16"), (1023, 1, 256, "bf16"), (1024, 2, 64, "f32"),
+                                          (1500, 3, 128, "bf16"), (2600, 1, 256, "f16"), (1100, 2, 256, "f32")])
+@pytest.mark.parametrize("per", [2, 7, 24])
+@pytest.mark.parametrize("special", [False, True])
+def test_store_of_interwoven_pages(T, hkv, d, kind, per, special):
+    """Stretches of 64 rows, the first one shorter, each of the rows of `per` pages and padding in random order: runs of one
+    to some dozens of rows that cross the kernels' groups, into pages that hold something, whose scales some outgrow."""
+    say(f"kv8 woven T={T} hkv={hkv} d={d} {kind} per={per} special={special}")
+    rng = np.random.default_rng(T + per)
+    slots, page = [], 0
+    while len(slots) < T:
+        n = 64 if slots else 37
+        of = rng.integers(0, per + 1, n)                         # `per`: padding
+        part = np.full(n, -1)
+        for q in range(per):
+            at = np.nonzero(of == q)[0]
+            part[at] = (page + q) * 64 + rng.permutation(np.arange(int(rng.integers(0, 2)), 64))[:len(at)]
+        slots += list(part)
+        page += per
+    slots = np.array(slots[:T])
+    order = rng.permutation(page)
+    slots = np.where(slots >= 0, order[np.maximum(slots, 0) // 64] * 64 + slots % 64, -1)
+    cache, ref = _pair(page, hkv, d, T)
+    k, v = (x.clone() for x in _rows(T, hkv, d, kind, T * 3 + per, False))
+    if special:
+        for x, seed in ((k, 1), (v, 2)):
+            hit = torch.rand(x.shape, generator=_gen(seed), device="cuda") < 0.003
+            x[hit] = torch.tensor([float("nan"), float("inf"), -float("inf")], device="cuda").to(x.dtype).repeat(x.numel())[:int(hit.sum())]
+    bst.kv8_store(k, v, _i32(slots), cache)
+    torch.cuda.synchronize()
+    old = ref.exps.copy()
+    ref.store(_f64(k), _f64(v), slots)
+    assert (ref.exps > old).any()
+    begun = np.zeros(page, bool)
+    there = slots[slots >= 0]
+    begun[there[there % 64 == 0] // 64] = True
+    loose = np.repeat(begun, 64)
+    loose[there] = False
+    codes = cache.codes.cpu().numpy()
+    ref.codes[loose] = codes[loose]
+    _same(cache, ref)
+
+
 @pytest.mark.parametrize("d,kind", [(64, "f32"), (128, "bf16"), (256, "f16")])
 def test_appended_tokens_raise_the_scale(d, kind):
     """Token after token into the pages of 5 requests, some larger than all before: after each call, codes and scales of
