@@ -18,8 +18,8 @@
 // from the slots: they lie within 64 consecutive rows of the call, so a wave that
 // holds the 64 slots before its group and the 128 from there on sees all of every
 // run that begins in the group.  A run of up to 8 rows takes the lanes of one row,
-// beside 7 others (decode, verify), a longer one the workgroup: with a workgroup
-// for every run 2,100 tokens of a page each took 31 us, and 7 in this way.
+// beside 7 others (decode, verify), a longer one the workgroup: one after the other,
+// 2,000 tokens of a page each (2 heads of 128) took 15.4 us, and take 5.6 so.
 #include <algorithm>
 #include <type_traits>
 
