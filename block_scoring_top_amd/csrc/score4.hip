@@ -246,7 +246,7 @@ __global__ __launch_bounds__(64 * kScoreWaves) void score4_decode_kernel(const S
   }
 }
 
-// Many rows a request: 8 rows a wave, 1,024 keys a workgroup in four stages of 256.
+// Many rows a request: 8 rows a wave, STAGES times 256 keys a workgroup.
 //
 // Bound by the scores' writes, and how fast those go depends on their order.
 // Stores alone, 8,192 rows of 16,384, us: 102 with each wave writing 4 rows x 256
@@ -258,11 +258,11 @@ __global__ __launch_bounds__(64 * kScoreWaves) void score4_decode_kernel(const S
 // would take an access of the vector cache for every 16 bytes); the 16-byte pieces
 // of 4 consecutive keys (256 bytes) are XOR-ed with their number, which spreads the
 // operands' reads over the banks.
-constexpr int kStage = 4, kStages = 4;  // tiles in LDS at a time, stages of a workgroup
-constexpr int kRowGroups = 2;           // of 4 rows, a wave
-template <int C>
+constexpr int kStage = 4;      // tiles in LDS at a time
+constexpr int kRowGroups = 2;  // of 4 rows, a wave
+template <int C, int STAGES>
 __global__ __launch_bounds__(64 * kScoreWaves, 3) void score4_prefill_kernel(const ScoreArgs a) {
-  constexpr int RG = kRowGroups, STAGES = kStages;
+  constexpr int RG = kRowGroups;
   constexpr int PAGE_KEYS = kPage / C, ROWS = 4 * RG * kScoreWaves, KEYS = kStage * kTile, PAGES = KEYS / PAGE_KEYS;
   static_assert(kScoreWaves == 4, "a wave copies a quarter of a tile, 16 keys of one page");
   static_assert(PAGES * STAGES <= 64, "a lane a page");
@@ -343,11 +343,16 @@ __global__ __launch_bounds__(64 * kScoreWaves, 3) void score4_prefill_kernel(con
 namespace {
 
 // The kernel for few rows goes through all rows of a request in each workgroup,
-// the other is at its best with many.  us, few and many: 1 request of 60,000 tokens
-// (c = 4) with 32 rows 6.1 and 9.8, 64 9.7 and 10.1, 200 25.8 and 10.3; 64
-// requests of 5 to 33 thousand keys with 6 rows 15.7 and 29.7; 16 of them with 13
-// rows on average 11.9 and 13.0.
-constexpr int64_t kFewRows = 8, kSomeRows = 32, kRowsInAll = 256;
+// the other is at its best with many; over 575 calls (1 to 256 requests of 6 to
+// 8,192 rows, 1,000 to 65,536 tokens, c = 1 and 4) this rule costs 2% more than the
+// best of the three.  us, few rows / many with one stage / with four: 64 requests of
+// 8,000 tokens (c = 4) with 12 rows 5.8 / 6.8 / 11.5, 20 7.6 / 7.7 / 12.0, 32 9.2 /
+// 8.7 / 11.6; 16 of 65,536 (c = 1) with 16 rows 24.6 / 31.4 / 28.6.
+constexpr int64_t kFewRows = 20;
+// Below so many workgroups of four stages: one stage each, four times as many.  1
+// request of 65,536 tokens (c = 4) with 64 rows (48 workgroups) 6.5 us with one
+// stage, 10.7 with four, 512 (272) 13.4 and 12.6, 2,000 (1,008) 36.0 and 32.7.
+constexpr int64_t kFewGroups = 320;
 // From so many keys in all on, two tiles a wave: 16 x 81,920 keys 18.1 us, 19.1 with
 // one, 19.1 with four.
 constexpr int64_t kManyKeys = 1 << 18;
@@ -360,8 +365,8 @@ int launch_idx4_score(const uint16_t* q, const uint8_t* codes, const uint8_t* sc
                       int32_t* row_len, hipStream_t stream) {
   const ScoreArgs a = {q,       codes,   scales,   (int32_t)num_pages, page_table, pt_stride, req_row_ptr,
                        row_pos, num_req, num_rows, max_vis,            scores,     ld,        row_len};
-  const int64_t keys = std::max(max_vis, 1), mean = (num_rows + (int64_t)num_req - 1) / num_req;
-  const bool few = mean <= kFewRows || (mean <= kSomeRows && num_rows <= kRowsInAll);
+  const int64_t keys = std::max(max_vis, 1);
+  const bool few = num_rows <= kFewRows * (int64_t)num_req;
   auto decode = [&](auto cc, auto tiles) {
     constexpr int TILES = decltype(tiles)::value, CHUNK = kScoreWaves * TILES * kTile;
     hipLaunchKernelGGL((score4_decode_kernel<decltype(cc)::value, TILES>), dim3((uint32_t)((keys + CHUNK - 1) / CHUNK), num_req),
@@ -369,10 +374,17 @@ int launch_idx4_score(const uint16_t* q, const uint8_t* codes, const uint8_t* sc
   };
   auto run = [&](auto cc) {
     if (!few) {
-      constexpr int ROWS = 4 * kRowGroups * kScoreWaves, CHUNK = kStages * kStage * kTile;
+      constexpr int ROWS = 4 * kRowGroups * kScoreWaves;
       const int64_t blocks = std::min<int64_t>(num_rows / ROWS + num_req, 65535);  // at least as many as there are
-      hipLaunchKernelGGL(score4_prefill_kernel<decltype(cc)::value>, dim3((uint32_t)((keys + CHUNK - 1) / CHUNK), (uint32_t)blocks),
-                         dim3(64 * kScoreWaves), 0, stream, a);
+      auto prefill = [&](auto stages) {
+        constexpr int STAGES = decltype(stages)::value, CHUNK = STAGES * kStage * kTile;
+        hipLaunchKernelGGL((score4_prefill_kernel<decltype(cc)::value, STAGES>),
+                           dim3((uint32_t)((keys + CHUNK - 1) / CHUNK), (uint32_t)blocks), dim3(64 * kScoreWaves), 0, stream, a);
+      };
+      if ((keys + 4 * kStage * kTile - 1) / (4 * kStage * kTile) * blocks < kFewGroups)
+        prefill(std::integral_constant<int, 1>());
+      else
+        prefill(std::integral_constant<int, 4>());
     } else if (num_req * keys >= kManyKeys) {
       decode(cc, std::integral_constant<int, 2>());
     } else {

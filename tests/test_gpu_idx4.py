@@ -163,6 +163,14 @@ def test_scores_match_the_definition(c, ctx, rows, spread):
     _check_scores(c, *case)
 
 
+@pytest.mark.parametrize("c,ctx,rows", [(1, [4000, 70, 2500], [1500, 40, 1200]), (4, [12001, 900, 5], [3000, 500, 2]), (1, [10241], [700]),
+                                        (4, [33000, 16500, 4100], [20, 700, 1100]), (1, [257, 1025, 30] * 20, [200, 130, 7] * 20)])
+def test_scores_of_many_rows(c, ctx, rows):
+    """Large grids: workgroups of several stages, the last of them cut by the context, by the rows or by causality."""
+    say(f"idx4 c={c} {ctx[:3]} rows={rows[:3]}")
+    _check_scores(c, *_score_case(c, ctx, rows, sum(rows)))
+
+
 @pytest.mark.parametrize("rows", [[1, 2], [6, 8], [100, 40]])
 @pytest.mark.parametrize("c", [1, 4])
 def test_scores_odd_rows(rows, c):
