@@ -535,8 +535,9 @@ int kv8_load(const uint8_t* codes, const float* scales, int64_t num_pages, const
  * slot is negative or >= cache_keys.
  *
  * idx4_compress_store - idx_compress_store into the 4-bit keys (c = 4): the key,
- * rounded to bf16 as that call stores it, is quantised.  Same arguments with codes
- * and scales in place of kcache.
+ * rounded to FP32 and to bf16, is quantised.  Norm and rotation run in FP64: each
+ * element is within 2^-30 of the exact value of these steps (positions below 2^20)
+ * before it is rounded.  Same arguments with codes and scales in place of kcache.
  *
  * idx4_score - idx_score_decode and idx_score_prefill over the 4-bit keys, any
  * number of rows a request: the same arguments, layouts, outputs, preconditions
@@ -607,6 +608,9 @@ int idx4_score(const uint16_t* q, const uint8_t* codes, const uint8_t* scales, i
  * below 0 or more than kv_len: no token goes) and puts its pages past
  * ceil(tokens / 64) at the ring's end, requests in order, their table entries
  * becoming -1.
+ * (The ring of raw index keys that idx_compress_store keeps is another: where a cut
+ * goes back behind the block that was unfinished, its slots are the caller's to
+ * set back.)
  *
  * Calls on the same state must not overlap in time.  Both return BS_OK,
  * BS_ERR_NULL, BS_ERR_ARG (negative counts, pt_stride < 1, ring_size outside 1

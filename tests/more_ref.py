@@ -120,6 +120,26 @@ def pages_release(kv_len, held, keep_len, table, ring, pool):
     return dict(kv_len=kv_len, held=held, table=table, ring=ring, pool=[head, count, 0, 0])
 
 
+def bf16(x):
+    """float64 -> bf16 by way of FP32, as float64 (finite values)."""
+    u = np.asarray(x, np.float32).view(np.uint32)
+    return ((u + 0x7FFF + (u >> 16 & 1)) & 0xFFFF0000).astype(np.uint32).view(np.float32).astype(np.float64)
+
+
+def compressed_keys(raw, pos, rot, sections, theta):
+    """raw [n, 4, 128] (bf16 values), pos [n, 3] (t, h, w of the first token): the compressed keys [n, 128] in bf16."""
+    r = np.asarray(raw, np.float32)
+    mean = ((((r[:, 0] + r[:, 1]) + r[:, 2]) + r[:, 3]) * np.float32(0.25)).astype(np.float64)
+    norm = np.sqrt((mean * mean).sum(1, keepdims=True))
+    y = np.divide(mean, norm, out=np.zeros_like(mean), where=norm > 0)
+    i = np.arange(rot // 2)
+    comp = np.repeat([0, 1, 2], sections)
+    angle = np.asarray(pos, np.float64)[:, comp] * theta ** (-2.0 * i / max(rot, 1))
+    lo, hi = y[:, :rot // 2].copy(), y[:, rot // 2:rot].copy()
+    y[:, :rot // 2], y[:, rot // 2:rot] = lo * np.cos(angle) - hi * np.sin(angle), hi * np.cos(angle) + lo * np.sin(angle)
+    return bf16(y)
+
+
 def score_row(q, k):
     """q [4, 128], k [n, 128] float64: scores [n] and their bound."""
     x = q @ k.T
