@@ -109,7 +109,9 @@ __device__ __forceinline__ void load_dwords(uint32_t (&dst)[N], const uint8_t* p
 // the operands read from there: 122 -> 117 us there, 22.4 -> 21.6 (19.6 now) for 64 decode
 // rows of a 4,096 window (4-bit, D = 128), and 40 registers fewer.  The 16-bit
 // pools are staged at D = 64 only: larger chunks would leave LDS for too few
-// waves.
+// waves.  The 8-bit cache leaves two a SIMD at D = 128: 64 x 6 rows of 2,051 slots
+// 75 us, 79 unstaged; with one buffer and three waves 67, but then 512 rows take 66
+// for 53, and 64 x 6 windows of 4,000 130 for 68 (they spill).
 //
 // A buffer holds the rows of the 32 keys (4-bit and 8-bit: K and V codes, which
 // lie together, then the scales; 16-bit: K, then V), their 16-byte pieces XOR-ed
