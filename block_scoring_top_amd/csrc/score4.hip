@@ -47,6 +47,7 @@ struct ScoreArgs {
   float* scores;
   int64_t ld;
   int32_t* row_len;
+  int32_t more;  // blocks past the requests' first ones (few rows)
 };
 
 // 4 query rows as they are loaded: lane l has 32 channels of head l mod 4 of row
@@ -115,18 +116,19 @@ __device__ __forceinline__ void request_rows(const ScoreArgs& a, int b, int& r0,
   r0 = max(a.req_row_ptr[b], 0), r1 = min(a.req_row_ptr[b + 1], a.num_rows);
 }
 
-// Block `block` of up to ROWS rows of one request, the requests' blocks numbered one after the other: false if
-// there is none.  Lane i looks at every 64th request.
-template <int ROWS>
+// Block `block` of up to ROWS rows of one request, the requests' blocks (from their FROM-th on) numbered one after the
+// other: false if there is none.  Lane i looks at every 64th request.
+template <int ROWS, int FROM>
 __device__ __forceinline__ bool locate_rows(const ScoreArgs& a, uint32_t block, int lane, int& b, int& first, int& end) {
   for (int base = 0; base < a.num_req; base += 64) {
     int r0 = 0, r1 = 0;
     if (base + lane < a.num_req) request_rows(a, base + lane, r0, r1);
-    const uint32_t upto = wave_incl_scan(r1 > r0 ? ((uint32_t)(r1 - r0) + ROWS - 1) / ROWS : 0u), all = readlane(upto, 63);
+    const uint32_t blocks = r1 > r0 ? ((uint32_t)(r1 - r0) + ROWS - 1) / ROWS : 0u;
+    const uint32_t upto = wave_incl_scan(blocks > FROM ? blocks - FROM : 0u), all = readlane(upto, 63);
     if (block < all) {
       const int i = __builtin_ctzll(ballot(upto > block));
       b = base + i, r0 = (int)readlane(r0, i), r1 = (int)readlane(r1, i);
-      first = r0 + (int)(block - (i > 0 ? readlane(upto, i - 1) : 0u)) * ROWS;
+      first = r0 + (int)(block - (i > 0 ? readlane(upto, i - 1) : 0u) + FROM) * ROWS;
       end = r1 - first < ROWS ? r1 : first + ROWS;
       return true;
     }
@@ -184,13 +186,18 @@ __device__ __forceinline__ void store_scores(const Query& q, const u32x4_t (&k)[
 
 }  // namespace
 
-// Few rows a request: TILES tiles a wave.
+// Rows of a block in the kernel for few rows: one block is of the first rows of each request, others of the rest of
+// those that have more (63 requests of one row beside one of 1,000, 30,000 tokens each, c = 4: 22 us, 172 with a
+// request's rows in one block).
+constexpr int kRowsOnce = 64;
+
+// Few rows a request: TILES tiles a wave, up to 64 rows.
 //
 // What a wave does before its first product takes about as long as the products:
 // so page ids are one load (a lane a page: loads of one id for all lanes were
 // scalar, waited for one by one), and the waves prepare the rows' operands for
 // each other (64 requests x 6 rows over 586,000 keys of c = 4: 46 us with neither,
-// 15.7 now).  With MFMA j of a tile taking keys 4n + j a lane stores 4 scores at
+// 15.5 now).  With MFMA j of a tile taking keys 4n + j a lane stores 4 scores at
 // once.
 template <int C, int TILES>
 __global__ __launch_bounds__(64 * kScoreWaves) void score4_decode_kernel(const ScoreArgs a) {
@@ -199,18 +206,22 @@ __global__ __launch_bounds__(64 * kScoreWaves) void score4_decode_kernel(const S
   __shared__ uint32_t q_exponent[BATCH][64];
   __shared__ int q_vis[BATCH][4];
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), b = blockIdx.y;
-  int r0, r1;
-  request_rows(a, b, r0, r1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int b = (int)blockIdx.y - a.more, r0, r1;  // the rest of the long requests first: the search takes its time
+  if (b >= 0) {
+    request_rows(a, b, r0, r1);
+    r1 = r1 > r0 ? r0 + min(r1 - r0, kRowsOnce) : r0;
+  } else if (!locate_rows<kRowsOnce, 1>(a, blockIdx.y, lane, b, r0, r1)) {
+    return;
+  }
   const int64_t block0 = (int64_t)blockIdx.x * (kScoreWaves * TILES * kTile), k0 = block0 + wave * (TILES * kTile);
   const int key0 = (int)min(k0, (int64_t)0x7FFFFF00);
   // The pages of the wave's keys, on their way while the rows' lengths are found.
   const int my_page = page_at(a, a.page_table + (int64_t)b * a.pt_stride, key0 / PAGE_KEYS + min(lane, TILES * C - 1));
-  if (blockIdx.x == 0 && a.row_len != nullptr)
-    for (int r = r0 + tid; r < r1; r += 64 * kScoreWaves) a.row_len[r] = visible_blocks(a.row_pos[r], C, a.max_vis);
-  int most = 0;
-  for (int r = r0 + lane; r < r1; r += 64) most = max(most, visible_blocks(a.row_pos[r], C, a.max_vis));
-  most = wave_most(most);
+  const int row = lane < r1 - r0 ? visible_blocks(a.row_pos[r0 + lane], C, a.max_vis) : 0;
+  static_assert(kRowsOnce <= 64, "a lane a row");
+  if (blockIdx.x == 0 && wave == 0 && a.row_len != nullptr && lane < r1 - r0) a.row_len[r0 + lane] = row;
+  const int most = wave_most(row);
   if (block0 >= most) return;
 
   u32x4_t k[TILES][4], ex[TILES];
@@ -273,7 +284,7 @@ __global__ __launch_bounds__(64 * kScoreWaves, 3) void score4_prefill_kernel(con
   const int64_t k0 = (int64_t)blockIdx.x * (STAGES * KEYS);
   const uint32_t blocks = a.num_rows / ROWS + a.num_req;  // at least as many as there are
   int b, first, end;
-  for (uint32_t block = blockIdx.y; block < blocks && locate_rows<ROWS>(a, block, lane, b, first, end); block += gridDim.y) {
+  for (uint32_t block = blockIdx.y; block < blocks && locate_rows<ROWS, 0>(a, block, lane, b, first, end); block += gridDim.y) {
     const int my_page = page_at(a, a.page_table + (int64_t)b * a.pt_stride,
                                 (int)min(k0 / PAGE_KEYS, (int64_t)0x7FFFFF00) + min(lane, PAGES * STAGES - 1));
     const int row = first + lane < end ? visible_blocks(a.row_pos[first + lane], C, a.max_vis) : 0;
@@ -342,7 +353,7 @@ __global__ __launch_bounds__(64 * kScoreWaves, 3) void score4_prefill_kernel(con
 
 namespace {
 
-// The kernel for few rows goes through all rows of a request in each workgroup,
+// The kernel for few rows goes through up to 64 rows of a request in each workgroup,
 // the other is at its best with many; over 575 calls (1 to 256 requests of 6 to
 // 8,192 rows, 1,000 to 65,536 tokens, c = 1 and 4) this rule costs 2% more than the
 // best of the three.  us, few rows / many with one stage / with four: 64 requests of
@@ -364,12 +375,13 @@ int launch_idx4_score(const uint16_t* q, const uint8_t* codes, const uint8_t* sc
                       const int32_t* row_pos, int32_t num_rows, int32_t c, int32_t max_vis, float* scores, int64_t ld,
                       int32_t* row_len, hipStream_t stream) {
   const ScoreArgs a = {q,       codes,   scales,   (int32_t)num_pages, page_table, pt_stride, req_row_ptr,
-                       row_pos, num_req, num_rows, max_vis,            scores,     ld,        row_len};
+                       row_pos, num_req, num_rows, max_vis,            scores,     ld,        row_len,     num_rows / kRowsOnce};
   const int64_t keys = std::max(max_vis, 1);
-  const bool few = num_rows <= kFewRows * (int64_t)num_req;
+  const uint32_t few_blocks = num_req + a.more;  // at least as many as there are
+  const bool few = num_rows <= kFewRows * (int64_t)num_req && few_blocks <= 65535;
   auto decode = [&](auto cc, auto tiles) {
     constexpr int TILES = decltype(tiles)::value, CHUNK = kScoreWaves * TILES * kTile;
-    hipLaunchKernelGGL((score4_decode_kernel<decltype(cc)::value, TILES>), dim3((uint32_t)((keys + CHUNK - 1) / CHUNK), num_req),
+    hipLaunchKernelGGL((score4_decode_kernel<decltype(cc)::value, TILES>), dim3((uint32_t)((keys + CHUNK - 1) / CHUNK), few_blocks),
                        dim3(64 * kScoreWaves), 0, stream, a);
   };
   auto run = [&](auto cc) {

@@ -201,6 +201,17 @@ def test_scores_match_the_definition(c, ctx, rows, spread):
     _check_scores(c, *case)
 
 
+@pytest.mark.parametrize("c,ctx,rows", [(4, [9000, 700] * 35, [1, 0] * 34 + [600, 1]), (1, [300, 1200, 100, 1300], [1, 64, 0, 1] * 1),
+                                        (1, [900] * 40 + [400] * 30, [65] + [1] * 38 + [200] + [0, 1] * 15),
+                                        (4, [2000] * 130, [1] * 64 + [129] + [3] * 65), (1, [500] * 7, [0, 0, 130, 0, 0, 0, 0])])
+def test_scores_of_long_requests_among_short_ones(c, ctx, rows):
+    """At most 20 rows a request on average: the kernel for few rows, in which blocks past a request's first 64 rows are
+    others' work."""
+    assert sum(rows) <= 20 * len(rows)
+    say(f"idx4 c={c} {len(ctx)} requests rows={max(rows)}")
+    _check_scores(c, *_score_case(c, ctx, rows, sum(rows)))
+
+
 @pytest.mark.parametrize("c,ctx,rows", [(1, [4000, 70, 2500], [1500, 40, 1200]), (4, [12001, 900, 5], [3000, 500, 2]), (1, [10241], [700]),
                                         (4, [33000, 16500, 4100], [20, 700, 1100]), (1, [257, 1025, 30] * 20, [200, 130, 7] * 20)])
 def test_scores_of_many_rows(c, ctx, rows):
