@@ -2,7 +2,7 @@
 // back.
 //
 // Store.  A page's scale belongs to all its tokens, so the rows of a call that
-// lie in one page are one workgroup's work, for one kv head: with m their largest
+// lie in one page are one workgroup's work, for each kv head: with m their largest
 // finite magnitude (K and V apart),
 //   e = the least with m <= 448 * 2^e;  a call that writes the page's first slot
 //   sets the page's scale to 2^e, any other raises it to 2^e if it is below,
@@ -18,8 +18,8 @@
 // from the slots: they lie within 64 consecutive rows of the call, so a wave that
 // holds the 64 slots before its group and the 128 from there on sees all of every
 // run that begins in the group.  A run of up to 8 rows takes the lanes of one row,
-// beside 7 others (decode, verify), a longer one the workgroup: one after the other,
-// 2,000 tokens of a page each (2 heads of 128) took 15.4 us, and take 5.6 so.
+// beside 7 others (decode, verify), a longer one the workgroup (2,000 tokens of a page
+// each, 2 heads of 128: 5.6 us, 15.4 with one run after the other).
 #include <algorithm>
 #include <type_traits>
 
