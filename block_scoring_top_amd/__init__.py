@@ -90,6 +90,9 @@ def lib():
         L.idx_compress_store.argtypes = [P, i32, P, P, P, i32, i32, i32, i32, i32, i32, C.c_double, P, P, P, i32,
                                          P, i64, P]
         L.idx_compress_store.restype = C.c_int
+        L.idx_compress_store_ring.argtypes = [P, i32, P, P, P, i32, i32, i32, i32, i32, i32, C.c_double, P, P, i32, P,
+                                              i32, P, i64, P]
+        L.idx_compress_store_ring.restype = C.c_int
         L.kv4_store.argtypes = [P, P, i32, i64, i64, P, i32, i32, i32, P, P, i64, P]
         L.kv4_store.restype = C.c_int
         L.kv4_load.argtypes = [P, P, i64, P, i32, i32, i32, P, P, i32, i64, i64, P]
@@ -105,6 +108,9 @@ def lib():
         L.idx4_compress_store.argtypes = [P, i32, P, P, P, i32, i32, i32, i32, i32, i32, C.c_double, P, P, P, i32,
                                           P, P, i64, P]
         L.idx4_compress_store.restype = C.c_int
+        L.idx4_compress_store_ring.argtypes = [P, i32, P, P, P, i32, i32, i32, i32, i32, i32, C.c_double, P, P, i32, P,
+                                               i32, P, P, i64, P]
+        L.idx4_compress_store_ring.restype = C.c_int
         L.idx4_score.argtypes = [P, P, P, i64, P, i32, P, i32, P, i32, i32, i32, P, i64, P, P]
         L.idx4_score.restype = C.c_int
         pages_args = [P, P, P, i32, P, i32, P, i32, P, P, P, P]
@@ -377,31 +383,33 @@ def idx_select_translate_planned(scores, max_len, k, req_row_ptr, row_pos, c, pa
 
 def _compress_head(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary_dim, sections, theta, ring, ring_pos,
                    page_table):
-    """The checked arguments that both compressing calls begin with."""
+    """The checked arguments that both compressing calls begin with (the C calls
+    with a ring of any depth, which its shape gives)."""
     dev = k_raw.device
     T = int(k_raw.shape[0])
     B = int(req_tok_ptr.shape[0]) - 1
     if k_raw.dim() != 2 or k_raw.shape[1] != 128:
         raise ValueError("k_raw must be [num_tok, 128]")
-    if tok_start.numel() != B or ring.shape != (B, 4, 128):
-        raise ValueError("tok_start must hold num_req entries and ring be [num_req, 4, 128]")
+    if tok_start.numel() != B or ring.dim() != 3 or ring.shape[0] != B or ring.shape[1] < 4 or ring.shape[2] != 128:
+        raise ValueError("tok_start must hold num_req entries and ring be [num_req, ring_slots, 128]")
+    slots = _size(ring.shape[1])
     if mrope_pos is not None and mrope_pos.shape != (T, 3):
         raise ValueError("mrope_pos must be [num_tok, 3]")
-    if ring_pos is not None and ring_pos.shape != (B, 3):
-        raise ValueError("ring_pos must be [num_req, 3]")
+    if ring_pos is not None and ring_pos.shape != (B, slots // 4, 3) and (slots > 4 or ring_pos.shape != (B, 3)):
+        raise ValueError("ring_pos must be [num_req, ring_slots / 4, 3]")
     sec = [int(v) for v in sections]
     if len(sec) != 3:
         raise ValueError("sections must hold 3 entries (t, h, w)")
     return (_ptr(k_raw, _BF16, "k_raw", dev), T, _ptr(req_tok_ptr, _I32, "req_tok_ptr", dev),
             _ptr(tok_start, _I32, "tok_start", dev), _ptr(mrope_pos, _I32, "mrope_pos", dev), B, int(max_tok),
             int(rotary_dim), sec[0], sec[1], sec[2], float(theta), _ptr(ring, _BF16, "ring", dev),
-            _ptr(ring_pos, _I32, "ring_pos", dev), _ptr(page_table, _I32, "page_table", dev),
+            _ptr(ring_pos, _I32, "ring_pos", dev), slots, _ptr(page_table, _I32, "page_table", dev),
             int(page_table.shape[1]))
 
 
 def _compress_args(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary_dim, sections, theta, ring,
                    ring_pos, page_table, kcache, num_pages):
-    """Checked argument tuple of an ``idx_compress_store`` call (all but the stream)."""
+    """Checked argument tuple of an ``idx_compress_store_ring`` call (all but the stream)."""
     if kcache.dim() != 2 or kcache.shape[1] != 128 or kcache.shape[0] < 16 * int(num_pages):
         raise ValueError("kcache must be [>= num_pages * 16, 128]")
     return (*_compress_head(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary_dim, sections, theta, ring,
@@ -411,10 +419,13 @@ def _compress_args(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary_dim
 def idx_compress_store(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary_dim, sections, theta, ring,
                        ring_pos, page_table, kcache, num_pages, stream=None):
     """Compress new raw index keys into the c = 4 key cache (and update the
-    rings).  See ``idx_compress_store`` in blockscore.h."""
+    rings).  ``ring`` [num_req, ring_slots, 128], ``ring_pos`` [num_req,
+    ring_slots / 4, 3] or None: 4 slots for requests that only grow, more (a power
+    of two, at least the tokens cut off + 3) for requests that are cut back.  See
+    ``idx_compress_store`` and ``idx_compress_store_ring`` in blockscore.h."""
     args = _compress_args(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary_dim, sections, theta, ring,
                           ring_pos, page_table, kcache, num_pages)
-    _check(lib().idx_compress_store(*args, _stream(stream, k_raw.device)), "idx_compress_store")
+    _check(lib().idx_compress_store_ring(*args, _stream(stream, k_raw.device)), "idx_compress_store")
 
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # bs_dtype
@@ -647,7 +658,7 @@ def idx4_load(cache: Idx4Cache, slots, keys, stream=None):
 
 def _idx4_compress_args(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary_dim, sections, theta, ring, ring_pos,
                         page_table, cache):
-    """Checked argument tuple of an ``idx4_compress_store`` call (all but the stream)."""
+    """Checked argument tuple of an ``idx4_compress_store_ring`` call (all but the stream)."""
     _idx4_cache(cache)
     if cache.c != 4:
         raise ValueError("compressed keys go to a cache of c = 4")
@@ -658,10 +669,11 @@ def _idx4_compress_args(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotar
 def idx4_compress_store(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary_dim, sections, theta, ring, ring_pos,
                         page_table, cache: Idx4Cache, stream=None):
     """Compress new raw index keys into the 4-bit c = 4 keys (and update the
-    rings).  See ``idx4_compress_store`` in blockscore.h."""
-    PreparedCall("idx4_compress_store", _idx4_compress_args(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok,
-                                                            rotary_dim, sections, theta, ring, ring_pos, page_table,
-                                                            cache), k_raw.device, once=True)(stream)
+    rings, which are ``idx_compress_store``'s).  See ``idx4_compress_store`` in
+    blockscore.h."""
+    PreparedCall("idx4_compress_store_ring", _idx4_compress_args(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok,
+                                                                 rotary_dim, sections, theta, ring, ring_pos,
+                                                                 page_table, cache), k_raw.device, once=True)(stream)
 
 
 def _idx4_score_args(q, cache, page_table, req_row_ptr, row_pos, max_vis, scores, row_len=None):
@@ -936,7 +948,7 @@ __all__ = [
 def prepare_compress_store(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary_dim, sections, theta, ring,
                            ring_pos, page_table, kcache, num_pages) -> PreparedCall:
     """``idx_compress_store`` with fixed arguments."""
-    return PreparedCall("idx_compress_store",
+    return PreparedCall("idx_compress_store_ring",
                         _compress_args(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary_dim, sections,
                                        theta, ring, ring_pos, page_table, kcache, num_pages), k_raw.device)
 
@@ -974,7 +986,7 @@ def prepare_idx4_load(cache: Idx4Cache, slots, keys) -> PreparedCall:
 def prepare_idx4_compress_store(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary_dim, sections, theta, ring,
                                 ring_pos, page_table, cache: Idx4Cache) -> PreparedCall:
     """``idx4_compress_store`` with fixed arguments."""
-    return PreparedCall("idx4_compress_store", _idx4_compress_args(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok,
+    return PreparedCall("idx4_compress_store_ring", _idx4_compress_args(k_raw, req_tok_ptr, tok_start, mrope_pos, max_tok,
                                                                    rotary_dim, sections, theta, ring, ring_pos,
                                                                    page_table, cache), k_raw.device)
 

@@ -224,13 +224,14 @@ namespace {
 inline int check_compress_args(const uint16_t* k_raw, int32_t num_tok, const int32_t* req_tok_ptr,
                                const int32_t* tok_start, const int32_t* mrope_pos, int32_t num_req, int32_t max_tok,
                                int32_t rotary_dim, int32_t sec_t, int32_t sec_h, int32_t sec_w, double theta,
-                               const uint16_t* ring, const int32_t* ring_pos, const int32_t* page_table,
-                               int32_t pt_stride, const void* cache, int64_t num_pages) {
+                               const uint16_t* ring, const int32_t* ring_pos, int32_t ring_slots,
+                               const int32_t* page_table, int32_t pt_stride, const void* cache, int64_t num_pages) {
   if (num_req < 0 || num_tok < 0 || max_tok < 0 || num_pages < 0 || num_req > 65535) return BS_ERR_ARG;
   if (max_tok > num_tok) return BS_ERR_ARG;
   if (rotary_dim < 0 || rotary_dim > BS_DIM || (rotary_dim & 1)) return BS_ERR_ARG;
   if (sec_t < 0 || sec_h < 0 || sec_w < 0 || sec_t + sec_h + sec_w != rotary_dim / 2) return BS_ERR_ARG;
   if (!(theta > 0.0) || !std::isfinite(theta)) return BS_ERR_ARG;
+  if (ring_slots < 4 || ring_slots > BS_MAX_RING_SLOTS || (ring_slots & (ring_slots - 1))) return BS_ERR_ARG;
   if (num_req == 0 || num_tok == 0 || max_tok == 0) return BS_OK;
   if (!k_raw || !req_tok_ptr || !tok_start || !ring || !page_table || !cache) return BS_ERR_NULL;
   if (mrope_pos && !ring_pos) return BS_ERR_NULL;
@@ -240,17 +241,28 @@ inline int check_compress_args(const uint16_t* k_raw, int32_t num_tok, const int
 
 }  // namespace
 
+BS_EXPORT int idx_compress_store_ring(const uint16_t* k_raw, int32_t num_tok, const int32_t* req_tok_ptr,
+                                      const int32_t* tok_start, const int32_t* mrope_pos, int32_t num_req,
+                                      int32_t max_tok, int32_t rotary_dim, int32_t sec_t, int32_t sec_h, int32_t sec_w,
+                                      double theta, uint16_t* ring, int32_t* ring_pos, int32_t ring_slots,
+                                      const int32_t* page_table, int32_t pt_stride, uint16_t* kcache,
+                                      int64_t num_pages, void* stream) {
+  const int st =
+      check_compress_args(k_raw, num_tok, req_tok_ptr, tok_start, mrope_pos, num_req, max_tok, rotary_dim, sec_t, sec_h,
+                          sec_w, theta, ring, ring_pos, ring_slots, page_table, pt_stride, kcache, num_pages);
+  if (st != BS_OK || num_req == 0 || num_tok == 0 || max_tok == 0) return st;
+  return bs::launch_compress(k_raw, num_tok, req_tok_ptr, tok_start, mrope_pos, num_req, max_tok, rotary_dim,
+                             sec_t, sec_h, theta, ring, ring_pos, ring_slots, page_table, pt_stride, kcache, num_pages,
+                             static_cast<hipStream_t>(stream));
+}
+
 BS_EXPORT int idx_compress_store(const uint16_t* k_raw, int32_t num_tok, const int32_t* req_tok_ptr,
                                  const int32_t* tok_start, const int32_t* mrope_pos, int32_t num_req,
                                  int32_t max_tok, int32_t rotary_dim, int32_t sec_t, int32_t sec_h, int32_t sec_w,
                                  double theta, uint16_t* ring, int32_t* ring_pos, const int32_t* page_table,
                                  int32_t pt_stride, uint16_t* kcache, int64_t num_pages, void* stream) {
-  const int st = check_compress_args(k_raw, num_tok, req_tok_ptr, tok_start, mrope_pos, num_req, max_tok, rotary_dim,
-                                     sec_t, sec_h, sec_w, theta, ring, ring_pos, page_table, pt_stride, kcache, num_pages);
-  if (st != BS_OK || num_req == 0 || num_tok == 0 || max_tok == 0) return st;
-  return bs::launch_compress(k_raw, num_tok, req_tok_ptr, tok_start, mrope_pos, num_req, max_tok, rotary_dim,
-                             sec_t, sec_h, theta, ring, ring_pos, page_table, pt_stride, kcache, num_pages,
-                             static_cast<hipStream_t>(stream));
+  return idx_compress_store_ring(k_raw, num_tok, req_tok_ptr, tok_start, mrope_pos, num_req, max_tok, rotary_dim, sec_t,
+                                 sec_h, sec_w, theta, ring, ring_pos, 4, page_table, pt_stride, kcache, num_pages, stream);
 }
 
 namespace {
@@ -380,20 +392,32 @@ BS_EXPORT int idx4_load(const uint8_t* codes, const uint8_t* scales, int64_t cac
                               static_cast<hipStream_t>(stream));
 }
 
+BS_EXPORT int idx4_compress_store_ring(const uint16_t* k_raw, int32_t num_tok, const int32_t* req_tok_ptr,
+                                       const int32_t* tok_start, const int32_t* mrope_pos, int32_t num_req,
+                                       int32_t max_tok, int32_t rotary_dim, int32_t sec_t, int32_t sec_h,
+                                       int32_t sec_w, double theta, uint16_t* ring, int32_t* ring_pos,
+                                       int32_t ring_slots, const int32_t* page_table, int32_t pt_stride, uint8_t* codes,
+                                       uint8_t* scales, int64_t num_pages, void* stream) {
+  const int st =
+      check_compress_args(k_raw, num_tok, req_tok_ptr, tok_start, mrope_pos, num_req, max_tok, rotary_dim, sec_t, sec_h,
+                          sec_w, theta, ring, ring_pos, ring_slots, page_table, pt_stride, codes, num_pages);
+  if (st != BS_OK || num_req == 0 || num_tok == 0 || max_tok == 0) return st;
+  if (!scales) return BS_ERR_NULL;
+  if (!aligned16(codes) || !aligned16(scales)) return BS_ERR_ARG;
+  return bs::launch_compress4(k_raw, num_tok, req_tok_ptr, tok_start, mrope_pos, num_req, max_tok, rotary_dim,
+                              sec_t, sec_h, theta, ring, ring_pos, ring_slots, page_table, pt_stride, codes, scales,
+                              num_pages, static_cast<hipStream_t>(stream));
+}
+
 BS_EXPORT int idx4_compress_store(const uint16_t* k_raw, int32_t num_tok, const int32_t* req_tok_ptr,
                                   const int32_t* tok_start, const int32_t* mrope_pos, int32_t num_req,
                                   int32_t max_tok, int32_t rotary_dim, int32_t sec_t, int32_t sec_h, int32_t sec_w,
                                   double theta, uint16_t* ring, int32_t* ring_pos, const int32_t* page_table,
                                   int32_t pt_stride, uint8_t* codes, uint8_t* scales, int64_t num_pages,
                                   void* stream) {
-  const int st = check_compress_args(k_raw, num_tok, req_tok_ptr, tok_start, mrope_pos, num_req, max_tok, rotary_dim,
-                                     sec_t, sec_h, sec_w, theta, ring, ring_pos, page_table, pt_stride, codes, num_pages);
-  if (st != BS_OK || num_req == 0 || num_tok == 0 || max_tok == 0) return st;
-  if (!scales) return BS_ERR_NULL;
-  if (!aligned16(codes) || !aligned16(scales)) return BS_ERR_ARG;
-  return bs::launch_compress4(k_raw, num_tok, req_tok_ptr, tok_start, mrope_pos, num_req, max_tok, rotary_dim,
-                              sec_t, sec_h, theta, ring, ring_pos, page_table, pt_stride, codes, scales, num_pages,
-                              static_cast<hipStream_t>(stream));
+  return idx4_compress_store_ring(k_raw, num_tok, req_tok_ptr, tok_start, mrope_pos, num_req, max_tok, rotary_dim, sec_t,
+                                  sec_h, sec_w, theta, ring, ring_pos, 4, page_table, pt_stride, codes, scales, num_pages,
+                                  stream);
 }
 
 BS_EXPORT int idx4_score(const uint16_t* q, const uint8_t* codes, const uint8_t* scales, int64_t num_pages,

@@ -24,6 +24,11 @@
 // sin/cos, FP32 rotation, one rounding to bf16, and a coalesced 256-byte
 // store.  The first wave of each request also updates its ring, after it has
 // consumed any ring entries.
+//
+// A ring of 4 slots holds what a request that only grows needs.  One that is cut
+// back (rejected draft tokens) needs the unfinished block of where it is cut, which
+// later tokens at the same positions mod 4 have overwritten there; a ring of S
+// slots, the token at position p in slot p mod S, still has it after a cut by S - 3.
 #include <cmath>
 #include <type_traits>
 
@@ -60,12 +65,14 @@ __device__ __forceinline__ float wave_max(float v) {
 // 4-bit cache (kcache: codes) in place of being stored as they are.  Half a step of
 // a 4-bit value is a quarter of it, so that a key on the wrong side of a tie would
 // be far off: norm and rotation are in FP64 then (8,192 tokens: 5.0 us, 4.7 in FP32).
-template <bool FOUR>
+// DEEP: the ring has more than 4 slots (with their number known 8,192 tokens take 3.9
+// and 4.4 us, 4.0 and 4.5 without).
+template <bool FOUR, bool DEEP>
 __global__ __launch_bounds__(64) void compress_kernel(
     const uint16_t* __restrict__ k_raw, int32_t num_tok, const int32_t* __restrict__ req_tok_ptr,
     const int32_t* __restrict__ tok_start, const int32_t* __restrict__ mrope_pos, int32_t max_tok,
     int32_t rot, int32_t sec0, int32_t sec01, double base,
-    uint16_t* ring, int32_t* ring_pos,
+    uint16_t* ring, int32_t* ring_pos, int32_t deep_slots,
     const int32_t* __restrict__ page_table, int32_t pt_stride,
     uint16_t* __restrict__ kcache, uint8_t* __restrict__ scales, int64_t num_pages) {
   __shared__ __align__(16) uint16_t raw[4][kDim];
@@ -89,9 +96,18 @@ __global__ __launch_bounds__(64) void compress_kernel(
   };
   const int u = lane >> 4, c16 = lane & 15;     // raw key u, 16-byte chunk c16
 
-  // Ring update of the request's first wave: slot u ends up holding the
-  // newest token p <= e with p mod 4 == u, when that token is new.  Its
-  // loads read k_raw only and are issued first; its stores come last.
+  // The slots of a position's raw key and of its block's MRoPE position (a
+  // power of two of each).
+  const int ring_slots = DEEP ? deep_slots : 4, slot_mask = ring_slots - 1, block_mask = slot_mask >> 2;
+  auto ring_key = [&](int64_t p) { return ring + ((int64_t)b * ring_slots + ((int)p & slot_mask)) * kDim; };
+  auto ring_block = [&](int64_t p) {
+    return ring_pos + ((int64_t)b * (ring_slots >> 2) + ((int)(p >> 2) & block_mask)) * 3;
+  };
+
+  // Ring update of the request's first wave: lanes u write the newest token
+  // p <= e with p mod 4 == u, when that token is new, and those before it that a
+  // deeper ring still holds.  Its loads read k_raw only and the first are issued
+  // first; its stores come last.
   const int64_t pu = e - ((e - u) & 3);
   const bool ring_slot = item == 0 && pu >= s;
   uint4 ring_val = make_uint4(0, 0, 0, 0);
@@ -100,7 +116,7 @@ __global__ __launch_bounds__(64) void compress_kernel(
   if (item < nb) {
     const int64_t j = j0 + item;
     const int64_t p = 4 * j + u;
-    const uint16_t* src = p >= s ? k_raw + row_of(p) * kDim : ring + ((int64_t)b * 4 + u) * kDim;
+    const uint16_t* src = p >= s ? k_raw + row_of(p) * kDim : ring_key(p);
     const uint4 v = reinterpret_cast<const uint4*>(src)[c16];
     const int64_t lp = (4 * j) >> 6;            // logical page of the block
     const int page = lp < pt_stride ? page_table[(int64_t)b * pt_stride + lp] : -1;
@@ -109,7 +125,7 @@ __global__ __launch_bounds__(64) void compress_kernel(
     if (mrope_pos == nullptr) {
       P[0] = P[1] = P[2] = (int)pf;
     } else {
-      const int32_t* mp = pf >= s ? mrope_pos + row_of(pf) * 3 : ring_pos + (int64_t)b * 3;
+      const int32_t* mp = pf >= s ? mrope_pos + row_of(pf) * 3 : ring_block(pf);
       P[0] = mp[0];
       P[1] = mp[1];
       P[2] = mp[2];
@@ -204,10 +220,14 @@ __global__ __launch_bounds__(64) void compress_kernel(
   if (item == 0) {
     // The block above read its ring entries into LDS before its first
     // barrier, so these stores come after those reads.
-    if (ring_slot) reinterpret_cast<uint4*>(ring + ((int64_t)b * 4 + u) * kDim)[c16] = ring_val;
+    if (ring_slot) reinterpret_cast<uint4*>(ring_key(pu))[c16] = ring_val;
+    if constexpr (DEEP)
+      for (int64_t p = pu - 4; p >= s && p > e - ring_slots; p -= 4)
+        reinterpret_cast<uint4*>(ring_key(p))[c16] = reinterpret_cast<const uint4*>(k_raw + row_of(p) * kDim)[c16];
     const int64_t p0 = e - (e & 3);             // newest block start <= e
-    if (ring_pos != nullptr && lane < 3 && p0 >= s)
-      ring_pos[(int64_t)b * 3 + lane] = mrope_pos != nullptr ? mrope_pos[row_of(p0) * 3 + lane] : (int32_t)p0;
+    if (ring_pos != nullptr && lane < 3)
+      for (int64_t p = p0; p >= s && p > p0 - ring_slots; p -= 4)
+        ring_block(p)[lane] = mrope_pos != nullptr ? mrope_pos[row_of(p) * 3 + lane] : (int32_t)p;
   }
 }
 
@@ -216,14 +236,20 @@ namespace {
 template <bool FOUR>
 int launch(const uint16_t* k_raw, int32_t num_tok, const int32_t* req_tok_ptr, const int32_t* tok_start,
            const int32_t* mrope_pos, int32_t num_req, int32_t max_tok, int32_t rotary_dim, int32_t sec_t, int32_t sec_h,
-           double theta, uint16_t* ring, int32_t* ring_pos, const int32_t* page_table, int32_t pt_stride,
+           double theta, uint16_t* ring, int32_t* ring_pos, int32_t ring_slots, const int32_t* page_table, int32_t pt_stride,
            uint16_t* kcache, uint8_t* scales, int64_t num_pages, hipStream_t stream) {
   const int items = max(1, (max_tok + 3) / 4);
   // theta^(-2/rot), the ratio of successive pair frequencies
   const double base = rotary_dim > 0 ? std::pow(theta, -2.0 / (double)rotary_dim) : 1.0;
-  hipLaunchKernelGGL(compress_kernel<FOUR>, dim3(items, num_req), dim3(64), 0, stream, k_raw, num_tok, req_tok_ptr,
-                     tok_start, mrope_pos, max_tok, rotary_dim, sec_t, sec_t + sec_h, base, ring, ring_pos,
-                     page_table, pt_stride, kcache, scales, num_pages);
+  auto go = [&](auto deep) {
+    hipLaunchKernelGGL((compress_kernel<FOUR, decltype(deep)::value>), dim3(items, num_req), dim3(64), 0, stream, k_raw,
+                       num_tok, req_tok_ptr, tok_start, mrope_pos, max_tok, rotary_dim, sec_t, sec_t + sec_h, base, ring,
+                       ring_pos, ring_slots, page_table, pt_stride, kcache, scales, num_pages);
+  };
+  if (ring_slots > 4)
+    go(std::true_type());
+  else
+    go(std::false_type());
   return hipGetLastError() == hipSuccess ? BS_OK : BS_ERR_LAUNCH;
 }
 
@@ -231,20 +257,20 @@ int launch(const uint16_t* k_raw, int32_t num_tok, const int32_t* req_tok_ptr, c
 
 int launch_compress(const uint16_t* k_raw, int32_t num_tok, const int32_t* req_tok_ptr, const int32_t* tok_start,
                     const int32_t* mrope_pos, int32_t num_req, int32_t max_tok, int32_t rotary_dim,
-                    int32_t sec_t, int32_t sec_h, double theta, uint16_t* ring, int32_t* ring_pos,
+                    int32_t sec_t, int32_t sec_h, double theta, uint16_t* ring, int32_t* ring_pos, int32_t ring_slots,
                     const int32_t* page_table, int32_t pt_stride, uint16_t* kcache, int64_t num_pages,
                     hipStream_t stream) {
   return launch<false>(k_raw, num_tok, req_tok_ptr, tok_start, mrope_pos, num_req, max_tok, rotary_dim, sec_t, sec_h,
-                       theta, ring, ring_pos, page_table, pt_stride, kcache, nullptr, num_pages, stream);
+                       theta, ring, ring_pos, ring_slots, page_table, pt_stride, kcache, nullptr, num_pages, stream);
 }
 
 int launch_compress4(const uint16_t* k_raw, int32_t num_tok, const int32_t* req_tok_ptr, const int32_t* tok_start,
                      const int32_t* mrope_pos, int32_t num_req, int32_t max_tok, int32_t rotary_dim,
-                     int32_t sec_t, int32_t sec_h, double theta, uint16_t* ring, int32_t* ring_pos,
+                     int32_t sec_t, int32_t sec_h, double theta, uint16_t* ring, int32_t* ring_pos, int32_t ring_slots,
                      const int32_t* page_table, int32_t pt_stride, uint8_t* codes, uint8_t* scales, int64_t num_pages,
                      hipStream_t stream) {
   return launch<true>(k_raw, num_tok, req_tok_ptr, tok_start, mrope_pos, num_req, max_tok, rotary_dim, sec_t, sec_h,
-                      theta, ring, ring_pos, page_table, pt_stride, reinterpret_cast<uint16_t*>(codes), scales, num_pages,
+                      theta, ring, ring_pos, ring_slots, page_table, pt_stride, reinterpret_cast<uint16_t*>(codes), scales, num_pages,
                       stream);
 }
 

@@ -24,8 +24,9 @@ class PagedBatch:
     ``extend``, ``req_row_ptr`` and ``row_pos`` are what the scorers, the
     selection and ``attn_window`` take, and ``slots`` what ``kv4_store``,
     ``kv8_store`` and ``idx4_store`` (c = 1) take; ``tok_start`` and
-    ``req_row_ptr`` are what the key compression takes.  Nothing here waits for the
-    GPU; calls on one batch belong on one stream."""
+    ``req_row_ptr`` are what the key compression takes, with a ring of
+    ``key_ring``.  Nothing here waits for the GPU; calls on one batch belong on one
+    stream."""
 
     def __init__(self, num_req: int, max_tokens: int, num_pages: int, num_rows: int, device):
         n = dict(dtype=torch.int32, device=device)
@@ -43,9 +44,22 @@ class PagedBatch:
         pages_extend(self.pool, self.kv_len, self.held, new_len, self.page_table, self.req_row_ptr, self.row_pos,
                      self.slots, tok_start=self.tok_start, stream=stream)
 
+    def key_ring(self, most_cut: int, mrope: bool = False):
+        """``ring`` and ``ring_pos`` (None unless the keys have MRoPE positions) for
+        the key compression of this batch, deep enough for requests that
+        ``release`` cuts back to up to ``most_cut`` tokens below the most that they
+        have had: the draft tokens of a step, say."""
+        slots = 4
+        while slots < int(most_cut) + 3:
+            slots *= 2
+        n, dev = self.kv_len.numel(), self.kv_len.device
+        return (torch.zeros((n, slots, 128), dtype=torch.bfloat16, device=dev),
+                torch.zeros((n, slots // 4, 3), dtype=torch.int32, device=dev) if mrope else None)
+
     def release(self, keep_len, stream=None):
         """Cuts requests back to ``keep_len`` [num_req] tokens (0: finished;
-        below 0: left alone)."""
+        below 0: left alone).  Compressed index keys (c = 4) come out right after
+        it if the raw keys' ring is deep enough (``key_ring``)."""
         pages_release(self.pool, self.kv_len, self.held, keep_len, self.page_table, stream=stream)
 
 

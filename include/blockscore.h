@@ -102,6 +102,7 @@ enum bs_status {
 #define BS_PAGE_TOKENS 64 /* tokens per KV page */
 #define BS_KMAX 2048      /* largest runtime k [TOPK] */
 #define BS_MAX_ADVANCE 1024 /* largest max_advance of idx_expand_translate_shared */
+#define BS_MAX_RING_SLOTS 65536 /* largest ring_slots of idx_compress_store_ring */
 
 /*
  * idx_score_decode - paged block scores for decode / speculative-verify rows
@@ -407,6 +408,19 @@ int idx_select_translate_planned(const float* scores, int64_t ld_scores, int32_t
  * BS_ERR_ARG (negative counts, num_req > 65535, max_tok > num_tok, bad
  * rotary_dim, sections or theta, pt_stride < 1, num_pages < 1) or
  * BS_ERR_LAUNCH.
+ *
+ * idx_compress_store_ring - the same with a ring of ring_slots raw keys, for
+ * requests that are cut back (rejected draft tokens).  The token at position p is
+ * written to ring slot p mod ring_slots and, when p mod 4 == 0, its MRoPE position
+ * to entry (p / 4) mod (ring_slots / 4) of ring_pos.  A request that has had
+ * tokens up to m of them and is cut back to n goes on at tok_start = n: the ring
+ * holds the unfinished block's keys from when they were new, as long as
+ * ring_slots >= m - n + 3.  (Past that, and so after any cut of a ring of 4 that
+ * overwrote one of them, the block's key is made of tokens that were cut off.)
+ *   ring        [num_req][ring_slots][128] bf16.
+ *   ring_pos    [num_req][ring_slots / 4][3] int32.
+ *   ring_slots  a power of two, 4 .. BS_MAX_RING_SLOTS (anything else:
+ *               BS_ERR_ARG); 4 is idx_compress_store.
  */
 int idx_compress_store(const uint16_t* k_raw, int32_t num_tok, const int32_t* req_tok_ptr,
                        const int32_t* tok_start, const int32_t* mrope_pos, int32_t num_req, int32_t max_tok,
@@ -414,6 +428,12 @@ int idx_compress_store(const uint16_t* k_raw, int32_t num_tok, const int32_t* re
                        uint16_t* ring, int32_t* ring_pos,
                        const int32_t* page_table, int32_t pt_stride, uint16_t* kcache, int64_t num_pages,
                        void* stream);
+int idx_compress_store_ring(const uint16_t* k_raw, int32_t num_tok, const int32_t* req_tok_ptr,
+                            const int32_t* tok_start, const int32_t* mrope_pos, int32_t num_req, int32_t max_tok,
+                            int32_t rotary_dim, int32_t sec_t, int32_t sec_h, int32_t sec_w, double theta,
+                            uint16_t* ring, int32_t* ring_pos, int32_t ring_slots,
+                            const int32_t* page_table, int32_t pt_stride, uint16_t* kcache, int64_t num_pages,
+                            void* stream);
 
 /*
  * Element types and cache forms of the calls below.
@@ -538,6 +558,7 @@ int kv8_load(const uint8_t* codes, const float* scales, int64_t num_pages, const
  * rounded to FP32 and to bf16, is quantised.  Norm and rotation run in FP64: each
  * element is within 2^-30 of the exact value of these steps (positions below 2^20)
  * before it is rounded.  Same arguments with codes and scales in place of kcache.
+ * idx4_compress_store_ring: the same of idx_compress_store_ring.
  *
  * idx4_score - idx_score_decode and idx_score_prefill over the 4-bit keys, any
  * number of rows a request: the same arguments, layouts, outputs, preconditions
@@ -566,6 +587,11 @@ int idx4_compress_store(const uint16_t* k_raw, int32_t num_tok, const int32_t* r
                         int32_t rotary_dim, int32_t sec_t, int32_t sec_h, int32_t sec_w, double theta,
                         uint16_t* ring, int32_t* ring_pos, const int32_t* page_table, int32_t pt_stride,
                         uint8_t* codes, uint8_t* scales, int64_t num_pages, void* stream);
+int idx4_compress_store_ring(const uint16_t* k_raw, int32_t num_tok, const int32_t* req_tok_ptr,
+                             const int32_t* tok_start, const int32_t* mrope_pos, int32_t num_req, int32_t max_tok,
+                             int32_t rotary_dim, int32_t sec_t, int32_t sec_h, int32_t sec_w, double theta,
+                             uint16_t* ring, int32_t* ring_pos, int32_t ring_slots, const int32_t* page_table,
+                             int32_t pt_stride, uint8_t* codes, uint8_t* scales, int64_t num_pages, void* stream);
 int idx4_score(const uint16_t* q, const uint8_t* codes, const uint8_t* scales, int64_t num_pages,
                const int32_t* page_table, int32_t pt_stride, const int32_t* req_row_ptr, int32_t num_req,
                const int32_t* row_pos, int32_t num_rows, int32_t c, int32_t max_vis,
@@ -608,9 +634,9 @@ int idx4_score(const uint16_t* q, const uint8_t* codes, const uint8_t* scales, i
  * below 0 or more than kv_len: no token goes) and puts its pages past
  * ceil(tokens / 64) at the ring's end, requests in order, their table entries
  * becoming -1.
- * (The ring of raw index keys that idx_compress_store keeps is another: where a cut
- * goes back behind the block that was unfinished, its slots are the caller's to
- * set back.)
+ * (The ring of raw index keys that the key compression keeps is another, and is not
+ * touched: a cut that does not end on a multiple of 4 tokens needs one of more
+ * than 4 slots, see idx_compress_store_ring.)
  *
  * Calls on the same state must not overlap in time.  Both return BS_OK,
  * BS_ERR_NULL, BS_ERR_ARG (negative counts, pt_stride < 1, ring_size outside 1
