@@ -152,6 +152,14 @@ __device__ __forceinline__ int lane_id() { return __lane_id(); }
 // caller's bound max_vis and at 0 for an invalid position.
 __device__ __forceinline__ int visible_blocks(int t, int c, int max_vis) { return max(0, min((t + 1) / c, max_vis)); }
 
+// Rows behind the last request's (the padding of a batch of a fixed number of rows)
+// see no block: the lengths that an earlier, fuller step left would have the
+// selection go through its scores.  Lane `first` of `lanes` takes every lanes-th.
+__device__ __forceinline__ void clear_padding(int32_t* row_len, const int32_t* req_row_ptr, int num_req, int num_rows,
+                                              int64_t first, int64_t lanes) {
+  for (int64_t r = max(req_row_ptr[num_req], 0) + first; r < num_rows; r += lanes) row_len[r] = 0;
+}
+
 // Reads FP32 entries of one row through a raw buffer resource: one lane
 // offset per load (no 64-bit address registers), and the hardware range check
 // returns 0 for entries at or past n, so reads past the row never fault.

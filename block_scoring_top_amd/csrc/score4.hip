@@ -220,7 +220,11 @@ __global__ __launch_bounds__(64 * kScoreWaves) void score4_decode_kernel(const S
   const int my_page = page_at(a, a.page_table + (int64_t)b * a.pt_stride, key0 / PAGE_KEYS + min(lane, TILES * C - 1));
   const int row = lane < r1 - r0 ? visible_blocks(a.row_pos[r0 + lane], C, a.max_vis) : 0;
   static_assert(kRowsOnce <= 64, "a lane a row");
-  if (blockIdx.x == 0 && wave == 0 && a.row_len != nullptr && lane < r1 - r0) a.row_len[r0 + lane] = row;
+  if (blockIdx.x == 0 && a.row_len != nullptr) {
+    if (wave == 0 && lane < r1 - r0) a.row_len[r0 + lane] = row;
+    if ((int)blockIdx.y >= a.more)
+      clear_padding(a.row_len, a.req_row_ptr, a.num_req, a.num_rows, (int64_t)b * blockDim.x + tid, (int64_t)a.num_req * blockDim.x);
+  }
   const int most = wave_most(row);
   if (block0 >= most) return;
 
@@ -282,6 +286,9 @@ __global__ __launch_bounds__(64 * kScoreWaves, 3) void score4_prefill_kernel(con
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t k0 = (int64_t)blockIdx.x * (STAGES * KEYS);
+  if (blockIdx.x == 0 && a.row_len != nullptr)
+    clear_padding(a.row_len, a.req_row_ptr, a.num_req, a.num_rows, (int64_t)blockIdx.y * blockDim.x + tid,
+                  (int64_t)gridDim.y * blockDim.x);
   const uint32_t blocks = a.num_rows / ROWS + a.num_req;  // at least as many as there are
   int b, first, end;
   for (uint32_t block = blockIdx.y; block < blocks && locate_rows<ROWS, 0>(a, block, lane, b, first, end); block += gridDim.y) {

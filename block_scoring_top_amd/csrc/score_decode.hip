@@ -74,7 +74,7 @@ template <int RG, int U>
 __global__ __launch_bounds__(256) void score_decode_kernel(
     const uint16_t* __restrict__ q, const uint16_t* __restrict__ kcache, int64_t num_pages,
     const int32_t* __restrict__ page_table, int32_t pt_stride,
-    const int32_t* __restrict__ req_row_ptr, const int32_t* __restrict__ row_pos,
+    const int32_t* __restrict__ req_row_ptr, const int32_t* __restrict__ row_pos, int32_t num_rows,
     int32_t c, int32_t max_vis, int32_t chunk,
     float* __restrict__ scores, int64_t ld, int32_t* __restrict__ row_len) {
   const int b = blockIdx.y;
@@ -84,8 +84,10 @@ __global__ __launch_bounds__(256) void score_decode_kernel(
 
   int nmax = 0;
   for (int r = r0; r < r1; ++r) nmax = max(nmax, visible_blocks(row_pos[r], c, max_vis));
-  if (blockIdx.x == 0 && row_len != nullptr)
+  if (blockIdx.x == 0 && row_len != nullptr) {
     for (int r = r0 + tid; r < r1; r += blockDim.x) row_len[r] = visible_blocks(row_pos[r], c, max_vis);
+    clear_padding(row_len, req_row_ptr, gridDim.y, num_rows, (int64_t)b * blockDim.x + tid, (int64_t)gridDim.y * blockDim.x);
+  }
 
   const int j0 = blockIdx.x * chunk;
   if (j0 >= nmax) return;
@@ -170,7 +172,7 @@ template <int NMS, int NW, int KSUB>
 __global__ __launch_bounds__(64 * NW) void score_rows_mfma_kernel(
     const uint16_t* __restrict__ q, const uint16_t* __restrict__ kcache, int64_t num_pages,
     const int32_t* __restrict__ page_table, int32_t pt_stride,
-    const int32_t* __restrict__ req_row_ptr, const int32_t* __restrict__ row_pos,
+    const int32_t* __restrict__ req_row_ptr, const int32_t* __restrict__ row_pos, int32_t num_rows,
     int32_t c, int32_t max_vis, int32_t chunk, int32_t fold,
     float* __restrict__ scores, int64_t ld, int32_t* __restrict__ row_len) {
   // Per wave KSUB subtiles of 16 keys (4 KiB each), key n of a subtile at
@@ -183,8 +185,10 @@ __global__ __launch_bounds__(64 * NW) void score_rows_mfma_kernel(
   const int g = lane >> 4, i16 = lane & 15;
   const int r0 = req_row_ptr[b];
   const int r1 = req_row_ptr[b + 1];
-  if (blockIdx.x == 0 && row_len != nullptr)
+  if (blockIdx.x == 0 && row_len != nullptr) {
     for (int r = r0 + tid; r < r1; r += blockDim.x) row_len[r] = visible_blocks(row_pos[r], c, max_vis);
+    clear_padding(row_len, req_row_ptr, gridDim.y, num_rows, (int64_t)b * blockDim.x + tid, (int64_t)gridDim.y * blockDim.x);
+  }
 
   // The request's longest visible range bounds the chunk.
   int nmax = 0;
@@ -323,21 +327,21 @@ int launch_score_decode(const uint16_t* q, const uint16_t* kcache, int64_t num_p
     dim3 gm(nch, num_req);
     if (avg <= 4)
       hipLaunchKernelGGL((score_rows_mfma_kernel<1, W, P>), gm, dim3(64 * W), 0, stream, q, kcache, num_pages, page_table,
-                         pt_stride, req_row_ptr, row_pos, c, max_vis, kChunkM, kFold, scores, ld, row_len);
+                         pt_stride, req_row_ptr, row_pos, num_rows, c, max_vis, kChunkM, kFold, scores, ld, row_len);
     else if (avg <= 8)
       hipLaunchKernelGGL((score_rows_mfma_kernel<2, W, P>), gm, dim3(64 * W), 0, stream, q, kcache, num_pages, page_table,
-                         pt_stride, req_row_ptr, row_pos, c, max_vis, kChunkM, kFold, scores, ld, row_len);
+                         pt_stride, req_row_ptr, row_pos, num_rows, c, max_vis, kChunkM, kFold, scores, ld, row_len);
     else
       hipLaunchKernelGGL((score_rows_mfma_kernel<4, W, P>), gm, dim3(64 * W), 0, stream, q, kcache, num_pages, page_table,
-                         pt_stride, req_row_ptr, row_pos, c, max_vis, kChunkM, kFold, scores, ld, row_len);
+                         pt_stride, req_row_ptr, row_pos, num_rows, c, max_vis, kChunkM, kFold, scores, ld, row_len);
     return hipGetLastError() == hipSuccess ? BS_OK : BS_ERR_LAUNCH;
   }
   if (avg <= 1)
     hipLaunchKernelGGL((score_decode_kernel<1, U>), grid, block, 0, stream, q, kcache, num_pages, page_table,
-                       pt_stride, req_row_ptr, row_pos, c, max_vis, (int32_t)chunk, scores, ld, row_len);
+                       pt_stride, req_row_ptr, row_pos, num_rows, c, max_vis, (int32_t)chunk, scores, ld, row_len);
   else
     hipLaunchKernelGGL((score_decode_kernel<2, U>), grid, block, 0, stream, q, kcache, num_pages, page_table,
-                       pt_stride, req_row_ptr, row_pos, c, max_vis, (int32_t)chunk, scores, ld, row_len);
+                       pt_stride, req_row_ptr, row_pos, num_rows, c, max_vis, (int32_t)chunk, scores, ld, row_len);
   return hipGetLastError() == hipSuccess ? BS_OK : BS_ERR_LAUNCH;
 }
 

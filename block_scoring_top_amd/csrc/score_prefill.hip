@@ -90,9 +90,11 @@ __global__ __launch_bounds__(256, 2) void score_prefill_kernel(
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, i16 = lane & 15;
 
-  if (row_len != nullptr)
+  if (row_len != nullptr) {
+    const int end = req_row_ptr[num_req];  // rows from there on are padding
     for (int64_t r = (int64_t)blockIdx.x * 256 + tid; r < num_rows; r += (int64_t)gridDim.x * 256)
-      row_len[r] = visible_blocks(row_pos[r], c, max_vis);
+      row_len[r] = r < end ? visible_blocks(row_pos[r], c, max_vis) : 0;
+  }
 
   // This workgroup's contiguous range of units.
   const int64_t u0 = units * blockIdx.x / gridDim.x;

@@ -84,7 +84,7 @@ class IndexerPath:
         ld = max(int(inp.max_vis), 1)
         ld = (ld + 3) // 4 * 4  # 16-byte aligned rows
         self.scores = torch.empty((R, ld), dtype=torch.float32, device=dev)
-        self.row_len = torch.zeros(R, dtype=torch.int32, device=dev)  # padding rows: no scorer writes it
+        self.row_len = torch.empty(R, dtype=torch.int32, device=dev)
         self.sel = torch.empty((R, inp.k), dtype=torch.int32, device=dev)
         self.sel_count = torch.empty(R, dtype=torch.int32, device=dev)
         ld_out = inp.k * inp.c + inp.c - 1

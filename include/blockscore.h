@@ -122,7 +122,9 @@ enum bs_status {
  *              kernels never score past it.  Requires max_vis <= ld_scores and
  *              c*max_vis <= 64*pt_stride.
  *   row_len    optional output [num_rows] int32: min(n_vis(r), max_vis), the
- *              length topk_select_rows takes.  May be NULL.
+ *              length topk_select_rows takes; 0 for rows from
+ *              req_row_ptr[num_req] on (padding: pages_extend), whose scores are
+ *              not written.  May be NULL.
  * Device preconditions: row_pos[r] >= 0; page ids valid; rows of a request
  * contiguous as given by req_row_ptr.
  * Returns BS_OK, BS_ERR_NULL (q, kcache, page_table, req_row_ptr, row_pos or
@@ -622,9 +624,9 @@ int idx4_score(const uint16_t* q, const uint8_t* codes, const uint8_t* scales, i
  *   slots       [num_rows]: each new token's slot, table entry * 64 + position
  *               mod 64, for the calls that store.
  * Rows behind the last new token get row_pos and slot -1 (a captured call is of a
- * fixed num_rows).  The stores skip them; the scorers and attn_window leave what
- * they have of them as it was, row_len too (fill it with zeros once); slot lists
- * of them hold nothing but -1.  When the ring has too few pages, the last
+ * fixed num_rows).  The stores skip them; the scorers write a row_len of 0 for them,
+ * so that nothing of them is selected, and no scores; their slot lists hold nothing
+ * but -1; attn_window leaves what it has of them as it was.  When the ring has too few pages, the last
  * requests' tokens have no page: slot -1 and their table entries as they were;
  * held_out counts the pages there are, and pool_out[2] is how many are lacking.
  * Such tokens are in kv_len_out all the same: cut them off with pages_release, or
