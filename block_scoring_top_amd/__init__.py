@@ -692,7 +692,8 @@ def idx4_score(q, cache: Idx4Cache, page_table, req_row_ptr, row_pos, max_vis, s
 class PagePool:
     """The free pages of a cache: ``ring`` int32 [size], their ids, and
     ``state`` int32 [4], head, count, what the last ``pages_extend`` lacked, 0
-    (``pages_extend`` in blockscore.h)."""
+    (``pages_extend`` in blockscore.h; a state made by hand needs the 0, one that is
+    only written, a ``pool_out``, may hold anything)."""
 
     def __init__(self, ring: torch.Tensor, state: torch.Tensor):
         if ring.dim() != 1 or state.shape != (4,):

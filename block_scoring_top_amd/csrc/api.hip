@@ -445,7 +445,7 @@ BS_EXPORT int pages_extend(const int32_t* kv_len, const int32_t* held, const int
   if (num_rows < 0) return BS_ERR_ARG;
   if (!req_row_ptr || (num_rows > 0 && (!row_pos || !slots))) return BS_ERR_NULL;
   return bs::launch_pages({kv_len, held, new_len, num_req, page_table, pt_stride, ring, ring_size, pool, kv_len_out,
-                           held_out, pool_out, req_row_ptr, tok_start, row_pos, slots, num_rows},
+                           held_out, pool_out, req_row_ptr, tok_start, row_pos, slots, num_rows, pool_out == pool},
                           false, static_cast<hipStream_t>(stream));
 }
 
@@ -457,7 +457,7 @@ BS_EXPORT int pages_release(const int32_t* kv_len, const int32_t* held, const in
                                   kv_len_out, held_out, pool_out);
   if (st != BS_OK) return st;
   return bs::launch_pages({kv_len, held, keep_len, num_req, page_table, pt_stride, ring, ring_size, pool, kv_len_out,
-                           held_out, pool_out, nullptr, nullptr, nullptr, nullptr, 0},
+                           held_out, pool_out, nullptr, nullptr, nullptr, nullptr, 0, pool_out == pool},
                           true, static_cast<hipStream_t>(stream));
 }
 

@@ -90,6 +90,7 @@ struct PagesCall {
   int32_t *kv_len_out, *held_out, *pool_out;
   int32_t *req_row_ptr, *tok_start, *row_pos, *slots;  // extend; tok_start may be null
   int32_t num_rows;
+  bool in_place;  // pool_out is pool
 };
 int launch_pages(const PagesCall& a, bool release, hipStream_t stream);
 

@@ -8,8 +8,9 @@
 // kilobytes move, so what bounds them is latency: the launch, the lengths'
 // load, the scans, a search, a load of the page id, the store.  Hence one
 // launch: every workgroup scans all requests by itself (they fit in LDS) and
-// writes its share of the rows and pages; the lengths, which a caller may have
-// updated in place, are written by the last workgroup to have read them.
+// writes its share of the rows and pages.  The lengths, where a caller has them
+// updated in place, are written by the last workgroup to have read them, which a
+// counter in the pool's state tells; into buffers of their own the first one writes.
 #include <algorithm>
 #include <type_traits>
 
@@ -94,7 +95,8 @@ __global__ __launch_bounds__(THREADS) void pages_kernel(const PagesCall a) {
     if (!RELEASE && blockIdx.x == 0) a.req_row_ptr[0] = 0;
   }
   uint32_t rows = 0, pages = 0;  // of the requests so far
-  bool last = gridDim.x == 1;
+  bool last = gridDim.x == 1 || (!a.in_place && blockIdx.x == 0);  // this workgroup writes the lengths
+  const bool counts = gridDim.x > 1 && a.in_place;
   for (int b0 = 0; b0 < a.num_req; b0 += BATCH) {  // one turn, unless one workgroup does everything
     const int nb = min(BATCH, a.num_req - b0);
     for (int i = tid; i < nb; i += THREADS) {
@@ -105,7 +107,7 @@ __global__ __launch_bounds__(THREADS) void pages_kernel(const PagesCall a) {
     }
     __syncthreads();
     const uint32_t head = sh.head, count = sh.count;
-    if (gridDim.x > 1 && tid == 0)
+    if (counts && tid == 0)
       sh.arrived = __hip_atomic_fetch_add(reinterpret_cast<uint32_t*>(a.pool_out + 3), 1u, __ATOMIC_RELAXED,
                                           __HIP_MEMORY_SCOPE_AGENT);
     for (int c0 = 0; c0 < nb; c0 += THREADS) {
@@ -176,7 +178,7 @@ __global__ __launch_bounds__(THREADS) void pages_kernel(const PagesCall a) {
     // Everything that this workgroup reads of the caller's lengths has been
     // read; the last one to say so may write them.
     __syncthreads();
-    if (gridDim.x > 1) last = sh.arrived == gridDim.x - 1;
+    if (counts) last = sh.arrived == gridDim.x - 1;
     if (last)
       for (int i = tid; i < nb; i += THREADS) a.kv_len_out[b0 + i] = sh.len[i], a.held_out[b0 + i] = sh.held[i];
     __syncthreads();
@@ -197,6 +199,18 @@ __global__ __launch_bounds__(THREADS) void pages_kernel(const PagesCall a) {
   }
 }
 
+// Whether several workgroups can take a call: its state is updated in place, with the
+// counter that the state has, or no workgroup reads what another writes.
+static bool can_share(const PagesCall& a) {
+  if (a.in_place) return true;
+  const int64_t n = a.num_req;
+  auto meet = [](const int32_t* x, int64_t nx, const int32_t* y, int64_t ny) { return x < y + ny && y < x + nx; };
+  auto read = [&](const int32_t* x, int64_t nx) {
+    return meet(x, nx, a.kv_len, n) || meet(x, nx, a.held, n) || meet(x, nx, a.change, n) || meet(x, nx, a.pool, 4);
+  };
+  return !read(a.kv_len_out, n) && !read(a.held_out, n) && !read(a.pool_out, 4);
+}
+
 // There is a workgroup for every kItems rows (extend) or 16 times as many page
 // table entries (release: few of them are given back).  us, both calls of 1,003
 // requests with 56,000 new tokens, kItems 512 / 1,024 / 2,048: 12.2 / 11.0 / 12.7.
@@ -207,7 +221,7 @@ int launch_pages(const PagesCall& a, bool release, hipStream_t stream) {
   auto go = [&](auto rel, auto threads, auto batch) {
     constexpr int THREADS = decltype(threads)::value, BATCH = decltype(batch)::value;
     const int64_t items = release ? (int64_t)a.num_req * a.pt_stride / 16 : a.num_rows;
-    const bool once = a.num_req > 0 && a.num_req <= BATCH;  // else one workgroup does everything, in turns
+    const bool once = a.num_req > 0 && a.num_req <= BATCH && can_share(a);  // else one workgroup does everything, in turns
     const uint32_t grid = once ? (uint32_t)std::min<int64_t>(128, std::max<int64_t>(1, items / kItems)) : 1;
     hipLaunchKernelGGL((pages_kernel<decltype(rel)::value, THREADS, BATCH>), dim3(grid), dim3(THREADS), 0, stream, a);
   };

@@ -608,10 +608,11 @@ int idx4_score(const uint16_t* q, const uint8_t* codes, const uint8_t* scales, i
  *   ring       [ring_size] int32: the ids of free pages, as a ring: `count` of
  *              them from index `head` on, wrapping at ring_size.  ring_size is at
  *              least the number of pages there are.
- *   pool       [4] int32: head, count, pages that the last extend lacked, 0.
+ *   pool       [4] int32: head, count, pages that the last extend lacked, 0 (a
+ *              call that updates the state in place counts there, and leaves 0).
  * kv_len_out, held_out and pool_out receive the state after the call and may be
- * kv_len, held and pool themselves; pool_out[3] must be 0 before the call, and
- * is 0 after it.
+ * kv_len, held and pool themselves, or buffers of their own, whatever these hold
+ * (all three of one kind: mixed, one workgroup does everything).
  *
  * pages_extend - appends new_len[b] tokens to request b (below 0 counts as 0; no
  * more than its table holds, 64 * pt_stride in all, and in the order of the
