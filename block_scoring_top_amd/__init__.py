@@ -464,7 +464,11 @@ class KV4Cache:
 class KV8Cache:
     """An 8-bit KV cache (layout: ``kv8_store`` in blockscore.h): ``codes``
     uint8 (or float8_e4m3fn) [slots, kv_heads, 2, head_dim] and ``scales``
-    float32 [slots / 64, kv_heads, 2], contiguous, ``slots`` a multiple of 64."""
+    float32 [slots / 64, kv_heads, 2], contiguous, ``slots`` a multiple of 64.
+
+    Its rows share a page's scale, so ``kv8_store`` asks more of its caller than
+    ``kv4_store``: the rows of one page lie within 64 consecutive rows of a call, and
+    a page's first slot is written before its others."""
 
     form = 8  # BS_KV_8
 
@@ -559,7 +563,11 @@ def kv4_store(k, v, slots, cache: KV4Cache, stream=None):
 
 
 def kv8_store(k, v, slots, cache: KV8Cache, stream=None):
-    """Quantise new K/V rows into the 8-bit cache.  See ``kv8_store`` in blockscore.h."""
+    """Quantise new K/V rows into the 8-bit cache.  The rows of one page (64 slots)
+    must lie within 64 consecutive rows of the call, as ``pages_extend`` lists them:
+    tokens ordered by step and then by request, say, are not written whole, which
+    ``kv4_store`` would do.  A row for a page's first slot begins the page anew.  See
+    ``kv8_store`` in blockscore.h."""
     PreparedCall("kv8_store", _kv_store_args(k, v, slots, cache, KV8Cache), cache.device, once=True)(stream)
 
 

@@ -518,7 +518,8 @@ int kv4_load(const uint8_t* codes, const uint8_t* scales, int64_t num_pages, con
  *   k, v, dtype, ld_k, ld_v, head_dim: as kv4_store.
  * Device preconditions: the slots of one call are distinct, and those of one
  * page lie within 64 consecutive rows (in any order, with other rows between), as
- * pages_extend lists them; otherwise what the page holds is unspecified.  Since a
+ * pages_extend lists them (kv4_store takes any order); otherwise what the page
+ * holds is unspecified, and some of its rows may not be written.  Since a
  * page begins anew with its first slot, a call that writes that one comes before
  * the calls that write the page's others; those may come in any order.
  *
@@ -612,7 +613,7 @@ int idx4_score(const uint16_t* q, const uint8_t* codes, const uint8_t* scales, i
  *              call that updates the state in place counts there, and leaves 0).
  * kv_len_out, held_out and pool_out receive the state after the call and may be
  * kv_len, held and pool themselves, or buffers of their own, whatever these hold
- * (all three of one kind: mixed, one workgroup does everything).
+ * (with a pool_out of its own and lengths in place, one workgroup does everything).
  *
  * pages_extend - appends new_len[b] tokens to request b (below 0 counts as 0; no
  * more than its table holds, 64 * pt_stride in all, and in the order of the
@@ -631,7 +632,9 @@ int idx4_score(const uint16_t* q, const uint8_t* codes, const uint8_t* scales, i
  * requests' tokens have no page: slot -1 and their table entries as they were;
  * held_out counts the pages there are, and pool_out[2] is how many are lacking.
  * Such tokens are in kv_len_out all the same: cut them off with pages_release, or
- * the pages that a later call finds for them will hold what they held before.
+ * the pages that a later call finds for them will hold what they held before; in
+ * an 8-bit cache with the scale that they had, to which that page's later tokens are
+ * rounded too.
  *
  * pages_release - cuts request b back to keep_len[b] tokens (0: it is finished;
  * below 0 or more than kv_len: no token goes) and puts its pages past
