@@ -43,10 +43,14 @@ constexpr int64_t kPartialBytes = (int64_t)BS_ATTN_WORKSPACE_BYTES - kCounterByt
 // The 8-bit cache: 16 query / 2 kv heads, gathered and not, D = 128: 100 rows, window
 // 1,200 (60,000 tiles times keys) 16 and 19 us, 300, 1,000 (150,000) 21 and 22, 700,
 // 1,000 (350,000) 41 and 27; 36 x 6 rows, window 700 18 and 22, 64 x 6, window 4,000
-// 65 and 60.  D = 64: 1,000 rows, window 1,000 (500,000) 18 and 24.  D = 256, where
-// its codes take the other's registers only for a page at a time: 100 rows, window
-// 1,000 (100,000) 23 and 37, 300, 2,000 (600,000) 74 and 54, 2,000 rows 292 and 159; 64 x
-// 6 rows, window 4,000 140 and 324.
+// 65 and 60.  D = 64: 1,000 rows, window 1,000 (500,000) 19 and 23, but 2,000, 500 (the
+// same number) 23 and 16.  D = 256, where its codes take the other's registers only
+// for a page at a time: 100 rows, window 1,000 (100,000) 23 and 36, 300, 1,000 (300,000) 43
+// and 49, 700, 500 (350,000) 41 and 51, 200, 2,000 (400,000) 39 and 49, 300, 1,500 (450,000)
+// 60 and 53, 300, 2,000 (600,000) 74 and 54, 2,000 rows 293 and 151; 64 x 6 rows, window
+// 4,000 140 and 324.  Over 42 such calls (60 to 2,000 rows, windows of 500 to 2,000) the
+// kernel chosen is 3% slower than the better one; at most 25% at D = 256, 10% at 128,
+// 42% at 64.
 bool gathers(const AttnCall& c, int64_t tiles, int64_t keys, int64_t pairs, int64_t num_req) {
   const bool kv4 = c.form == BS_KV_4, kv8 = c.form == BS_KV_8;
   if (pairs <= 16 || (kv4 && c.d == 256)) return true;
@@ -123,11 +127,15 @@ void split_heads(GatherArgs& a, int nt) {
 // sweeps of 1 to 128 parts (1 to 240 groups of 250 to 64,000 keys, both caches, all
 // head dims) the number chosen is 1.6% slower than the best one; as many as 512
 // workgroups and 256 keys a part allow, 11%: 1 row of 256 slots 5.5 and 8.0 us, 30
-// requests x 2 rows x 8 heads of D = 256 over 4,096 keys 24 and 42.
+// requests x 2 rows x 8 heads of D = 256 over 4,096 keys 24 and 42.  Those were the
+// 16-bit pools and the 4-bit cache; the 8-bit one has the latter's constants, with
+// which its number is 3.9, 1.0 and 2.1% slower than the best at D = 64, 128 and 256
+// (38 calls each: 1 to 120 rows of 256 to 32,768 slots, 2 and 8 kv heads; at most
+// 17, 10 and 20%).
 int gather_splits(const AttnCall& c, int nt, int cols, int64_t groups, int64_t keys, int64_t most) {
-  const bool kv4 = c.form != BS_KV_16;
-  const double chunk = 0.6 + 0.7 * nt * c.d / 128 + (kv4 || c.d == 64 ? 0. : c.d == 256 ? 3. : 1.1);
-  const double read = groups * keys * c.d * (c.form == BS_KV_4 ? 17. / 16 : kv4 ? 2. : 4.) / 4.5e6;
+  const bool codes = c.form != BS_KV_16;
+  const double chunk = 0.6 + 0.7 * nt * c.d / 128 + (codes || c.d == 64 ? 0. : c.d == 256 ? 3. : 1.1);
+  const double read = groups * keys * c.d * (c.form == BS_KV_4 ? 17. / 16 : codes ? 2. : 4.) / 4.5e6;
   const double part = cols * (c.d + 4) * 4e-6 * groups, rounds = cols * c.d / 16384.;
   int64_t best = 1;
   double least = 0;
