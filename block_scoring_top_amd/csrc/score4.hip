@@ -14,9 +14,12 @@
 // rows, their 4 heads on adjacent rows, so a lane's 4 accumulators are the heads
 // of one (query row, key) pair: ReLU, head sum and scale stay in the lane.
 //
-// Few rows a request (decode, verify): a stream of 68 bytes a key, bound by HBM.
-// A wave takes TILES tiles of 64 keys, all of their loads in flight at once, and
-// runs the request's rows over them.  Many rows (prefill): 1,024 flop and 4
+// Few rows a request (decode, verify): a stream of 68 bytes a key, bound by the
+// latency of memory (16 rows x 81,920 keys, 94 MB: 18.1 us out of the Infinity Cache,
+// 23.4 from HBM, 2 to 3 of them the timing's own).  A wave takes TILES tiles of 64
+// keys, all of their loads in flight at once, and runs the request's rows over them.
+// The grid is of max_vis keys for every request: 64 x 6 rows over 586,000 keys 15.2
+// us, 22.2 with max_vis four times the longest request.  Many rows (prefill): 1,024 flop and 4
 // bytes written a (row, key) pair, bound by the writes.  A workgroup copies a
 // chunk of keys into LDS, each of its waves holds its own rows' operands, and
 // the chunk is gone through without waiting for anything but LDS.
@@ -158,7 +161,7 @@ __device__ __forceinline__ int wave_most(int x) {
 
 // The scores of 4 rows with TILES tiles of keys from `key` on: lane l has those of row l/16 (which sees vis keys) with
 // keys 4n .. 4n + 3 of each tile, n = l mod 16, and stores them at dst.  e, byte j: the exponents of k[..][j].
-// Non-temporal: the selection reads the scores after the whole launch (8,192 rows: 112 us, 160 with cached stores).
+// Non-temporal: the selection reads the scores after the whole launch (8,192 rows: 96 us, 118 with cached stores).
 template <int TILES>
 __device__ __forceinline__ void store_scores(const Query& q, const u32x4_t (&k)[TILES][4], const uint32_t (&e)[TILES], float* dst,
                                              int vis, int key, int n) {
@@ -187,7 +190,7 @@ __device__ __forceinline__ void store_scores(const Query& q, const u32x4_t (&k)[
 }  // namespace
 
 // Rows of a block in the kernel for few rows: one block is of the first rows of each request, others of the rest of
-// those that have more (63 requests of one row beside one of 1,000, 30,000 tokens each, c = 4: 22 us, 172 with a
+// those that have more (63 requests of one row beside one of 1,000, 30,000 tokens each, c = 4: 20 to 22 us, 172 with a
 // request's rows in one block).
 constexpr int kRowsOnce = 64;
 
@@ -362,14 +365,16 @@ namespace {
 
 // The kernel for few rows goes through up to 64 rows of a request in each workgroup,
 // the other is at its best with many; over 575 calls (1 to 256 requests of 6 to
-// 8,192 rows, 1,000 to 65,536 tokens, c = 1 and 4) this rule costs 2% more than the
-// best of the three.  us, few rows / many with one stage / with four: 64 requests of
-// 8,000 tokens (c = 4) with 12 rows 5.8 / 6.8 / 11.5, 20 7.6 / 7.7 / 12.0, 32 9.2 /
-// 8.7 / 11.6; 16 of 65,536 (c = 1) with 16 rows 24.6 / 31.4 / 28.6.
+// 8,192 rows, 1,000 to 65,536 tokens, c = 1 and 4) this rule costs 1.5% more than the
+// best of the three (at most 27%: 16 requests of 8,000 with 256 rows 15.4 for 12.1).
+// us, few rows / many with one stage / with four: 64 requests of 8,000 tokens (c = 4)
+// with 12 rows 5.9 / 7.0 / 11.3, 20 7.5 / 7.7 / 12.0, 32 9.1 / 8.6 / 11.5; 16 of
+// 65,536 (c = 1) with 16 rows 25.1 / 31.1 / 28.0.  num_rows counts padding: 64
+// requests of 8,000 tokens with one row each 4.3 us, 10.9 in a call of 8,192 rows.
 constexpr int64_t kFewRows = 20;
 // Below so many workgroups of four stages: one stage each, four times as many.  1
 // request of 65,536 tokens (c = 4) with 64 rows (48 workgroups) 6.5 us with one
-// stage, 10.7 with four, 512 (272) 13.4 and 12.6, 2,000 (1,008) 36.0 and 32.7.
+// stage, 10.8 with four, 512 (272) 13.4 and 12.6, 2,000 (1,008) 36.3 and 33.2.
 constexpr int64_t kFewGroups = 320;
 // From so many keys in all on, two tiles a wave: 16 x 81,920 keys 18.1 us, 19.1 with
 // one, 19.1 with four.
