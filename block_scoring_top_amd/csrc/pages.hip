@@ -213,9 +213,9 @@ static bool can_share(const PagesCall& a) {
 
 // There is a workgroup for every kItems rows (extend) or 16 times as many page
 // table entries (release: few of them are given back).  us, both calls of 1,003
-// requests with 56,000 new tokens, kItems 512 / 1,024 / 2,048: 12.2 / 11.0 / 12.7.
+// requests with 56,000 new tokens, kItems 512 / 1,024 / 2,048: 10.6 / 10.6 / 12.5.
 // Up to 256 requests: workgroups of 256, whose barriers and scans are shorter
-// (64 requests x 6 rows: 7.7 us, 8.9 with 1,024; the host takes about as long).
+// (64 requests x 6 rows: 7.6 us, 8.8 with 1,024; 7.1 of them on the GPU).
 int launch_pages(const PagesCall& a, bool release, hipStream_t stream) {
   constexpr int64_t kItems = 1024;
   auto go = [&](auto rel, auto threads, auto batch) {
