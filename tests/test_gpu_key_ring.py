@@ -60,7 +60,7 @@ class Loop:
 def _steps(rng, B, draft, most_cut, n):
     """Per step: new tokens of each request, what is kept after it (-1: all), raw keys and positions; the tokens that each
     request has at the end, as indexes into them.  A cut goes back up to ``most_cut`` tokens from the longest that the
-    request has been, into the tokens of earlier steps too."""
+    request has been, into the tokens of earlier steps too; some requests finish, and others begin in their place."""
     tokens, high, out, total, cuts = [[] for _ in range(B)], np.zeros(B, int), [], 0, set()
     for i in range(n):
         new = rng.integers(1, draft + 1, B) if i else rng.integers(1, 90, B)
@@ -71,7 +71,9 @@ def _steps(rng, B, draft, most_cut, n):
             total += new[b]
             high[b] = max(high[b], len(tokens[b]))
             low = max(0, high[b] - most_cut)
-            if i and rng.random() < 0.7 and len(tokens[b]) > low:
+            if i and rng.random() < 0.04:
+                keep[b], tokens[b], high[b] = 0, [], 0
+            elif i and rng.random() < 0.7 and len(tokens[b]) > low:
                 keep[b] = rng.integers(low, len(tokens[b]))
                 cuts.add((len(tokens[b]) % 4, keep[b] % 4))
                 tokens[b] = tokens[b][:keep[b]]
